@@ -23,7 +23,8 @@ __all__ = ["DFlashError", "Model", "Cache", "lib", "dflash_model_create", "dflas
            "dflash_launch_count", "dflash_profile_start", "dflash_profile_stop", "dflash_inject_context_noalloc",
            "dflash_selftest_wait_timeout", "dflash_sampling_workspace", "dflash_verify_sampled", "dflash_sample_tokens",
            "BlockPolicy", "dflash_packed_attention_workspace", "dflash_packed_block_attention",
-           "dflash_packed_attention_status"]
+           "dflash_packed_attention_status", "dflash_token_logprobs", "dflash_token_logprobs_backward",
+           "dflash_clip_workspace", "dflash_clip_grad_norm"]
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
@@ -329,6 +330,136 @@ def dflash_packed_attention_status(workspace: torch.Tensor, stream=None) -> int:
     check(lib().dflash_packed_attention_status(_ptr(workspace), _stream_ptr(stream), ctypes.byref(st)),
           "dflash_packed_attention_status")
     return st.value
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    """(rows, vocab, elements between rows) of a [..., V] tensor whose rows are evenly spaced."""
+    if t.dim() == 0 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be a float32 or bfloat16 [..., V] tensor")
+    V = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // V if V else 0), V, V
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, V)
+        except RuntimeError:
+            raise ValueError(f"{name}: the rows must be evenly spaced") from None
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    return (1, V, V) if t.dim() == 1 else (t.shape[0], V, t.stride(0))
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.Tensor, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of n values on the device of `like` (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {like.device}")
+    return t.data_ptr()
+
+
+def _on_current_device(t: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+
+
+def dflash_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], temperature: float,
+                          logprob: Optional[torch.Tensor], entropy: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, top_ids: Optional[torch.Tensor] = None,
+                          top_logprobs: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Log probabilities of tokens int32 [...] under softmax(logits / T), logits
+    fp32 or bf16 [..., V] with evenly spaced rows -> logprob, entropy and lse
+    fp32 [...] and the likeliest tokens top_ids int32 / top_logprobs fp32
+    [..., k]; what is None is not computed (tokens and logprob go together)."""
+    _on_current_device(logits)
+    rows, V, stride = _rows_of(logits, "logits")
+    k = 0
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_logprobs is None or top_ids.dim() == 0:
+            raise ValueError("top_ids and top_logprobs [..., k] go together")
+        k = top_ids.shape[-1]
+    check(lib().dflash_token_logprobs(
+        logits.data_ptr(), _abi.DTYPE_F32 if logits.dtype == torch.float32 else _abi.DTYPE_BF16, stride,
+        _vector(tokens, rows, torch.int32, logits, "tokens"), rows, V, float(temperature), k,
+        _vector(logprob, rows, torch.float32, logits, "logprob"),
+        _vector(entropy, rows, torch.float32, logits, "entropy"), _vector(lse, rows, torch.float32, logits, "lse"),
+        _vector(top_ids, rows * k, torch.int32, logits, "top_ids"),
+        _vector(top_logprobs, rows * k, torch.float32, logits, "top_logprobs"), _stream_ptr(stream)),
+        "dflash_token_logprobs")
+
+
+def dflash_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.Tensor], temperature: float,
+                                   lse: torch.Tensor, d_logits: torch.Tensor,
+                                   d_logprob: Optional[torch.Tensor] = None, entropy: Optional[torch.Tensor] = None,
+                                   d_entropy: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of sum(d_logprob * logprob) + sum(d_entropy * entropy) with
+    respect to the logits, in their type, into d_logits [..., V] (which may be
+    the logits themselves); lse and entropy are dflash_token_logprobs'."""
+    _on_current_device(logits)
+    rows, V, stride = _rows_of(logits, "logits")
+    d_rows, d_V, d_stride = _rows_of(d_logits, "d_logits")
+    if d_rows != rows or d_V != V or d_logits.dtype != logits.dtype or d_logits.device != logits.device:
+        raise ValueError("d_logits must have the logits' rows, type and device")
+    check(lib().dflash_token_logprobs_backward(
+        logits.data_ptr(), _abi.DTYPE_F32 if logits.dtype == torch.float32 else _abi.DTYPE_BF16, stride,
+        _vector(tokens, rows, torch.int32, logits, "tokens"), rows, V, float(temperature),
+        _vector(lse, rows, torch.float32, logits, "lse"), _vector(entropy, rows, torch.float32, logits, "entropy"),
+        _vector(d_logprob, rows, torch.float32, logits, "d_logprob"),
+        _vector(d_entropy, rows, torch.float32, logits, "d_entropy"), d_logits.data_ptr(), d_stride,
+        _stream_ptr(stream)), "dflash_token_logprobs_backward")
+
+
+def _scratch(nbytes: int, stream=None) -> torch.Tensor:
+    """Device scratch of the caching allocator, ordered with the stream the call runs on."""
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def dflash_clip_workspace() -> torch.Tensor:
+    """Device scratch for dflash_clip_grad_norm (a few kilobytes, whatever the tensors)."""
+    n = int(lib().dflash_clip_workspace_bytes())
+    if n == 0:
+        raise ValueError("no current device")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def dflash_clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Global 2-norm of the contiguous fp32 / bf16 tensors `grads` into norm
+    fp32 [1], and grads scaled by max_norm / norm where it exceeds max_norm:
+    in place, or into the tensors `out` of the same types and sizes.  A norm
+    that is not finite leaves the gradients as they are; max_norm = inf
+    computes the norm alone."""
+    _on_current_device(norm)
+    n, dev = len(grads), norm.device
+    ptrs, dtypes, numels = [0] * n, [0] * n, [0] * n
+    outs = None if out is None else [0] * n
+    if out is not None and len(out) != n:
+        raise ValueError("out must have one tensor for each of grads")
+    for i, g in enumerate(grads):
+        dt = g.dtype
+        if dt is torch.bfloat16:
+            dtypes[i] = _abi.DTYPE_BF16
+        elif dt is not torch.float32:
+            raise ValueError("gradients must be float32 or bfloat16")
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous tensors on the norm's device")
+        ptrs[i] = g.data_ptr()
+        numels[i] = g.numel()
+        if outs is not None:
+            o = out[i]
+            if o.dtype is not dt or o.numel() != numels[i] or o.device != dev or not o.is_contiguous():
+                raise ValueError("out tensors must be contiguous, of the gradients' types and sizes")
+            outs[i] = o.data_ptr()
+    if workspace is None:
+        workspace = _scratch(int(lib().dflash_clip_workspace_bytes()), stream)
+    ptr_array = ctypes.c_void_p * n
+    check(lib().dflash_clip_grad_norm(
+        ptr_array(*ptrs), None if outs is None else ptr_array(*outs), (ctypes.c_int64 * n)(*numels),
+        (ctypes.c_int32 * n)(*dtypes), n, float(max_norm), _vector(norm, 1, torch.float32, norm, "norm"),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "dflash_clip_grad_norm")
 
 
 class BlockPolicy:

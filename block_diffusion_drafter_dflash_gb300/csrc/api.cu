@@ -5,6 +5,8 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <new>
+#include <utility>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -17,6 +19,8 @@
 #include "attn_tc.cuh"
 #include "persist.cuh"
 #include "sampling.cuh"
+#include "logprobs.cuh"
+#include "grad_clip.cuh"
 #include "packed_attention.cuh"
 
 using namespace dflash;
@@ -1353,6 +1357,154 @@ int32_t dflash_packed_attention_status(const void* workspace, dflash_stream_t st
   DF_CUDA(cudaMemcpyAsync(status_host, workspace, sizeof(int32_t), cudaMemcpyDeviceToHost, (cudaStream_t)stream),
           "status read");
   DF_CUDA(cudaStreamSynchronize((cudaStream_t)stream), "status sync");
+  return DFLASH_OK;
+}
+
+namespace {
+int32_t check_logprobs(int rows, int vocab, float temperature, int32_t dtype, int64_t row_stride, const void* logits) {
+  if (rows < 0) return fail(DFLASH_ERR_INVALID_ARG, "rows %d < 0", rows);
+  if (rows > 65535) return fail(DFLASH_ERR_SHAPE, "%d logits rows > 65535", rows);
+  if (vocab <= 0 || vocab > (1 << 24)) return fail(DFLASH_ERR_SHAPE, "vocab %d outside [1, 2^24]", vocab);
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return fail(DFLASH_ERR_INVALID_ARG, "temperature must be positive and finite, and so its reciprocal");
+  if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  if (rows > 1 && row_stride < vocab)
+    return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld < vocab %d", (long long)row_stride, vocab);
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == DFLASH_DTYPE_F32 ? 4 : 2))
+    return fail(DFLASH_ERR_INVALID_ARG, "logits are not aligned to their type");
+  return DFLASH_OK;
+}
+}  // namespace
+
+int32_t dflash_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* tokens,
+                              int32_t rows, int32_t vocab, float temperature, int32_t top_k, float* logprob,
+                              float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                              dflash_stream_t stream) {
+  int32_t rc = check_logprobs(rows, vocab, temperature, dtype, row_stride, logits);
+  if (rc) return rc;
+  if (top_k < 0 || top_k > kMaxTopK || top_k > vocab)
+    return fail(DFLASH_ERR_SHAPE, "top_k %d outside [0, min(%d, vocab)]", top_k, kMaxTopK);
+  if (rows == 0) return DFLASH_OK;
+  if (!logits || (top_k && (!top_ids || !top_logprobs))) return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (!tokens != !logprob) return fail(DFLASH_ERR_INVALID_ARG, "tokens and logprob go together: both or neither");
+  if (!logprob && !entropy && !lse && !top_k) return fail(DFLASH_ERR_INVALID_ARG, "no output is asked for");
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  LogprobArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.tokens = tokens;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.top_k = top_k;
+  a.temperature = temperature;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  DF_CUDA(token_logprobs_launch(a, dtype == DFLASH_DTYPE_BF16, sms, (cudaStream_t)stream), "token log probabilities");
+  g_launch_count += 1;
+  return DFLASH_OK;
+}
+
+int32_t dflash_token_logprobs_backward(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* tokens,
+                                       int32_t rows, int32_t vocab, float temperature, const float* lse,
+                                       const float* entropy, const float* d_logprob, const float* d_entropy,
+                                       void* d_logits, int64_t d_row_stride, dflash_stream_t stream) {
+  int32_t rc = check_logprobs(rows, vocab, temperature, dtype, row_stride, logits);
+  if (rc) return rc;
+  if (rows == 0) return DFLASH_OK;
+  if (!logits || !lse || !d_logits) return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (!d_logprob && !d_entropy) return fail(DFLASH_ERR_INVALID_ARG, "d_logprob or d_entropy is needed");
+  if (d_logprob && !tokens) return fail(DFLASH_ERR_INVALID_ARG, "d_logprob needs the tokens");
+  if (d_entropy && !entropy) return fail(DFLASH_ERR_INVALID_ARG, "d_entropy needs the entropy");
+  if (rows > 1 && d_row_stride < vocab)
+    return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld of the gradient < vocab %d", (long long)d_row_stride, vocab);
+  const size_t es = dtype == DFLASH_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(d_logits) % es) return fail(DFLASH_ERR_INVALID_ARG, "d_logits is not aligned to its type");
+  // the gradient may take the logits' place, element for element; any other overlap would be read after it is written
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(d_logits);
+  const uintptr_t x1 = x0 + ((size_t)(rows - 1) * (rows > 1 ? row_stride : 0) + vocab) * es;
+  const uintptr_t d1 = d0 + ((size_t)(rows - 1) * (rows > 1 ? d_row_stride : 0) + vocab) * es;
+  if (x0 < d1 && d0 < x1 && !(x0 == d0 && (rows == 1 || row_stride == d_row_stride)))
+    return fail(DFLASH_ERR_INVALID_ARG, "d_logits overlaps the logits without being the same rows");
+  LogprobGradArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.tokens = d_logprob ? tokens : nullptr;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.temperature = temperature;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.d_logprob = d_logprob;
+  a.d_entropy = d_entropy;
+  a.d_logits = d_logits;
+  a.d_row_stride = d_row_stride;
+  DF_CUDA(token_logprobs_backward_launch(a, dtype == DFLASH_DTYPE_BF16, (cudaStream_t)stream),
+          "token log probability gradient");
+  g_launch_count += 1;
+  return DFLASH_OK;
+}
+
+size_t dflash_clip_workspace_bytes(void) {
+  const int sms = current_sms();
+  return sms > 0 ? clip_workspace_bytes(sms) : 0;
+}
+
+int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_host, const int64_t* numel_host,
+                              const int32_t* dtype_host, int32_t n_tensors, float max_norm, float* norm_dev,
+                              void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  if (n_tensors < 0) return fail(DFLASH_ERR_INVALID_ARG, "n_tensors %d < 0", n_tensors);
+  if (n_tensors > 0 && (!grads_host || !numel_host || !dtype_host)) return fail(DFLASH_ERR_INVALID_ARG, "a host array is NULL");
+  if (!(max_norm >= 0.f)) return fail(DFLASH_ERR_INVALID_ARG, "max_norm must be at least 0 (infinity: the norm alone)");
+  if (!norm_dev || !workspace) return fail(DFLASH_ERR_INVALID_ARG, "norm_dev or workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 8) return fail(DFLASH_ERR_INVALID_ARG, "workspace must be 8-byte aligned");
+  try {
+    std::vector<ClipTensor> t(n_tensors);
+    std::vector<std::pair<uintptr_t, uintptr_t>> outs;   // byte ranges written
+    outs.reserve(n_tensors);
+    for (int i = 0; i < n_tensors; ++i) {
+      if (numel_host[i] < 0 || numel_host[i] > (int64_t(1) << 48))
+        return fail(DFLASH_ERR_SHAPE, "tensor %d has %lld elements", i, (long long)numel_host[i]);
+      if (dtype_host[i] != DFLASH_DTYPE_F32 && dtype_host[i] != DFLASH_DTYPE_BF16)
+        return fail(DFLASH_ERR_INVALID_ARG, "tensor %d: bad dtype %d", i, dtype_host[i]);
+      t[i].in = grads_host[i];
+      t[i].out = out_host ? out_host[i] : const_cast<void*>(grads_host[i]);
+      t[i].numel = numel_host[i];
+      t[i].bf16 = dtype_host[i] == DFLASH_DTYPE_BF16;
+      if (!t[i].numel) continue;
+      if (!t[i].in || !t[i].out) return fail(DFLASH_ERR_INVALID_ARG, "tensor %d is NULL", i);
+      const uintptr_t es = t[i].bf16 ? 2 : 4, o = reinterpret_cast<uintptr_t>(t[i].out);
+      if (reinterpret_cast<uintptr_t>(t[i].in) % es || o % es)
+        return fail(DFLASH_ERR_INVALID_ARG, "tensor %d is not aligned to its type", i);
+      outs.emplace_back(o, o + t[i].numel * es);
+    }
+    // what is written may be its own input, and nothing else that is read or written
+    std::sort(outs.begin(), outs.end());
+    for (size_t i = 1; i < outs.size(); ++i)
+      if (outs[i].first < outs[i - 1].second)
+        return fail(DFLASH_ERR_INVALID_ARG, "two tensors to be written overlap (one tensor given twice?)");
+    for (int i = 0; i < n_tensors; ++i) {
+      if (!t[i].numel || t[i].in == t[i].out) continue;
+      const uintptr_t b = reinterpret_cast<uintptr_t>(t[i].in), e = b + t[i].numel * (t[i].bf16 ? 2 : 4);
+      auto it = std::lower_bound(outs.begin(), outs.end(), std::make_pair(e, uintptr_t(0)));   // first that starts at e or later
+      if (it != outs.begin() && std::prev(it)->second > b)
+        return fail(DFLASH_ERR_INVALID_ARG, "tensor %d overlaps a tensor to be written", i);
+    }
+    const int sms = current_sms();
+    if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+    if (ws_bytes < clip_workspace_bytes(sms))
+      return fail(DFLASH_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, clip_workspace_bytes(sms));
+    int launches = 0;
+    DF_CUDA(clip_grad_norm_launch(t.data(), n_tensors, max_norm, norm_dev, workspace, sms, &launches,
+                                  (cudaStream_t)stream),
+            "gradient clipping");
+    g_launch_count += launches;
+  } catch (const std::bad_alloc&) {
+    return fail(DFLASH_ERR_INVALID_ARG, "out of host memory for %d tensors", n_tensors);
+  }
   return DFLASH_OK;
 }
 

@@ -381,6 +381,75 @@ int32_t dflash_packed_block_attention(const void* q_dev, const void* k_ctx_dev, 
 /* Synchronises `stream` and copies the call's status word to *status_host. */
 int32_t dflash_packed_attention_status(const void* workspace, dflash_stream_t stream, int32_t* status_host);
 
+/* --- log probabilities of given tokens, and their gradient ----------------------
+ * Scoring beside the draws above: what a served token's probability was, how
+ * sure the distribution is and what else it held; and the loss of a drafter's
+ * training (paper §4.2, eq. 1: cross-entropy weighted by position) with its
+ * gradient.  For every row x of logits, with z = x / T and p = softmax(z):
+ *   lse = ln sum_v e^(z_v)      logprob = z_token - lse
+ *   entropy = -sum_v p_v ln p_v (nats, 0 ln 0 = 0)
+ *   top_ids, top_logprobs: the top_k likeliest tokens, descending, ties to the
+ *   lowest id, with their log probabilities
+ * One launch, no workspace; the logits are read once.
+ *   logits_dev  [rows][vocab] in `dtype`, rows row_stride (>= vocab) elements
+ *               apart; any vocab in [1, 2^24], any alignment of the type
+ *   tokens_dev  int32 [rows] with logprob_dev fp32 [rows], or both NULL; a token
+ *               outside [0, vocab) (padding, -1) scores 0
+ *   entropy_dev, lse_dev   fp32 [rows] or NULL
+ *   top_ids_dev int32, top_logprobs_dev fp32 [rows][top_k]; unused for top_k = 0;
+ *               top_k <= min(32, vocab)
+ * Masked logits (-inf, or the type's lowest value) have probability 0.  A row
+ * of -inf alone has lse -inf, log probabilities -inf and entropy 0.  A row
+ * with a NaN or +inf gives NaN, its top_ids being those of its largest logits
+ * that are numbers (-1 where there are none left).  rows <= 65535; 0 < T and
+ * 1/T < inf; rows = 0 launches nothing. */
+int32_t dflash_token_logprobs(const void* logits_dev, int32_t dtype, int64_t row_stride, const int32_t* tokens_dev,
+                              int32_t rows, int32_t vocab, float temperature, int32_t top_k, float* logprob_dev,
+                              float* entropy_dev, float* lse_dev, int32_t* top_ids_dev, float* top_logprobs_dev,
+                              dflash_stream_t stream);
+
+/* d_logits = gradient of sum_r (d_logprob[r] logprob[r] + d_entropy[r] entropy[r]):
+ *   dx_v = (1/T) [ d_logprob (1[v = token] - p_v) - d_entropy p_v (ln p_v + entropy) ]
+ * from lse (and entropy) as dflash_token_logprobs gave them for the same
+ * logits and T.  The position-weighted cross-entropy is d_logprob[r] = -w_r / n.
+ *   d_logprob_dev with tokens_dev, and d_entropy_dev with entropy_dev, fp32
+ *               [rows]; either pair may be NULL, not both
+ *   d_logits_dev  [rows][vocab] in `dtype`, rows d_row_stride apart, rounded to
+ *               nearest; may be the logits themselves (the same rows), and
+ *               overlaps them in no other way
+ * A token outside [0, vocab) has no gradient of its log probability; neither
+ * has a row that masks everything (lse below -1e30) any gradient.  p is
+ * computed from lse, so its relative error grows as |lse| * 2^-24. */
+int32_t dflash_token_logprobs_backward(const void* logits_dev, int32_t dtype, int64_t row_stride,
+                                       const int32_t* tokens_dev, int32_t rows, int32_t vocab, float temperature,
+                                       const float* lse_dev, const float* entropy_dev, const float* d_logprob_dev,
+                                       const float* d_entropy_dev, void* d_logits_dev, int64_t d_row_stride,
+                                       dflash_stream_t stream);
+
+/* --- global gradient norm and clipping -------------------------------------------
+ * Paper §7.1 trains the drafter with gradients clipped at norm 1.0.  Over all
+ * tensors together, norm = sqrt(sum g^2); where it is finite and exceeds
+ * max_norm every gradient is multiplied by max_norm / norm, else it stays as
+ * it is, bit for bit (a norm of inf or NaN clips nothing: read it and drop the
+ * step).
+ *   grads_host, out_host   HOST arrays of n_tensors device pointers; out_host
+ *               NULL clips in place, else the (clipped) gradients are written
+ *               there; out_host[i] may be grads_host[i] and overlaps no other
+ *               tensor
+ *   numel_host  elements of each tensor (contiguous; 0 is skipped, its pointers
+ *               may be NULL);  dtype_host  DFLASH_DTYPE_* of each
+ *   max_norm    >= 0; infinity in place computes the norm alone
+ *   norm_dev    fp32 [1]: the norm before clipping
+ *   workspace   >= dflash_clip_workspace_bytes() bytes, 8-byte aligned
+ * The host arrays are read before the call returns.  Sums of squares are kept
+ * in double, so finite gradients of any size have a finite norm (norm_dev
+ * itself is inf where it exceeds fp32), and are added in a fixed order: the
+ * same call gives the same bits on the same device. */
+size_t dflash_clip_workspace_bytes(void);
+int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_host, const int64_t* numel_host,
+                              const int32_t* dtype_host, int32_t n_tensors, float max_norm, float* norm_dev,
+                              void* workspace, size_t workspace_bytes, dflash_stream_t stream);
+
 /* --- block-size scheduling (host policy) ---------------------------------------
  * Paper §5.5.4: a drafter trained at a large block size serves smaller
  * inference-time block sizes nearly as well, and large blocks raise the
