@@ -24,7 +24,8 @@ __all__ = ["DFlashError", "Model", "Cache", "lib", "dflash_model_create", "dflas
            "dflash_selftest_wait_timeout", "dflash_sampling_workspace", "dflash_verify_sampled", "dflash_sample_tokens",
            "BlockPolicy", "dflash_packed_attention_workspace", "dflash_packed_block_attention",
            "dflash_packed_attention_status", "dflash_token_logprobs", "dflash_token_logprobs_backward",
-           "dflash_clip_workspace", "dflash_clip_grad_norm"]
+           "dflash_clip_workspace", "dflash_clip_grad_norm", "dflash_packed_attention_backward_workspace",
+           "dflash_packed_block_attention_backward"]
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
@@ -305,9 +306,12 @@ def dflash_packed_attention_workspace(n_blocks: int, block: int, seq_len: int, n
 
 def dflash_packed_block_attention(q: torch.Tensor, k_ctx: torch.Tensor, v_ctx: torch.Tensor, k_blk: torch.Tensor,
                                   v_blk: torch.Tensor, anchors_dev: torch.Tensor, out: torch.Tensor,
-                                  workspace: torch.Tensor, anchors_host=None, stream=None) -> None:
+                                  workspace: torch.Tensor, anchors_host=None, stream=None,
+                                  lse: Optional[torch.Tensor] = None) -> None:
     """Packed training attention: q [N, g, nq, hd], k_ctx / v_ctx [S, nkv, hd],
-    k_blk / v_blk [N, g, nkv, hd] (fp32 or bf16), anchors int32 [N] -> out fp32 [N, g, nq, hd]."""
+    k_blk / v_blk [N, g, nkv, hd] (fp32 or bf16), anchors int32 [N] -> out fp32 [N, g, nq, hd];
+    lse fp32 [N, g, nq], if given, receives the log-sum-exp of each row's scores
+    (what dflash_packed_block_attention_backward needs)."""
     N, g, nq, hd = q.shape
     S, nkv = k_ctx.shape[0], k_blk.shape[2]
     dt = _abi.DTYPE_F32 if q.dtype == torch.float32 else _abi.DTYPE_BF16
@@ -319,10 +323,63 @@ def dflash_packed_block_attention(q: torch.Tensor, k_ctx: torch.Tensor, v_ctx: t
     host = None
     if anchors_host is not None:
         host = (ctypes.c_int32 * N)(*[int(a) for a in anchors_host])
+    if lse is not None:
+        check(lib().dflash_packed_block_attention_lse(
+            _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk), _ptr(anchors_dev), host, N, g, S, nq, nkv, hd,
+            dt, _ptr(out), _vector(lse, N * g * nq, torch.float32, q, "lse"), _ptr(workspace), workspace.numel(),
+            _stream_ptr(stream)), "dflash_packed_block_attention_lse")
+        return
     check(lib().dflash_packed_block_attention(_ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk),
                                               _ptr(anchors_dev), host, N, g, S, nq, nkv, hd, dt, _ptr(out),
                                               _ptr(workspace), workspace.numel(), _stream_ptr(stream)),
           "dflash_packed_block_attention")
+
+
+def dflash_packed_attention_backward_workspace(n_blocks: int, block: int, seq_len: int, n_q_heads: int,
+                                               n_kv_heads: int, head_dim: int, dtype: torch.dtype) -> torch.Tensor:
+    """Device scratch for dflash_packed_block_attention_backward with operands of `dtype`."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("operands are float32 or bfloat16")
+    n = int(lib().dflash_packed_attention_backward_workspace_bytes(
+        n_blocks, block, seq_len, n_q_heads, n_kv_heads, head_dim,
+        _abi.DTYPE_F32 if dtype == torch.float32 else _abi.DTYPE_BF16))
+    if n == 0:
+        raise ValueError("invalid packed attention shape")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def dflash_packed_block_attention_backward(q: torch.Tensor, k_ctx: torch.Tensor, v_ctx: torch.Tensor,
+                                           k_blk: torch.Tensor, v_blk: torch.Tensor, anchors_dev: torch.Tensor,
+                                           out: torch.Tensor, lse: torch.Tensor, d_out: torch.Tensor,
+                                           d_q: torch.Tensor, d_k_ctx: torch.Tensor, d_v_ctx: torch.Tensor,
+                                           d_k_blk: torch.Tensor, d_v_blk: torch.Tensor, workspace: torch.Tensor,
+                                           anchors_host=None, stream=None) -> None:
+    """Gradients of dflash_packed_block_attention: from its operands, its out and
+    lse and d_out fp32 [N, g, nq, hd] -> d_q, d_k_ctx, d_v_ctx, d_k_blk, d_v_blk,
+    shaped and typed as the operands (every element is written)."""
+    _on_current_device(q)
+    if q.dim() != 4 or k_ctx.dim() != 3 or k_blk.dim() != 4:
+        raise ValueError("q [N, g, nq, hd], k_ctx [S, nkv, hd] and k_blk [N, g, nkv, hd] are expected")
+    N, g, nq, hd = q.shape
+    S, nkv = k_ctx.shape[0], k_blk.shape[2]
+    dt = q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("operands are float32 or bfloat16")
+    rows, ctx, blk = N * g * nq * hd, S * nkv * hd, N * g * nkv * hd
+    vec = lambda t, n, name: _vector(t, n, dt, q, name)  # noqa: E731
+    host = None
+    if anchors_host is not None:
+        if len(anchors_host) != N:
+            raise ValueError("anchors_host must have one entry per block")
+        host = (ctypes.c_int32 * N)(*[int(a) for a in anchors_host])
+    check(lib().dflash_packed_block_attention_backward(
+        vec(q, rows, "q"), vec(k_ctx, ctx, "k_ctx"), vec(v_ctx, ctx, "v_ctx"), vec(k_blk, blk, "k_blk"),
+        vec(v_blk, blk, "v_blk"), _vector(anchors_dev, N, torch.int32, q, "anchors_dev"), host, N, g, S, nq, nkv, hd,
+        _abi.DTYPE_F32 if dt == torch.float32 else _abi.DTYPE_BF16, _vector(out, rows, torch.float32, q, "out"),
+        _vector(lse, N * g * nq, torch.float32, q, "lse"), _vector(d_out, rows, torch.float32, q, "d_out"),
+        vec(d_q, rows, "d_q"), vec(d_k_ctx, ctx, "d_k_ctx"), vec(d_v_ctx, ctx, "d_v_ctx"), vec(d_k_blk, blk, "d_k_blk"),
+        vec(d_v_blk, blk, "d_v_blk"), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream)), "dflash_packed_block_attention_backward")
 
 
 def dflash_packed_attention_status(workspace: torch.Tensor, stream=None) -> int:

@@ -87,6 +87,12 @@ SIGNATURES = {
     "dflash_packed_block_attention": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_i32p, c_i32, c_i32, c_i32,
                                               c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_size, c_ptr]),
     "dflash_packed_attention_status": (c_i32, [c_ptr, c_ptr, c_i32p]),
+    "dflash_packed_block_attention_lse": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_i32p, c_i32, c_i32, c_i32,
+                                                  c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_size, c_ptr]),
+    "dflash_packed_attention_backward_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "dflash_packed_block_attention_backward": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_i32p, c_i32, c_i32,
+                                                       c_i32, c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_ptr,
+                                                       c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_size, c_ptr]),
     "dflash_token_logprobs": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_i32, c_i32, ctypes.c_float, c_i32, c_ptr,
                                       c_ptr, c_ptr, c_ptr, c_ptr, c_ptr]),
     "dflash_token_logprobs_backward": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_i32, c_i32, ctypes.c_float, c_ptr,

@@ -22,6 +22,7 @@
 #include "logprobs.cuh"
 #include "grad_clip.cuh"
 #include "packed_attention.cuh"
+#include "packed_attention_bwd.cuh"
 
 using namespace dflash;
 
@@ -1313,11 +1314,11 @@ size_t dflash_packed_attention_workspace_bytes(int32_t n_blocks, int32_t block, 
   return packed_workspace_bytes(std::max(n_blocks, 1), block, seq_len, nq, nkv, hd, sms);
 }
 
-int32_t dflash_packed_block_attention(const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
-                                      const void* v_blk, const int32_t* anchors_dev, const int32_t* anchors_host,
-                                      int32_t n_blocks, int32_t block, int32_t seq_len, int32_t nq, int32_t nkv,
-                                      int32_t hd, int32_t dtype, float* out, void* workspace, size_t ws_bytes,
-                                      dflash_stream_t stream) {
+namespace {
+int32_t packed_forward(const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk, const void* v_blk,
+                       const int32_t* anchors_dev, const int32_t* anchors_host, int32_t n_blocks, int32_t block,
+                       int32_t seq_len, int32_t nq, int32_t nkv, int32_t hd, int32_t dtype, float* out, float* lse,
+                       void* workspace, size_t ws_bytes, dflash_stream_t stream) {
   int32_t rc = packed_shape(n_blocks, block, seq_len, nq, nkv, hd);
   if (rc) return rc;
   if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", dtype);
@@ -1348,6 +1349,122 @@ int32_t dflash_packed_block_attention(const void* q, const void* k_ctx, const vo
   DF_CUDA(packed_attention_run(pl, dtype == DFLASH_DTYPE_F32, q, seq_len ? k_ctx : nullptr, seq_len ? v_ctx : nullptr,
                                k_blk, v_blk, anchors_dev, out, sms, &launches, (cudaStream_t)stream),
           "packed block attention");
+  g_launch_count += launches;
+  if (lse) {
+    DF_CUDA(packed_lse_launch(pl.ml, n_blocks, block, nq, pl.splits, lse, (cudaStream_t)stream), "packed attention lse");
+    g_launch_count += 1;
+  }
+  return DFLASH_OK;
+}
+}  // namespace
+
+int32_t dflash_packed_block_attention(const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
+                                      const void* v_blk, const int32_t* anchors_dev, const int32_t* anchors_host,
+                                      int32_t n_blocks, int32_t block, int32_t seq_len, int32_t nq, int32_t nkv,
+                                      int32_t hd, int32_t dtype, float* out, void* workspace, size_t ws_bytes,
+                                      dflash_stream_t stream) {
+  return packed_forward(q, k_ctx, v_ctx, k_blk, v_blk, anchors_dev, anchors_host, n_blocks, block, seq_len, nq, nkv, hd,
+                        dtype, out, nullptr, workspace, ws_bytes, stream);
+}
+
+int32_t dflash_packed_block_attention_lse(const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
+                                          const void* v_blk, const int32_t* anchors_dev, const int32_t* anchors_host,
+                                          int32_t n_blocks, int32_t block, int32_t seq_len, int32_t nq, int32_t nkv,
+                                          int32_t hd, int32_t dtype, float* out, float* lse, void* workspace,
+                                          size_t ws_bytes, dflash_stream_t stream) {
+  if (n_blocks > 0 && !lse) return fail(DFLASH_ERR_INVALID_ARG, "lse is NULL");
+  return packed_forward(q, k_ctx, v_ctx, k_blk, v_blk, anchors_dev, anchors_host, n_blocks, block, seq_len, nq, nkv, hd,
+                        dtype, out, lse, workspace, ws_bytes, stream);
+}
+
+namespace {
+// What the gradient's 32-bit row coordinates can hold, on top of the forward's limits.
+int32_t packed_bwd_shape(int32_t n_blocks, int32_t block, int32_t seq_len, int32_t nq, int32_t nkv, int32_t hd,
+                         int32_t dtype) {
+  int32_t rc = packed_shape(n_blocks, block, seq_len, nq, nkv, hd);
+  if (rc) return rc;
+  if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  const long long tiles = (n_blocks + 128 / block - 1) / (128 / block), keys = (seq_len + 127) / 128;
+  if (tiles * 128 * nq * 2 >= (1LL << 31) || keys * 128 * nkv * 2 >= (1LL << 31) ||
+      (keys + 2 * tiles) * nq + 1024 >= (1LL << 31))
+    return fail(DFLASH_ERR_SHAPE, "packed attention gradient exceeds 2^31 rows");
+  return DFLASH_OK;
+}
+}  // namespace
+
+size_t dflash_packed_attention_backward_workspace_bytes(int32_t n_blocks, int32_t block, int32_t seq_len, int32_t nq,
+                                                        int32_t nkv, int32_t hd, int32_t dtype) {
+  if (packed_bwd_shape(n_blocks, block, seq_len, nq, nkv, hd, dtype) != DFLASH_OK) return 0;
+  const int sms = current_sms();
+  if (sms <= 0) return 0;
+  return packed_bwd_plan(nullptr, std::max(n_blocks, 1), block, seq_len, nq, nkv, hd, dtype == DFLASH_DTYPE_F32, sms).bytes;
+}
+
+int32_t dflash_packed_block_attention_backward(const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
+                                               const void* v_blk, const int32_t* anchors_dev,
+                                               const int32_t* anchors_host, int32_t n_blocks, int32_t block,
+                                               int32_t seq_len, int32_t nq, int32_t nkv, int32_t hd, int32_t dtype,
+                                               const float* out, const float* lse, const float* d_out, void* d_q,
+                                               void* d_k_ctx, void* d_v_ctx, void* d_k_blk, void* d_v_blk,
+                                               void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  int32_t rc = packed_bwd_shape(n_blocks, block, seq_len, nq, nkv, hd, dtype);
+  if (rc) return rc;
+  if (seq_len > 0 && (!d_k_ctx || !d_v_ctx)) return fail(DFLASH_ERR_INVALID_ARG, "d_k_ctx or d_v_ctx is NULL");
+  if (!workspace) return fail(DFLASH_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(DFLASH_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (n_blocks > 0 && (!q || !k_blk || !v_blk || !anchors_dev || !out || !lse || !d_out || !d_q || !d_k_blk || !d_v_blk ||
+                       (seq_len > 0 && (!k_ctx || !v_ctx))))
+    return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  for (const void* p : {static_cast<const void*>(d_q), static_cast<const void*>(d_k_ctx), static_cast<const void*>(d_v_ctx),
+                        static_cast<const void*>(d_k_blk), static_cast<const void*>(d_v_blk)})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return fail(DFLASH_ERR_INVALID_ARG, "gradients must be 16-byte aligned");
+  const uintptr_t es = dtype == DFLASH_DTYPE_F32 ? 4 : 2;
+  for (const void* p : {q, k_ctx, v_ctx, k_blk, v_blk})
+    if (reinterpret_cast<uintptr_t>(p) % es) return fail(DFLASH_ERR_INVALID_ARG, "an operand is not aligned to its type");
+  if (anchors_host)
+    for (int n = 0; n < n_blocks; ++n)
+      if (anchors_host[n] < 0 || anchors_host[n] > seq_len)
+        return fail(DFLASH_ERR_INVALID_ARG, "anchor[%d] = %d outside [0, %d]", n, anchors_host[n], seq_len);
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  const bool f32 = dtype == DFLASH_DTYPE_F32;
+  const PackedBwdPlan pl = packed_bwd_plan(workspace, std::max(n_blocks, 1), block, seq_len, nq, nkv, hd, f32, sms);
+  if (ws_bytes < pl.bytes) return fail(DFLASH_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, pl.bytes);
+  if (n_blocks == 0) {   // the context has no reader: its gradients are zero
+    const size_t bytes = (size_t)seq_len * nkv * hd * es;
+    DF_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream), "status reset");
+    if (bytes) {
+      DF_CUDA(cudaMemsetAsync(d_k_ctx, 0, bytes, (cudaStream_t)stream), "zero gradient");
+      DF_CUDA(cudaMemsetAsync(d_v_ctx, 0, bytes, (cudaStream_t)stream), "zero gradient");
+    }
+    return DFLASH_OK;
+  }
+  // shared-memory opt-in of the gradient kernel, once per device, head size and type
+  static std::atomic<unsigned> prepared[64];
+  int dev = 0;
+  DF_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  const unsigned bit = (hd == 64 ? 1u : 2u) << (f32 ? 2 : 0);
+  if (dev < 0 || dev >= 64 || !(prepared[dev].load() & bit)) {
+    DF_CUDA(packed_bwd_prepare(hd, f32), "packed attention gradient set-up");
+    if (dev >= 0 && dev < 64) prepared[dev].fetch_or(bit);
+  }
+  PackedBwdTensors t{};
+  t.q = q;
+  t.k_ctx = k_ctx;
+  t.v_ctx = v_ctx;
+  t.k_blk = k_blk;
+  t.v_blk = v_blk;
+  t.anchors = anchors_dev;
+  t.out = out;
+  t.lse = lse;
+  t.d_out = d_out;
+  t.d_q = d_q;
+  t.d_k_ctx = d_k_ctx;
+  t.d_v_ctx = d_v_ctx;
+  t.d_k_blk = d_k_blk;
+  t.d_v_blk = d_v_blk;
+  int launches = 0;
+  DF_CUDA(packed_bwd_run(pl, t, sms, &launches, (cudaStream_t)stream), "packed block attention gradient");
   g_launch_count += launches;
   return DFLASH_OK;
 }

@@ -1,0 +1,56 @@
+// Gradients of the packed training attention (packed_attention_bwd.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace dflash {
+
+// Shapes and operand layout of one call, carved from the caller's workspace.
+// Rows are the blocks in ascending order of their anchors, whole blocks to a
+// tile of 128 rows (`per` of them, then padding).
+struct PackedBwdPlan {
+  int N, block, S, nq, nkv, hd;
+  int planes;             // bf16 operand planes: 1 (bf16 tensors) or 2 (fp32 tensors as hi + lo)
+  int per;                // blocks in a row tile
+  int T;                  // row tiles
+  int KT;                 // 128-key tiles of the context
+  int splits;             // CTAs that share one (q head, context key tile)'s row tiles
+  int32_t* status;
+  int32_t* order;         // [N] block of each sorted place
+  int32_t* sorted;        // [N] anchors in ascending order
+  int32_t* row_anchor;    // [T*128] anchor of the row's block (0 in padding)
+  float* lse2;            // [nq][T*128] lse log2(e), +inf in padding
+  float* delta;           // [nq][T*128] sum_d d_out out
+  __nv_bfloat16* q;       // [nq][planes][T*128][hd], zero in padding (d_o, kb and vb too)
+  __nv_bfloat16* d_o;
+  __nv_bfloat16* kc;      // [nkv][planes][KT*128][hd]
+  __nv_bfloat16* vc;
+  __nv_bfloat16* kb;      // [nkv][planes][T*128][hd]
+  __nv_bfloat16* vb;
+  float* dk_part;         // [nq*splits][S][hd] this head's and split's share of d_k_ctx
+  float* dv_part;
+  size_t bytes;
+};
+
+PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv, int hd, bool f32, int sms);
+
+struct PackedBwdTensors {
+  const void *q, *k_ctx, *v_ctx, *k_blk, *v_blk;
+  const int32_t* anchors;
+  const float *out, *lse, *d_out;
+  void *d_q, *d_k_ctx, *d_v_ctx, *d_k_blk, *d_v_blk;
+};
+
+// Shared-memory opt-in of the gradient kernel (once per device).
+cudaError_t packed_bwd_prepare(int hd, bool f32);
+cudaError_t packed_bwd_run(const PackedBwdPlan& pl, const PackedBwdTensors& t, int sms, int* launches, cudaStream_t s);
+
+// lse[n][i][h] = ln of the softmax denominator of each query row, from the
+// forward's split partials.
+cudaError_t packed_lse_launch(const float2* ml, int N, int block, int nq, int splits, float* lse, cudaStream_t s);
+
+}  // namespace dflash

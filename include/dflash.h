@@ -378,6 +378,47 @@ int32_t dflash_packed_block_attention(const void* q_dev, const void* k_ctx_dev, 
                                       int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
                                       float* out_dev, void* workspace, size_t workspace_bytes,
                                       dflash_stream_t stream);
+/* The same, and lse_dev fp32 [n_blocks][block][n_q_heads]: the natural log of
+ * the sum of e^(scores) of each row, for the gradient below. */
+int32_t dflash_packed_block_attention_lse(const void* q_dev, const void* k_ctx_dev, const void* v_ctx_dev,
+                                          const void* k_blk_dev, const void* v_blk_dev, const int32_t* anchors_dev,
+                                          const int32_t* anchors_host, int32_t n_blocks, int32_t block, int32_t seq_len,
+                                          int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                          float* out_dev, float* lse_dev, void* workspace, size_t workspace_bytes,
+                                          dflash_stream_t stream);
+
+/* --- training-time packed block attention (gradient) ---------------------------
+ * Gradients of every operand of dflash_packed_block_attention.  With P the
+ * softmax, D = sum_d d_out out and ds = P (d_out v^T - D):
+ *   d_q = ds k / sqrt(head_dim)   d_k = ds^T q / sqrt(head_dim)   d_v = P^T d_out
+ * A context key's gradients sum over the blocks anchored behind it and over
+ * the query heads that share its kv head; those of keys that no block sees
+ * are 0.
+ *   operands, anchors (and their checks) as in the forward
+ *   out_dev, lse_dev   the forward's; d_out_dev fp32, as out_dev
+ *   d_q_dev, d_k_ctx_dev, d_v_ctx_dev, d_k_blk_dev, d_v_blk_dev   shaped as the
+ *               operands, in `dtype`, 16-byte aligned; every element is written
+ *   workspace   >= dflash_packed_attention_backward_workspace_bytes(...) bytes,
+ *               256-byte aligned; its first int32 is the call's status word
+ *               (dflash_packed_attention_status)
+ * Operands have to be finite: a NaN or an infinity spreads to gradients that
+ * do not depend on it.  bf16: products of bf16 operands (P and ds rounded to
+ * bf16) summed in fp32; fp32: hi/lo bf16 pairs, fp32-level precision.  The
+ * same call gives the same bits on the same device.  n_blocks = 0 zeroes
+ * d_k_ctx and d_v_ctx.  The forward's limits, and 2^31 rows of laid-out
+ * operands.  The workspace size depends on the current device's SM count. */
+size_t dflash_packed_attention_backward_workspace_bytes(int32_t n_blocks, int32_t block, int32_t seq_len,
+                                                        int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                        int32_t dtype);
+int32_t dflash_packed_block_attention_backward(const void* q_dev, const void* k_ctx_dev, const void* v_ctx_dev,
+                                               const void* k_blk_dev, const void* v_blk_dev, const int32_t* anchors_dev,
+                                               const int32_t* anchors_host, int32_t n_blocks, int32_t block,
+                                               int32_t seq_len, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                               int32_t dtype, const float* out_dev, const float* lse_dev,
+                                               const float* d_out_dev, void* d_q_dev, void* d_k_ctx_dev,
+                                               void* d_v_ctx_dev, void* d_k_blk_dev, void* d_v_blk_dev, void* workspace,
+                                               size_t workspace_bytes, dflash_stream_t stream);
+
 /* Synchronises `stream` and copies the call's status word to *status_host. */
 int32_t dflash_packed_attention_status(const void* workspace, dflash_stream_t stream, int32_t* status_host);
 
