@@ -34,11 +34,16 @@
 // Each operand tile is staged once and read in both directions: K-major for S and
 // dP, MN-major as the B operand of the gradients.
 //
-// bf16 tensors: one bf16 plane; P and dS enter their products rounded to bf16
-// (2^-9 of each term, below the rounding of the bf16 gradients themselves), every
-// sum and the softmax are fp32.  fp32 tensors: every operand, P and dS included,
-// is a hi + lo pair of bf16 and each product three MMAs (hi hi, hi lo, lo hi; what
-// is dropped is 2^-18 of a term).
+// Operands, P and dS enter the products as fp16, which has three more bits than
+// bf16, scaled by powers of two so that its range holds them: q, k, v and d_out
+// each by the power that brings its largest value to 2^14 .. 2^15, P (at most 1) by
+// 2^14, and ds by what the largest norms of d_out's and v's rows allow it
+// (|dp| <= |d_out_r| |v_j|).  The scales are folded into factors that are there
+// anyway, and powers of two are exact.  bf16 tensors take one plane: the operands
+// are then exact but for d_out, and d_out, P and ds are rounded by 2^-12 of
+// themselves, an eighth of the rounding of the bf16 gradients.  fp32 tensors
+// take each operand, P and ds included, as a hi + lo pair (22 bits) and each
+// product as three MMAs (hi hi, hi lo, lo hi).  Every sum and the softmax are fp32.
 #include <cuda.h>
 
 #include <algorithm>
@@ -54,38 +59,36 @@ namespace {
 constexpr int kRows = 128;           // rows of a row tile, keys of a key tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr long long kBudget = 400000000LL;
+constexpr int kOpExp = 14;           // an operand's largest value lies in [2^14, 2^15)
+constexpr int kPExp = 14;            // P is held times 2^14
+constexpr int kRangeValues = 6;      // largest |q|, |k|, |v|, |d_out|, and largest norm of a row of v, d_out
+constexpr int kRangeThreads = 512;
 
-// ---------------------------------------------------------------- anchors in ascending order
-// Place of block n: how many blocks have a smaller anchor, or the same and a
-// smaller number.  Anchors outside [0, S] are clamped and flagged.
-__global__ void __launch_bounds__(256) rank_kernel(PackedBwdPlan pl, const int32_t* anchors) {
-  griddep_wait();
-  griddep_trigger();
-  __shared__ int32_t tile[1024];
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  auto at = [&](int i) { return min(max(anchors[i], 0), pl.S); };
-  const int own = n < pl.N ? at(n) : 0;
-  int rank = 0, bad = 0;
-  for (int base = 0; base < pl.N; base += 1024) {
-    const int cnt = min(1024, pl.N - base);
-    __syncthreads();
-    for (int i = threadIdx.x; i < cnt; i += 256) {
-      const int a = anchors[base + i];
-      bad |= a < 0 || a > pl.S;
-      tile[i] = min(max(a, 0), pl.S);
-    }
-    __syncthreads();
-    for (int i = 0; i < cnt; ++i) rank += tile[i] < own || (tile[i] == own && base + i < n);
-  }
-  bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *pl.status = bad ? DFLASH_ERR_INVALID_ARG : 0;
-  if (n < pl.N) {
-    pl.order[rank] = n;
-    pl.sorted[rank] = own;
-  }
+// Exponents e of the scales 2^e of q, k, v and d_out, and of dp (and D):
+// ds is held as P 2^14 (dp - D) 2^dp.
+struct Scales {
+  int q, k, v, o, dp;
+};
+__device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
+// The exponent that brings m into [2^14, 2^15), within what a float holds.
+__device__ __forceinline__ int scale_exp(float m) {
+  if (!(m > 0.f) || isinf(m)) return 0;
+  return max(-120, min(120, kOpExp - ilogbf(m)));
 }
+__device__ __forceinline__ Scales scales_of(const float* m) {
+  Scales s;
+  s.q = scale_exp(m[0]);
+  s.k = scale_exp(m[1]);
+  s.v = scale_exp(m[2]);
+  s.o = scale_exp(m[3]);
+  // |dp - D| <= 2 |d_out| |v| by the rows' norms
+  auto norm_exp = [](float n) { return n > 0.f && !isinf(n) ? ilogbf(n) + 1 : 0; };
+  s.dp = -(norm_exp(m[4]) + norm_exp(m[5]) + 1);
+  return s;
+}
+__device__ __forceinline__ Scales load_scales(const int32_t* p) { return Scales{p[0], p[1], p[2], p[3], p[4]}; }
 
-// ---------------------------------------------------------------- operand layout
+// ---------------------------------------------------------------- loads
 // E (2 or 4) consecutive values, in one load where their address allows it.
 template <int E>
 __device__ __forceinline__ void load_values(const float* p, float* v) {
@@ -120,17 +123,133 @@ __device__ __forceinline__ void load_values(const __nv_bfloat16* p, float* v) {
   }
 }
 
-// E = hd / 32 values of a lane, as one or two bf16 planes `plane` apart.
+// ---------------------------------------------------------------- anchors in order, ranges of the operands
+// Place of block n: how many blocks have a smaller anchor, or the same and a
+// smaller number.  Anchors outside [0, S] are clamped and flagged.
+__device__ void rank_blocks(const PackedBwdPlan& pl, const int32_t* anchors, int cta) {
+  __shared__ int32_t tile[1024];
+  const int n = cta * kRangeThreads + threadIdx.x;
+  const int own = n < pl.N ? min(max(anchors[n], 0), pl.S) : 0;
+  int rank = 0, bad = 0;
+  for (int base = 0; base < pl.N; base += 1024) {
+    const int cnt = min(1024, pl.N - base);
+    __syncthreads();
+    for (int i = threadIdx.x; i < cnt; i += kRangeThreads) {
+      const int a = anchors[base + i];
+      bad |= a < 0 || a > pl.S;
+      tile[i] = min(max(a, 0), pl.S);
+    }
+    __syncthreads();
+    for (int i = 0; i < cnt; ++i) rank += tile[i] < own || (tile[i] == own && base + i < n);
+  }
+  bad = __syncthreads_or(bad);
+  if (cta == 0 && threadIdx.x == 0) *pl.status = bad ? DFLASH_ERR_INVALID_ARG : 0;
+  if (n < pl.N) {
+    pl.order[rank] = n;
+    pl.sorted[rank] = own;
+  }
+}
+
+// Largest value (and, where NORM, largest norm of a row) of `rows` rows of
+// HD values; a warp takes four rows at a time.
+template <typename T, int HD, bool NORM>
+__device__ __forceinline__ void range_rows(const T* x, long long rows, int part, int parts, float& mx, float& nm) {
+  constexpr int E = HD / 32, U = 4;
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)parts * (kRangeThreads / 32);
+  for (long long r0 = ((long long)part * (kRangeThreads / 32) + (threadIdx.x >> 5)) * U; r0 < rows; r0 += warps * U) {
+    float v[U][E] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u < rows) load_values<E>(x + (size_t)(r0 + u) * HD + E * lane, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        mx = fmaxf(mx, fabsf(v[u][e]));
+        if (NORM) sq = fmaf(v[u][e], v[u][e], sq);
+      }
+      if (NORM) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        if (sq > 1.0e-30f && sq < 1.0e36f) {
+          nm = fmaxf(nm, sqrtf(sq));
+        } else {   // zeros, or squares outside fp32's range: over the row's largest value
+          float top = 0.f, s2 = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[u][e]));
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (top > 0.f) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s2 = fmaf(v[u][e] / top, v[u][e] / top, s2);
+            for (int o = 16; o; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+            nm = fmaxf(nm, top * sqrtf(s2));
+          }
+        }
+      }
+    }
+  }
+}
+
+// The first CTAs put the blocks in order, the others look for the operands'
+// ranges (one row of maxima each, merged by the next kernel).
+template <typename T, int HD>
+__global__ void __launch_bounds__(kRangeThreads) range_kernel(PackedBwdPlan pl, PackedBwdTensors t) {
+  griddep_wait();
+  griddep_trigger();
+  const int rank_ctas = (pl.N + kRangeThreads - 1) / kRangeThreads;
+  if ((int)blockIdx.x < rank_ctas) {
+    rank_blocks(pl, t.anchors, blockIdx.x);
+    return;
+  }
+  const int part = blockIdx.x - rank_ctas, parts = pl.parts;
+  float m[kRangeValues] = {};
+  float none = 0.f;
+  const long long qr = (long long)pl.N * pl.block * pl.nq, br = (long long)pl.N * pl.block * pl.nkv,
+                  cr = (long long)pl.S * pl.nkv;
+  range_rows<T, HD, false>(static_cast<const T*>(t.q), qr, part, parts, m[0], none);
+  range_rows<float, HD, true>(t.d_out, qr, part, parts, m[3], m[5]);
+  range_rows<T, HD, false>(static_cast<const T*>(t.k_blk), br, part, parts, m[1], none);
+  range_rows<T, HD, true>(static_cast<const T*>(t.v_blk), br, part, parts, m[2], m[4]);
+  range_rows<T, HD, false>(static_cast<const T*>(t.k_ctx), cr, part, parts, m[1], none);
+  range_rows<T, HD, true>(static_cast<const T*>(t.v_ctx), cr, part, parts, m[2], m[4]);
+  __shared__ float sh[kRangeThreads / 32][kRangeValues];
+#pragma unroll
+  for (int i = 0; i < kRangeValues; ++i) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5][i] = m[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kRangeValues) {
+    float x = 0.f;
+    for (int w = 0; w < kRangeThreads / 32; ++w) x = fmaxf(x, sh[w][threadIdx.x]);
+    pl.part[part * kRangeValues + threadIdx.x] = x;
+  }
+}
+
+// ---------------------------------------------------------------- operand layout
+// E = hd / 32 values of a lane times `scale`, as one or two fp16 planes `plane`
+// apart; v becomes what the planes hold.
 template <int E>
-__device__ __forceinline__ void put_planes(__nv_bfloat16* dst, size_t plane, int planes, const float* v) {
-  __nv_bfloat162 h[E / 2], l[E / 2];
+__device__ __forceinline__ void put_planes(__half* dst, size_t plane, int planes, float scale, float* v) {
+  __half2 h[E / 2], l[E / 2];
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
-    h[e / 2] = __floats2bfloat162_rn(v[e], v[e + 1]);
-    const float2 f = __bfloat1622float2(h[e / 2]);
-    l[e / 2] = __floats2bfloat162_rn(v[e] - f.x, v[e + 1] - f.y);
+    const float x = v[e] * scale, y = v[e + 1] * scale;
+    h[e / 2] = __floats2half2_rn(x, y);
+    float2 f = __half22float2(h[e / 2]);
+    l[e / 2] = __floats2half2_rn(x - f.x, y - f.y);
+    v[e] = f.x;
+    v[e + 1] = f.y;
+    if (planes == 2) {
+      f = __half22float2(l[e / 2]);
+      v[e] += f.x;
+      v[e + 1] += f.y;
+    }
   }
-  auto put = [&](__nv_bfloat16* d, const __nv_bfloat162* x) {
+  auto put = [&](__half* d, const __half2* x) {
     if constexpr (E == 4)
       *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(x);
     else
@@ -150,6 +269,30 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
   const int lane = threadIdx.x & 31, g = pl.block, rows = pl.T * kRows, ctx = pl.KT * kRows;
   const long long n_q = (long long)rows * pl.nq, n_b = (long long)rows * pl.nkv, n_c = (long long)ctx * pl.nkv;
   const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+  // the CTAs' maxima become the scales
+  __shared__ float s_max[kRangeValues];
+  __shared__ Scales s_sc;
+  if (threadIdx.x < 32 * kRangeValues) {
+    const int i = threadIdx.x >> 5;
+    float x = 0.f;
+    for (int p = lane; p < pl.parts; p += 32) x = fmaxf(x, pl.part[p * kRangeValues + i]);
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (lane == 0) s_max[i] = x;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s_sc = scales_of(s_max);
+    if (blockIdx.x == 0) {
+      pl.scale[0] = s_sc.q;
+      pl.scale[1] = s_sc.k;
+      pl.scale[2] = s_sc.v;
+      pl.scale[3] = s_sc.o;
+      pl.scale[4] = s_sc.dp;
+    }
+  }
+  __syncthreads();
+  const float f_q = pow2(s_sc.q), f_k = pow2(s_sc.k), f_v = pow2(s_sc.v), f_o = pow2(s_sc.o);
+  const int e_d = s_sc.dp - s_sc.o;   // D is summed over the scaled d_out
   // block and position of a row; -1: padding
   auto place = [&](int r, int& n, int& i) {
     const int k = r % kRows, b = k / g, at = (r / kRows) * pl.per + b;
@@ -169,17 +312,18 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
         load_values<E>(static_cast<const T*>(t.q) + o, a);
         load_values<E>(t.d_out + o, b);
         load_values<E>(t.out + o, c);
-        l = t.lse[row] * kLog2e;
-#pragma unroll
-        for (int e = 0; e < E; ++e) d = fmaf(b[e], c[e], d);
+        l = fmaf(t.lse[row], kLog2e, -(float)kPExp);
       }
-      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
       const size_t dst = ((size_t)h * pl.planes * rows + r) * HD + E * lane, plane = (size_t)rows * HD;
-      put_planes<E>(pl.q + dst, plane, pl.planes, a);
-      put_planes<E>(pl.d_o + dst, plane, pl.planes, b);
+      put_planes<E>(pl.q + dst, plane, pl.planes, f_q, a);
+      put_planes<E>(pl.d_o + dst, plane, pl.planes, f_o, b);
+      // D from d_out as the products see it: its rounding then cancels in dp - D as exactly as d_out itself would
+#pragma unroll
+      for (int e = 0; e < E; ++e) d = fmaf(b[e], c[e], d);
+      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
       if (lane == 0) {
         pl.lse2[(size_t)h * rows + r] = l;
-        pl.delta[(size_t)h * rows + r] = d;
+        pl.delta[(size_t)h * rows + r] = ldexpf(d, e_d);
         if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : 0;
       }
     } else if (w < n_q + n_b) {
@@ -193,8 +337,8 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
         load_values<E>(static_cast<const T*>(t.v_blk) + o, b);
       }
       const size_t dst = ((size_t)h * pl.planes * rows + r) * HD + E * lane, plane = (size_t)rows * HD;
-      put_planes<E>(pl.kb + dst, plane, pl.planes, a);
-      put_planes<E>(pl.vb + dst, plane, pl.planes, b);
+      put_planes<E>(pl.kb + dst, plane, pl.planes, f_k, a);
+      put_planes<E>(pl.vb + dst, plane, pl.planes, f_v, b);
     } else {
       const long long u = w - n_q - n_b;
       const int h = (int)(u % pl.nkv), r = (int)(u / pl.nkv);
@@ -204,14 +348,19 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
         load_values<E>(static_cast<const T*>(t.v_ctx) + o, b);
       }
       const size_t dst = ((size_t)h * pl.planes * ctx + r) * HD + E * lane, plane = (size_t)ctx * HD;
-      put_planes<E>(pl.kc + dst, plane, pl.planes, a);
-      put_planes<E>(pl.vc + dst, plane, pl.planes, b);
+      put_planes<E>(pl.kc + dst, plane, pl.planes, f_k, a);
+      put_planes<E>(pl.vc + dst, plane, pl.planes, f_v, b);
     }
   }
 }
 
 // ---------------------------------------------------------------- tensor-core pieces
-// D[tmem] (+)= A[tmem] B[smem], bf16 in, fp32 out: A's rows on the lanes, two
+// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, M x N (formats of
+// A and B zero; both K-major).
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B[smem], fp16 in, fp32 out: A's rows on the lanes, two
 // consecutive K values to a 32-bit column.
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -221,7 +370,7 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdes
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// A tile of rows of 64 bf16 (128-byte swizzle) as an MN-major operand: the 64
+// A tile of rows of 64 fp16 (128-byte swizzle) as an MN-major operand: the 64
 // values of a row run along N, the rows along K.  lbo: bytes to the tile of the
 // next 64 values; 8 rows are 1024 bytes.
 __device__ __forceinline__ uint64_t smem_desc_mn(const void* tile, int lbo) {
@@ -254,7 +403,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 32 values as 16 columns of bf16 pairs from column `at` on and, with two
+// 32 values as 16 columns of fp16 pairs from column `at` on and, with two
 // planes, their rounding residuals in the next 16: the 32 columns that the
 // values were read from.
 template <int PL>
@@ -262,11 +411,11 @@ __device__ __forceinline__ void put_pairs(uint32_t at, const float* v) {
   uint32_t h[16], l[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
     h[j] = *reinterpret_cast<uint32_t*>(&b);
     if (PL == 2) {
-      const float2 f = __bfloat1622float2(b);
-      __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+      const float2 f = __half22float2(b);
+      __half2 r = __floats2half2_rn(v[2 * j] - f.x, v[2 * j + 1] - f.y);
       l[j] = *reinterpret_cast<uint32_t*>(&r);
     }
   }
@@ -334,7 +483,7 @@ __device__ __forceinline__ void store32(T* dst, const float* v) {
 template <int HD, int PL>
 __device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* res, const uint8_t* str) {
   using C = GradCfg<HD, PL>;
-  constexpr uint32_t id = ptx::idesc_bf16_f32(kRows, C::kN);
+  constexpr uint32_t id = idesc_f16(kRows, C::kN);
   uint32_t acc = 0;
 #pragma unroll
   for (int pr = 0; pr < (PL == 2 ? 3 : 1); ++pr) {   // hi hi, hi lo, lo hi
@@ -354,7 +503,7 @@ __device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* res, const
 template <int HD, int PL>
 __device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, const uint8_t* str, uint32_t accumulate) {
   using C = GradCfg<HD, PL>;
-  constexpr uint32_t id = ptx::idesc_bf16_f32(kRows, HD) | kBMajorMN;
+  constexpr uint32_t id = idesc_f16(kRows, HD) | kBMajorMN;
   uint32_t acc = accumulate;
 #pragma unroll
   for (int pr = 0; pr < (PL == 2 ? 3 : 1); ++pr) {
@@ -591,7 +740,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
     const int q4 = warp & 3, half = warp >> 2, me = 32 * q4 + lane;   // my lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
     const int c0 = half * C::kHalf;                                   // my first column
-    const float sc2 = kLog2e * rsqrtf((float)HD);
+    const Scales sc = load_scales(pl.scale);
+    const float sc2 = ldexpf(kLog2e * rsqrtf((float)HD), -sc.q - sc.k);   // the products' scales leave with it
+    const float f_dp = ldexpf(1.f, sc.dp - sc.o - sc.v);
+    const float scale = rsqrtf((float)HD);
     auto arrive = [&](uint64_t* b) {
       ptx::tc_fence_before();
       __syncwarp();
@@ -648,10 +800,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 x = *reinterpret_cast<const float4*>(delta + c + j);
-            d[j] = p[c + j] * (d[j] - x.x);
-            d[j + 1] = p[c + j + 1] * (d[j + 1] - x.y);
-            d[j + 2] = p[c + j + 2] * (d[j + 2] - x.z);
-            d[j + 3] = p[c + j + 3] * (d[j + 3] - x.w);
+            d[j] = p[c + j] * fmaf(d[j], f_dp, -x.x);
+            d[j + 1] = p[c + j + 1] * fmaf(d[j + 1], f_dp, -x.y);
+            d[j + 2] = p[c + j + 2] * fmaf(d[j + 2], f_dp, -x.z);
+            d[j + 3] = p[c + j + 3] * fmaf(d[j + 3], f_dp, -x.w);
           }
           put_pairs<PL>(tP + c, d);
         }
@@ -661,7 +813,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       // ---- dV and dK of my key, half of the columns each
       if (n > 0) wait(&bars->done, 0);
       if (ok) {
-        const float scale = rsqrtf((float)HD);
+        const int e_v = -kPExp - sc.o, e_k = -kPExp - sc.dp - sc.q;
         constexpr int kCols = HD / 2;
         float* pk = nullptr;
         float* pv = nullptr;
@@ -689,7 +841,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
             ptx::tmem_ld32(tB + lanes + HD + half * kCols + c, k);
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) k[j] *= scale;
+          for (int j = 0; j < 32; ++j) {
+            k[j] = ldexpf(k[j] * scale, e_k);
+            v[j] = ldexpf(v[j], e_v);
+          }
           if (pk) {
             store32(pk + c, k);
             store32(pv + c, v);
@@ -726,7 +881,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           float s[32];
           ptx::tmem_ld32(tS + c, s);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = ex2(fmaf(s[j], sc2, -lse2)) * (d[c + j] - delta);
+          for (int j = 0; j < 32; ++j) s[j] = ex2(fmaf(s[j], sc2, -lse2)) * fmaf(d[c + j], f_dp, -delta);
           if (!all) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -739,7 +894,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       }
       wait(&bars->done, 0);
       if (ok) {
-        const float scale = rsqrtf((float)HD);
+        const int e_q = -kPExp - sc.dp - sc.k;
         constexpr int kCols = HD / 2;
         const int at = tile * pl.per + own;
         T* dst = nullptr;
@@ -751,7 +906,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           float v[32];
           ptx::tmem_ld32(tB + 128 + lanes + half * kCols + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= scale;
+          for (int j = 0; j < 32; ++j) v[j] = ldexpf(v[j] * scale, e_q);
           if (dst) store32(dst + c, v);
         }
       }
@@ -826,17 +981,18 @@ template <typename T, int HD, int PL>
 cudaError_t run_grad(const PackedBwdPlan& pl, const PackedBwdTensors& t, int sms, int* launches, cudaStream_t s) {
   using C = GradCfg<HD, PL>;
   const int rows = pl.T * kRows, ctx = pl.KT * kRows;
-  cudaError_t e = launch_pdl(rank_kernel, dim3((pl.N + 255) / 256), dim3(256), 0, s, pl, t.anchors);
+  cudaError_t e = launch_pdl(range_kernel<T, HD>, dim3((pl.N + kRangeThreads - 1) / kRangeThreads + pl.parts),
+                             dim3(kRangeThreads), 0, s, pl, t);
   if (e != cudaSuccess) return e;
   ++*launches;
   const long long warps = (long long)rows * (pl.nq + pl.nkv) + (long long)ctx * pl.nkv;
-  const int grid = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 64);
+  const int grid = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
   e = launch_pdl(pack_bwd_kernel<T, HD>, dim3(grid), dim3(256), 0, s, pl, t);
   if (e != cudaSuccess) return e;
   ++*launches;
   GradMaps m;
   const int q_rows = pl.nq * PL * rows, b_rows = pl.nkv * PL * rows, c_rows = pl.nkv * PL * std::max(ctx, kRows);
-  auto enc = [&](CUtensorMap* a, CUtensorMap* b, const __nv_bfloat16* p, int n) {
+  auto enc = [&](CUtensorMap* a, CUtensorMap* b, const __half* p, int n) {   // a copy of 16-bit values, whatever they are
     return encode_activation_map(a, p, HD, n, HD, kRows) && encode_activation_map(b, p, HD, n, HD, C::kN);
   };
   if (!enc(&m.q, &m.qs, pl.q, q_rows) || !enc(&m.d_o, &m.d_os, pl.d_o, q_rows) || !enc(&m.kc, &m.kcs, pl.kc, c_rows) ||
@@ -883,17 +1039,20 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   };
   const size_t pe = 2 * (size_t)p.planes;
   p.status = reinterpret_cast<int32_t*>(take(4));
+  p.parts = 2 * sms;
+  p.part = reinterpret_cast<float*>(take(4 * (size_t)p.parts * kRangeValues));
+  p.scale = reinterpret_cast<int32_t*>(take(4 * 5));
   p.order = reinterpret_cast<int32_t*>(take(4 * (size_t)N));
   p.sorted = reinterpret_cast<int32_t*>(take(4 * (size_t)N));
   p.row_anchor = reinterpret_cast<int32_t*>(take(4 * rows));
   p.lse2 = reinterpret_cast<float*>(take(4 * rows * nq));
   p.delta = reinterpret_cast<float*>(take(4 * rows * nq));
-  p.q = reinterpret_cast<__nv_bfloat16*>(take(pe * rows * nq * hd));
-  p.d_o = reinterpret_cast<__nv_bfloat16*>(take(pe * rows * nq * hd));
-  p.kc = reinterpret_cast<__nv_bfloat16*>(take(pe * ctx * nkv * hd));
-  p.vc = reinterpret_cast<__nv_bfloat16*>(take(pe * ctx * nkv * hd));
-  p.kb = reinterpret_cast<__nv_bfloat16*>(take(pe * rows * nkv * hd));
-  p.vb = reinterpret_cast<__nv_bfloat16*>(take(pe * rows * nkv * hd));
+  p.q = reinterpret_cast<__half*>(take(pe * rows * nq * hd));
+  p.d_o = reinterpret_cast<__half*>(take(pe * rows * nq * hd));
+  p.kc = reinterpret_cast<__half*>(take(pe * ctx * nkv * hd));
+  p.vc = reinterpret_cast<__half*>(take(pe * ctx * nkv * hd));
+  p.kb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
+  p.vb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
   const size_t part = 4 * (size_t)nq * p.splits * S * hd;
   p.dk_part = reinterpret_cast<float*>(take(part));
   p.dv_part = reinterpret_cast<float*>(take(part));

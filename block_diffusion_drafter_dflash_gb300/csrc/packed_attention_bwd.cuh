@@ -1,7 +1,7 @@
 // Gradients of the packed training attention (packed_attention_bwd.cu).
 #pragma once
 
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -14,23 +14,26 @@ namespace dflash {
 // tile of 128 rows (`per` of them, then padding).
 struct PackedBwdPlan {
   int N, block, S, nq, nkv, hd;
-  int planes;             // bf16 operand planes: 1 (bf16 tensors) or 2 (fp32 tensors as hi + lo)
+  int planes;             // fp16 operand planes: 1 (bf16 tensors) or 2 (fp32 tensors as hi + lo)
   int per;                // blocks in a row tile
   int T;                  // row tiles
   int KT;                 // 128-key tiles of the context
   int splits;             // CTAs that share one (q head, context key tile)'s row tiles
+  int parts;              // CTAs that look for the operands' ranges
   int32_t* status;
+  float* part;            // [parts][kRangeValues] their maxima
+  int32_t* scale;         // [5] exponents of the powers of two the operands are scaled by (Scales)
   int32_t* order;         // [N] block of each sorted place
   int32_t* sorted;        // [N] anchors in ascending order
   int32_t* row_anchor;    // [T*128] anchor of the row's block (0 in padding)
-  float* lse2;            // [nq][T*128] lse log2(e), +inf in padding
-  float* delta;           // [nq][T*128] sum_d d_out out
-  __nv_bfloat16* q;       // [nq][planes][T*128][hd], zero in padding (d_o, kb and vb too)
-  __nv_bfloat16* d_o;
-  __nv_bfloat16* kc;      // [nkv][planes][KT*128][hd]
-  __nv_bfloat16* vc;
-  __nv_bfloat16* kb;      // [nkv][planes][T*128][hd]
-  __nv_bfloat16* vb;
+  float* lse2;            // [nq][T*128] lse log2(e) - kPExp, +inf in padding
+  float* delta;           // [nq][T*128] sum_d d_out out, scaled as dp
+  __half* q;              // [nq][planes][T*128][hd], zero in padding (d_o, kb and vb too)
+  __half* d_o;
+  __half* kc;             // [nkv][planes][KT*128][hd]
+  __half* vc;
+  __half* kb;             // [nkv][planes][T*128][hd]
+  __half* vb;
   float* dk_part;         // [nq*splits][S][hd] this head's and split's share of d_k_ctx
   float* dv_part;
   size_t bytes;

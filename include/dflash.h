@@ -402,9 +402,9 @@ int32_t dflash_packed_block_attention_lse(const void* q_dev, const void* k_ctx_d
  *               256-byte aligned; its first int32 is the call's status word
  *               (dflash_packed_attention_status)
  * Operands have to be finite: a NaN or an infinity spreads to gradients that
- * do not depend on it.  bf16: products of bf16 operands (P and ds rounded to
- * bf16) summed in fp32; fp32: hi/lo bf16 pairs, fp32-level precision.  The
- * same call gives the same bits on the same device.  n_blocks = 0 zeroes
+ * do not depend on it.  Operands, P and ds enter their products as scaled fp16
+ * (fp32 operands: as hi/lo pairs of it, 22 bits), sums are fp32.  The same
+ * call gives the same bits on the same device.  n_blocks = 0 zeroes
  * d_k_ctx and d_v_ctx.  The forward's limits, and 2^31 rows of laid-out
  * operands.  The workspace size depends on the current device's SM count. */
 size_t dflash_packed_attention_backward_workspace_bytes(int32_t n_blocks, int32_t block, int32_t seq_len,

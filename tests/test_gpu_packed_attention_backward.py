@@ -1,15 +1,18 @@
 """dflash_packed_block_attention_backward (and the forward's lse) against the
 formula in 64 bits, element by element.
 
-Tolerances follow the roundings.  With u the rounding of one operand of a
-product (bf16 operands: 2^-8, exact for q, k, v; fp32 operands as hi/lo pairs:
-3 * 2^-16 with the lo lo product that is left out), a score carries
-es = n_s |q| |k| / sqrt(hd), P the factor es + 2^-20 (e^, lse), dp = dO v the
-error u |dO| |v|, and ds = P (dp - D)
+Tolerances follow the roundings.  Operands, P and ds enter their products as
+scaled fp16: with u the rounding of one of them (bf16 tensors: 2^-11, q, k and v
+being exact; fp32 tensors as hi/lo pairs: 3 * 2^-22 with the lo lo product that
+is left out), a score carries n_s |q| |k| / sqrt(hd), P the factor e^ of that and
+2^-20 (e^, lse), dp = dO v the error u |dO| |v|, and ds = P (dp - D)
   E_ds = E_P |dp - D| + P (E_dp + hd 2^-23 |dO| |O|) + u |ds|.
 dv sums (E_P + 2 u P) |dO|, dq sums E_ds |k|, dk sums E_ds |q| (and u of the other
 operand for fp32), each with n 2^-24 of its sum of absolute terms for n
-additions, and the gradient's own rounding (bf16: 2^-8)."""
+additions, and the gradient's own rounding (bf16: 2^-8).  Scaled values under
+fp16's normal range are good to 2^-38 of their largest: absolute values are
+taken with 2^-16 of the largest added, P with 2^-16, ds with 2^-16 of the norms'
+bound."""
 import math
 
 import pytest
@@ -35,28 +38,32 @@ def tolerances(ops, anchors, d_out, grads, dtype):
     both = lambda x, ctx, blk: torch.cat([torch.einsum("nihd,shd->nihs", x, rep(ctx, 1)),
                                           torch.einsum("nihd,njhd->nihj", x, rep(blk, 2))], dim=-1)
     bf16 = dtype == torch.bfloat16
-    u = 2.0 ** -8 if bf16 else 3 * 2.0 ** -16
+    u = 2.0 ** -11 if bf16 else 3 * 2.0 ** -22
     n_s = hd * 2.0 ** -24 + (0 if bf16 else u)
     w = 0 if bf16 else u                      # of an operand that is exact in bf16
     out, lse, p = forward_reference(*ops, anchors)
-    a = [t.abs() for t in (kc, vc, kb, vb)]
-    e_p = p * (n_s * c * both(q.abs(), a[0], a[2]) + 2.0 ** -20 + 2.0 ** -23 * lse.abs()[..., None])
-    adov = both(d_out.abs(), a[1], a[3])
+    floor = 2.0 ** -16
+    size = lambda *t: max([float(x.abs().max()) for x in t if x.numel()])
+    mag = lambda t, top: t.abs() + floor * top
+    norm = lambda *t: max([float(x.norm(dim=-1).max()) for x in t if x.numel()])
+    a = [mag(t, m) for t, m in ((kc, size(kc, kb)), (vc, size(vc, vb)), (kb, size(kc, kb)), (vb, size(vc, vb)))]
+    aq, x = mag(q, size(q)), mag(d_out, size(d_out))
+    e_p = p * (n_s * c * both(aq, a[0], a[2]) + 2.0 ** -20 + 2.0 ** -23 * lse.abs()[..., None])
+    adov = both(x, a[1], a[3])
     d = (d_out * out).sum(-1, keepdim=True)
     dp = both(d_out, vc, vb)
     ds = p * (dp - d)
     e_dp = (u + hd * 2.0 ** -24) * adov
-    e_ds = e_p * (dp - d).abs() + p * (e_dp + hd * 2.0 ** -23 * (d_out * out).abs().sum(-1, keepdim=True)) + u * ds.abs()
-    e_dv = e_p + 2 * u * p
+    e_ds = e_p * (dp - d).abs() + p * (e_dp + hd * 2.0 ** -23 * (d_out * out).abs().sum(-1, keepdim=True)) + u * mag(ds, norm(d_out) * norm(vc, vb))
+    e_dv = e_p + 2 * u * (p + floor)
     n_q, n_k = (S + g) * 2.0 ** -24, N * g * G * 2.0 ** -24
     ads = (e_ds + (w + n_q) * ds.abs()) * c, (e_ds + (w + n_k) * ds.abs()) * c
     adv = e_dv + n_k * p
-    x = d_out.abs()
     t_q = torch.einsum("nihs,shd->nihd", ads[0][..., :S], rep(a[0], 1)) + torch.einsum("nihj,njhd->nihd", ads[0][..., S:],
                                                                                        rep(a[2], 2))
-    tol = (t_q, fold(torch.einsum("nihs,nihd->shd", ads[1][..., :S], q.abs()), 1),
+    tol = (t_q, fold(torch.einsum("nihs,nihd->shd", ads[1][..., :S], aq), 1),
            fold(torch.einsum("nihs,nihd->shd", adv[..., :S], x), 1),
-           fold(torch.einsum("nihj,nihd->njhd", ads[1][..., S:], q.abs()), 2),
+           fold(torch.einsum("nihj,nihd->njhd", ads[1][..., S:], aq), 2),
            fold(torch.einsum("nihj,nihd->njhd", adv[..., S:], x), 2))
     own = 2.0 ** -8 if bf16 else 2.0 ** -24
     return [t * 1.02 + own * r.abs() * 1.01 + 1e-30 for t, r in zip(tol, grads)]
@@ -155,6 +162,36 @@ def test_same_bits_every_time_other_stream_and_graph():
     other = run(new, anchors[::-1], d_out)[2]
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(other, grads)) and not torch.equal(other[0], first[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_operands_far_from_one(dtype):
+    """Operands and gradients of any size (their squares outside fp32): the gradients scale exactly with them."""
+    S, N, g, nq, nkv, hd = 200, 20, 6, 4, 2, 64
+    anchors = anchors_of(N, S, 8)
+    ops = operands(S, N, g, nq, nkv, hd, dtype, 12, "cuda")
+    d_out = torch.randn(ops[0].shape, device="cuda")
+    want = run(ops, anchors, d_out)[2]
+    for eq, ev, eo in ((40, 70, -90), (-30, -80, 60), (0, 20, -100), (60, 0, 20)):
+        # q 2^eq, k 2^-eq, v 2^ev, d_out 2^eo: the scores stay, every gradient is scaled by a power of two
+        f = [2.0 ** e for e in (eq, -eq, ev, -eq, ev)]
+        scaled = tuple(o * s for o, s in zip(ops, f))
+        df = _df()
+        a = torch.tensor(anchors, dtype=torch.int32, device="cuda")
+        out, lse, _, ws = run(ops, anchors, d_out)
+        grads = [torch.full_like(t, math.nan) for t in ops]
+        df.dflash_packed_block_attention_backward(*scaled, a, out * 2.0 ** ev, lse, d_out * 2.0 ** eo, *grads, ws)
+        for got, w, e in zip(grads, want, (ev + eo - eq, ev + eo + eq, eo, ev + eo + eq, eo)):
+            assert torch.equal(got, w * 2.0 ** e)
+
+
+def test_zero_gradient_and_operands():
+    S, N, g, nq, nkv, hd = 100, 9, 4, 4, 2, 64
+    anchors = anchors_of(N, S, 8)
+    ops = operands(S, N, g, nq, nkv, hd, torch.bfloat16, 12, "cuda")
+    for z in (ops, tuple(torch.zeros_like(o) for o in ops)):
+        grads = run(z, anchors, torch.zeros(ops[0].shape, device="cuda"))[2]
+        assert all(bool((t == 0).all()) for t in grads)
 
 
 def test_anchors_outside_the_sequence_are_clamped_and_flagged():
