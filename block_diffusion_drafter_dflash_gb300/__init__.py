@@ -10,6 +10,7 @@ library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional
 
 import torch
@@ -410,7 +411,7 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.T
     """Address of a contiguous tensor of n values on the device of `like` (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or t.device != like.device or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != like.get_device() or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {like.device}")
     return t.data_ptr()
 
@@ -418,7 +419,7 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.T
 def _on_current_device(t: torch.Tensor) -> None:
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
 
 
@@ -468,6 +469,9 @@ def dflash_token_logprobs_backward(logits: torch.Tensor, tokens: Optional[torch.
         _stream_ptr(stream)), "dflash_token_logprobs_backward")
 
 
+_CLIP_DTYPES = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}
+
+
 def _scratch(nbytes: int, stream=None) -> torch.Tensor:
     """Device scratch of the caching allocator, ordered with the stream the call runs on."""
     with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
@@ -490,33 +494,26 @@ def dflash_clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None,
     that is not finite leaves the gradients as they are; max_norm = inf
     computes the norm alone."""
     _on_current_device(norm)
-    n, dev = len(grads), norm.device
-    ptrs, dtypes, numels = [0] * n, [0] * n, [0] * n
-    outs = None if out is None else [0] * n
-    if out is not None and len(out) != n:
-        raise ValueError("out must have one tensor for each of grads")
-    for i, g in enumerate(grads):
-        dt = g.dtype
-        if dt is torch.bfloat16:
-            dtypes[i] = _abi.DTYPE_BF16
-        elif dt is not torch.float32:
-            raise ValueError("gradients must be float32 or bfloat16")
-        if g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous tensors on the norm's device")
-        ptrs[i] = g.data_ptr()
-        numels[i] = g.numel()
-        if outs is not None:
-            o = out[i]
-            if o.dtype is not dt or o.numel() != numels[i] or o.device != dev or not o.is_contiguous():
-                raise ValueError("out tensors must be contiguous, of the gradients' types and sizes")
-            outs[i] = o.data_ptr()
+    n = len(grads)
+    tensors = [*grads] if out is None else [*grads, *out]
+    dtypes = [t.dtype for t in tensors]
+    numels = list(map(torch.Tensor.numel, tensors))
+    if n and (not all(map(torch.Tensor.is_contiguous, tensors)) or
+              set(map(torch.Tensor.get_device, tensors)) != {norm.get_device()}):
+        raise ValueError("gradients must be contiguous tensors on the norm's device")
+    if out is not None and (len(out) != n or dtypes[:n] != dtypes[n:] or numels[:n] != numels[n:]):
+        raise ValueError("out must have one tensor for each of grads, of its type and size")
+    if not _CLIP_DTYPES.keys() >= set(dtypes):
+        raise ValueError("gradients must be float32 or bfloat16")
+    ptrs = array("Q", map(torch.Tensor.data_ptr, tensors))
+    sizes, types = array("q", numels[:n]), array("i", [_CLIP_DTYPES[t] for t in dtypes[:n]])
+    at = ptrs.buffer_info()[0]
     if workspace is None:
         workspace = _scratch(int(lib().dflash_clip_workspace_bytes()), stream)
-    ptr_array = ctypes.c_void_p * n
     check(lib().dflash_clip_grad_norm(
-        ptr_array(*ptrs), None if outs is None else ptr_array(*outs), (ctypes.c_int64 * n)(*numels),
-        (ctypes.c_int32 * n)(*dtypes), n, float(max_norm), _vector(norm, 1, torch.float32, norm, "norm"),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "dflash_clip_grad_norm")
+        at, None if out is None else at + 8 * n, sizes.buffer_info()[0], types.buffer_info()[0], n, float(max_norm),
+        _vector(norm, 1, torch.float32, norm, "norm"), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream)), "dflash_clip_grad_norm")
 
 
 class BlockPolicy:

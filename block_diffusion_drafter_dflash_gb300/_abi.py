@@ -98,8 +98,7 @@ SIGNATURES = {
     "dflash_token_logprobs_backward": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_i32, c_i32, ctypes.c_float, c_ptr,
                                                c_ptr, c_ptr, c_ptr, c_ptr, ctypes.c_int64, c_ptr]),
     "dflash_clip_workspace_bytes": (c_size, []),
-    "dflash_clip_grad_norm": (c_i32, [ctypes.POINTER(c_ptr), ctypes.POINTER(c_ptr), ctypes.POINTER(ctypes.c_int64),
-                                      c_i32p, c_i32, ctypes.c_float, c_ptr, c_ptr, c_size, c_ptr]),
+    "dflash_clip_grad_norm": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_i32, ctypes.c_float, c_ptr, c_ptr, c_size, c_ptr]),
     "dflash_launch_count": (ctypes.c_uint64, []),
     "dflash_synthetic_target": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_i32, c_ptr, c_ptr, c_ptr, c_i32, c_i32, c_i32,
                                         c_ptr, c_ptr]),

@@ -34,7 +34,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                          // vectors of a thread and chunk
 constexpr int kChunkVec = kThreads * kVec;       // 32 KB
-constexpr int kMaxTensors = 512;                 // 16 KB of launch parameters
+// Tensors a launch's parameters hold: 2 KB or 16 KB of them
+constexpr int kFewTensors = 64, kMaxTensors = 512;
 constexpr int kCtasPerSm = 4;
 
 struct Entry {
@@ -43,14 +44,17 @@ struct Entry {
   long long numel;
   long long first;   // number of its first chunk, shifted left by one, plus 1 if bf16
 };
+template <int MAX>
 struct Table {
+  static constexpr int kMax = MAX;
   int n;
   long long chunks;
-  Entry e[kMaxTensors];
+  Entry e[MAX];
 };
 
 // Entry holding chunk c.
-__device__ __forceinline__ int find_entry(const Table& t, long long c) {
+template <class Tab>
+__device__ __forceinline__ int find_entry(const Tab& t, long long c) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -136,7 +140,8 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
 }
 
 // partial[cta] (+)= the squares of this launch's chunks cta, cta + grid, ...
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_square_sum_kernel(const __grid_constant__ Table t,
+template <class Tab>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_square_sum_kernel(const __grid_constant__ Tab t,
                                                                               double* partial, int accumulate) {
   griddep_wait();
   griddep_trigger();
@@ -168,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_square_sum_kernel(c
 
 // Every CTA adds the partial sums of all (in the same order), then scales its
 // chunks, the list's last ones first.
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const __grid_constant__ Table t,
+template <class Tab>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const __grid_constant__ Tab t,
                                                                          const double* partial, int partials,
                                                                          float max_norm, float* norm_out,
                                                                          int in_place) {
@@ -230,11 +236,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
   }
 }
 
-// The next up to kMaxTensors tensors from t[at], empty ones left out.
-int fill(Table& tab, const ClipTensor* t, int n, int at) {
+// The next tensors from t[at] that the table holds, empty ones left out.
+template <class Tab>
+int fill(Tab& tab, const ClipTensor* t, int n, int at) {
   tab.n = 0;
   tab.chunks = 0;
-  for (; at < n && tab.n < kMaxTensors; ++at) {
+  for (; at < n && tab.n < Tab::kMax; ++at) {
     if (t[at].numel == 0) continue;
     const long long bytes = t[at].numel * (t[at].bf16 ? 2 : 4) + (long long)(reinterpret_cast<uintptr_t>(t[at].in) & 15);
     Entry& e = tab.e[tab.n++];
@@ -247,6 +254,37 @@ int fill(Table& tab, const ClipTensor* t, int n, int at) {
   return at;
 }
 
+template <class Tab>
+cudaError_t run(const ClipTensor* t, int n, float max_norm, float* norm, double* partial, int full, int* launches,
+                cudaStream_t s) {
+  const bool many = n > Tab::kMax;   // several launches, each adding to the same CTAs' sums
+  int in_place = 1;
+  for (int i = 0; i < n; ++i)
+    if (t[i].numel && t[i].in != t[i].out) in_place = 0;
+  Tab tab;
+  auto grid_of = [&] { return (int)(tab.chunks < full ? (tab.chunks > 0 ? tab.chunks : 1) : full); };
+  int at = 0, partials = 0;
+  for (bool first = true; first || at < n; first = false) {
+    at = fill(tab, t, n, at);
+    partials = many ? full : grid_of();
+    cudaError_t e = launch_pdl(grad_square_sum_kernel<Tab>, dim3(partials), dim3(kThreads), 0, s, tab, partial,
+                               first ? 0 : 1);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  // the norm alone: no gradient can exceed an infinite limit
+  const bool norm_only = in_place && std::isinf(max_norm);
+  at = 0;
+  for (bool first = true; first || (at < n && !norm_only); first = false) {
+    at = many ? fill(tab, t, n, at) : n;   // one table still holds them all
+    cudaError_t e = launch_pdl(grad_scale_kernel<Tab>, dim3(norm_only ? 1 : grid_of()), dim3(kThreads), 0, s, tab,
+                               static_cast<const double*>(partial), partials, max_norm, first ? norm : nullptr, in_place);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 int clip_grid(int sms) { return sms * kCtasPerSm; }
@@ -254,39 +292,10 @@ size_t clip_workspace_bytes(int sms) { return sizeof(double) * (size_t)clip_grid
 
 cudaError_t clip_grad_norm_launch(const ClipTensor* t, int n, float max_norm, float* norm, void* ws, int sms,
                                   int* launches, cudaStream_t s) {
-  double* partial = static_cast<double*>(ws);
-  const int full = clip_grid(sms);
   *launches = 0;
-  int in_place = 1;
-  for (int i = 0; i < n; ++i)
-    if (t[i].numel && t[i].in != t[i].out) in_place = 0;
-  Table tab;
-  int at = 0, grid0 = 0;
-  for (bool first = true; first || at < n; first = false) {
-    at = fill(tab, t, n, at);
-    // the first launch's CTAs hold a partial sum each; later ones add to the same
-    int grid = (int)(tab.chunks < full ? (tab.chunks > 0 ? tab.chunks : 1) : full);
-    if (first) grid0 = n > kMaxTensors ? full : grid;
-    if (n > kMaxTensors) grid = full;
-    cudaError_t e = launch_pdl(grad_square_sum_kernel, dim3(grid), dim3(kThreads), 0, s, tab, partial, first ? 0 : 1);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-  }
-  // the norm alone: no gradient can exceed an infinite limit
-  const bool norm_only = in_place && std::isinf(max_norm);
-  int done = 0;
-  at = 0;
-  for (bool first = true; first || (at < n && !norm_only); first = false) {
-    at = fill(tab, t, n, at);
-    const int grid = norm_only ? 1 : (int)(tab.chunks < full ? (tab.chunks > 0 ? tab.chunks : 1) : full);
-    cudaError_t e = launch_pdl(grad_scale_kernel, dim3(grid), dim3(kThreads), 0, s, tab,
-                               static_cast<const double*>(partial), grid0, max_norm, done == 0 ? norm : nullptr,
-                               in_place);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-    ++done;
-  }
-  return cudaSuccess;
+  double* partial = static_cast<double*>(ws);
+  return n <= kFewTensors ? run<Table<kFewTensors>>(t, n, max_norm, norm, partial, clip_grid(sms), launches, s)
+                          : run<Table<kMaxTensors>>(t, n, max_norm, norm, partial, clip_grid(sms), launches, s);
 }
 
 }  // namespace dflash

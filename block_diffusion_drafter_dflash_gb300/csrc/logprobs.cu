@@ -20,14 +20,17 @@
 // of terms of one sign, so nothing cancels.
 //
 // Top k.  Each warp keeps its k largest (value, id) keys sorted over its
-// lanes.  A batch of loaded logits enters only where its maximum beats the
-// warp's k-th value, which is rare once the list is warm, so a logit costs
-// nothing beyond the maximum that the softmax needs anyway.  Lists are merged
-// in pairs (elementwise maximum of one list with the other reversed, then a
-// bitonic merge).
+// lanes.  After the first batch of loads the CTA sorts its threads' maxima: the
+// k-th of them, a value that k logits are known to reach, is the bar that the
+// rest has to reach (with 4096 logits or more behind it hardly more than k
+// pass).  A batch whose maximum is below the bar costs the top k nothing beyond
+// that maximum, which the softmax needs anyway.  Lists are merged in pairs
+// (elementwise maximum of one list with the other reversed, then a bitonic
+// merge).
 #include <cooperative_groups.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "logprobs.cuh"
@@ -45,6 +48,33 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // ---------------------------------------------------------------- 16-byte vectors of a row
@@ -69,19 +99,32 @@ __device__ __forceinline__ void unpack(uint4 r, float* x, __nv_bfloat16) {
   }
 }
 
+// The largest of a vector's values (NaN aside).
+__device__ __forceinline__ float vec_max(uint4 r, float) {
+  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+__device__ __forceinline__ float vec_max(uint4 r, __nv_bfloat16) {
+  auto as2 = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
+  const float2 m = __bfloat1622float2(__hmax2(__hmax2(as2(r.x), as2(r.y)), __hmax2(as2(r.z), as2(r.w))));
+  return fmaxf(m.x, m.y);
+}
+
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // Vector i of the row at `row` (V elements, misalignment mis); elements
 // outside the row are -inf and are not read.
 template <typename T>
 __device__ __forceinline__ uint4 load_vec(const T* row, int V, int mis, int i) {
   constexpr int E = Vec<T>::kE;
   const int u0 = i * E - mis;
-  if (u0 >= 0 && u0 + E <= V) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(row + u0));
-    return r;
-  }
+  if (u0 >= 0 && u0 + E <= V) return load16(row + u0);
   uint32_t w[4];
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -140,15 +183,17 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
 }
 
-// Sorted list of a warp: lane i holds the i-th largest key.  thr is the key
-// of lane k-1, thr_x its value; full: that entry exists.
+// Sorted list of a warp: lane i holds the i-th largest key.  A key enters when
+// it is larger than thr: the bar, then the list's k-th key once there are k.
 struct TopList {
   unsigned long long key, thr;
-  float thr_x;
 };
-__device__ __forceinline__ void set_threshold(TopList& l, int k) {
-  l.thr = __shfl_sync(kAll, l.key, k - 1);
-  l.thr_x = l.thr ? key_value(l.thr) : -INFINITY;
+// Whether a batch with maximum m may hold a key above thr: a tie with the bar
+// does (its id part is 0), one with a listed key does not (later batches hold
+// higher ids).
+__device__ __forceinline__ bool reaches(float m, unsigned long long thr) {
+  const float x = thr ? key_value(thr) : -INFINITY;
+  return static_cast<unsigned>(thr) == 0 ? m >= x : m > x;
 }
 // Take `key` (the same in every lane) into the list.
 __device__ __forceinline__ void insert(TopList& l, unsigned long long key, int k) {
@@ -157,7 +202,8 @@ __device__ __forceinline__ void insert(TopList& l, unsigned long long key, int k
   const unsigned long long up = __shfl_up_sync(kAll, l.key, 1);
   if (lane == at) l.key = key;
   if (lane > at) l.key = up;
-  set_threshold(l, k);
+  const unsigned long long kth = __shfl_sync(kAll, l.key, k - 1);
+  if (kth > l.thr) l.thr = kth;
 }
 // Every lane's candidate that beats the threshold.
 __device__ __forceinline__ void offer(TopList& l, unsigned long long key, int k) {
@@ -167,6 +213,30 @@ __device__ __forceinline__ void offer(TopList& l, unsigned long long key, int k)
     if (c > l.thr) insert(l, c, k);
     todo &= todo - 1;
   }
+}
+// The lanes' values in descending order.
+__device__ __forceinline__ float sort_desc(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int o = k >> 1; o; o >>= 1) {
+      const float w = __shfl_xor_sync(kAll, v, o);
+      const bool larger = ((lane & o) == 0) == ((lane & k) == 0 || k == 32);   // this lane keeps the larger
+      v = larger ? fmaxf(v, w) : fminf(v, w);
+    }
+  return v;
+}
+// The 32 largest of two descending lists of values, descending.
+__device__ __forceinline__ float merge_values(float a, float b) {
+  const int lane = threadIdx.x & 31;
+  float v = fmaxf(a, __shfl_sync(kAll, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float w = __shfl_xor_sync(kAll, v, o);
+    v = (lane & o) ? fminf(v, w) : fmaxf(v, w);
+  }
+  return v;
 }
 // The 32 largest of two sorted lists, sorted.
 __device__ __forceinline__ unsigned long long merge_lists(unsigned long long a, unsigned long long b) {
@@ -182,17 +252,15 @@ __device__ __forceinline__ unsigned long long merge_lists(unsigned long long a, 
 }
 
 // ---------------------------------------------------------------- forward
-constexpr int kFwdThreads = 256;
-constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kFwdVec = 4;         // vectors a thread loads before it uses any (64 bytes)
 constexpr int kMaxCluster = 8;     // the portable cluster size
 
-// grid (C, rows) with clusters of (C, 1, 1): one row a cluster.
-template <typename T, bool TOPK>
-__global__ void __launch_bounds__(kFwdThreads) token_logprobs_kernel(LogprobArgs a, float scale2, float inv_t) {
+// grid (C, rows) with clusters of (C, 1, 1): one row a cluster, NT threads a CTA.
+template <typename T, bool TOPK, int NT>
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(LogprobArgs a, float scale2, float inv_t) {
   griddep_wait();
   griddep_trigger();
-  constexpr int E = Vec<T>::kE;
+  constexpr int E = Vec<T>::kE, kWarps = NT / 32;
   const int C = gridDim.x, part = blockIdx.x, row = blockIdx.y, V = a.vocab, k = a.top_k;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* x = static_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
@@ -203,8 +271,9 @@ __global__ void __launch_bounds__(kFwdThreads) token_logprobs_kernel(LogprobArgs
   cg::cluster_group cluster = cg::this_cluster();
   if (C > 1) cluster.barrier_arrive();   // the first CTA's shared memory is there once every CTA has started
 
-  __shared__ Stats s_stats[kFwdWarps];                               // the CTA's warps
-  __shared__ unsigned long long s_list[TOPK ? kFwdWarps : 1][32];
+  __shared__ Stats s_stats[kWarps];                                  // the CTA's warps
+  __shared__ unsigned long long s_list[TOPK ? kWarps : 1][32];
+  __shared__ float s_max[TOPK ? kWarps : 1][32];
   __shared__ Stats c_stats[kMaxCluster];                             // the cluster's CTAs (first CTA's copy)
   __shared__ unsigned long long c_list[TOPK ? kMaxCluster : 1][32];
 
@@ -217,45 +286,74 @@ __global__ void __launch_bounds__(kFwdThreads) token_logprobs_kernel(LogprobArgs
   }
 
   Stats st{-INFINITY, 0.f, 0.f};
-  TopList top{0, 0, -INFINITY};
-  for (int base = i0; base < i1; base += kFwdThreads * kFwdVec) {
-    uint4 r[kFwdVec];
+  TopList top{0, 0};
+  const uint64_t scale_pair = pack2(scale2, scale2);
+  // vectors [full0, full1) of mine lie wholly in the row
+  const int full0 = mis ? 1 : 0, full1 = min(i1, (V + mis) / E);
+  auto load_batch = [&](int base, uint4* r) {
+    if (base >= full0 && base + NT * kFwdVec <= full1) {
+      const T* p = x + (ptrdiff_t)(base + tid) * E - mis;
 #pragma unroll
-    for (int j = 0; j < kFwdVec; ++j) {
-      const int i = base + tid + j * kFwdThreads;
-      if (i < i1)
-        r[j] = load_vec(x, V, mis, i);
-      else
-        r[j] = sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
-                              : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-    }
-    float bm = -INFINITY;
+      for (int j = 0; j < kFwdVec; ++j) r[j] = load16(p + j * NT * E);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kFwdVec; ++j) {
-      float v[E];
-      unpack(r[j], v, T());
-#pragma unroll
-      for (int e = 0; e < E; ++e) bm = fmaxf(bm, v[e]);
-    }
-    if (bm > st.m) st = rescaled(st, bm, scale2);
-    const float m = st.m == -INFINITY ? 0.f : st.m;   // nothing yet: every e is 0
-#pragma unroll
-    for (int j = 0; j < kFwdVec; ++j) {
-      float v[E];
-      unpack(r[j], v, T());
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float w = (v[e] - m) * scale2, p = ex2(w);
-        st.s += p;
-        st.t = fmaf(p, fmaxf(w, -1.0e4f), st.t);   // 0 where p is 0, -inf included
+      for (int j = 0; j < kFwdVec; ++j) {
+        const int i = base + tid + j * NT;
+        if (i < i1)
+          r[j] = load_vec(x, V, mis, i);
+        else
+          r[j] = sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
+                                : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
       }
     }
+  };
+  uint4 next[kFwdVec];
+  load_batch(i0, next);
+  for (int base = i0; base < i1; base += NT * kFwdVec) {
+    uint4 r[kFwdVec];
+#pragma unroll
+    for (int j = 0; j < kFwdVec; ++j) r[j] = next[j];
+    if (base + NT * kFwdVec < i1) load_batch(base + NT * kFwdVec, next);   // in flight while this one is used
+    float bm = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kFwdVec; ++j) bm = fmaxf(bm, vec_max(r[j], T()));
+    if (bm > st.m) st = rescaled(st, bm, scale2);
+    const float m = st.m == -INFINITY ? 0.f : st.m;   // nothing yet: every e is 0
+    const uint64_t minus_m = pack2(-m, -m);
+    uint64_t sum = 0, dot = 0;                        // pairs of zeros
+#pragma unroll
+    for (int j = 0; j < kFwdVec; ++j) {
+      float v[E];
+      unpack(r[j], v, T());
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 w = unpack2(mul2(add2(pack2(v[e], v[e + 1]), minus_m), scale_pair));
+        const uint64_t p = pack2(ex2(w.x), ex2(w.y));
+        sum = add2(sum, p);
+        dot = fma2(p, pack2(fmaxf(w.x, -1.0e4f), fmaxf(w.y, -1.0e4f)), dot);   // 0 where p is 0, -inf included
+      }
+    }
+    const float2 ds = unpack2(sum), dt = unpack2(dot);
+    st.s += ds.x + ds.y;
+    st.t += dt.x + dt.y;
     if constexpr (TOPK) {
-      // later batches hold higher ids, so a tie with the threshold loses
-      if (__any_sync(kAll, bm > top.thr_x || top.thr == 0)) {
+      if (base == i0) {   // the bar: the k-th of the threads' maxima
+        s_max[warp][lane] = sort_desc(bm);
+        __syncthreads();
+#pragma unroll
+        for (int half = kWarps / 2; half; half >>= 1) {
+          if (warp < half) s_max[warp][lane] = merge_values(s_max[warp][lane], s_max[warp + half][lane]);
+          __syncthreads();
+        }
+        const float bar = s_max[0][k - 1];
+        // below -inf's key nothing is a logit (0: no bar, where fewer than k threads hold one)
+        top.thr = bar == -INFINITY ? 0 : make_key(bar, -1) & 0xffffffff00000000ull;
+      }
+      if (__any_sync(kAll, reaches(bm, top.thr))) {
 #pragma unroll
         for (int j = 0; j < kFwdVec; ++j) {
-          const int i = base + tid + j * kFwdThreads;
+          if (!__any_sync(kAll, reaches(vec_max(r[j], T()), top.thr))) continue;
+          const int i = base + tid + j * NT;
           float v[E];
           unpack(r[j], v, T());
 #pragma unroll
@@ -275,13 +373,13 @@ __global__ void __launch_bounds__(kFwdThreads) token_logprobs_kernel(LogprobArgs
   __syncthreads();
   if constexpr (TOPK) {
 #pragma unroll
-    for (int half = kFwdWarps / 2; half; half >>= 1) {
+    for (int half = kWarps / 2; half; half >>= 1) {
       if (warp < half) s_list[warp][lane] = merge_lists(s_list[warp][lane], s_list[warp + half][lane]);
       __syncthreads();
     }
   }
   if (warp == 0) {
-    st = lane < kFwdWarps ? s_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
+    st = lane < kWarps ? s_stats[lane] : Stats{-INFINITY, 0.f, 0.f};
     st = warp_merged(st, scale2);
   }
   if (C > 1) {
@@ -328,11 +426,11 @@ __global__ void __launch_bounds__(kFwdThreads) token_logprobs_kernel(LogprobArgs
   }
 }
 
-template <typename T, bool TOPK>
+template <typename T, bool TOPK, int NT>
 cudaError_t launch_fwd(const LogprobArgs& a, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster, a.rows);
-  cfg.blockDim = dim3(kFwdThreads);
+  cfg.blockDim = dim3(NT);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -343,7 +441,7 @@ cudaError_t launch_fwd(const LogprobArgs& a, int cluster, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOPK>, a, kLog2e / a.temperature, 1.f / a.temperature);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOPK, NT>, a, kLog2e / a.temperature, 1.f / a.temperature);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -452,14 +550,21 @@ cudaError_t launch_bwd(const LogprobGradArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t token_logprobs_launch(const LogprobArgs& a, bool bf16, int sms, cudaStream_t s) {
-  // enough CTAs to fill the GPU a few times over, as far as clusters go
+  // enough CTAs to fill the GPU a few times over, as far as clusters go, and
+  // at least one vector a thread
   int cluster = 1;
-  while (cluster < kMaxCluster && (long long)a.rows * cluster < 8LL * sms) cluster *= 2;
+  while (cluster < kMaxCluster && (long long)a.rows * cluster < 2LL * sms) cluster *= 2;
   const int nvec = a.vocab / (bf16 ? 8 : 4);
-  while (cluster > 1 && nvec < cluster * kFwdThreads) cluster /= 2;   // at least one vector a thread
-  if (bf16)
-    return a.top_k ? launch_fwd<__nv_bfloat16, true>(a, cluster, s) : launch_fwd<__nv_bfloat16, false>(a, cluster, s);
-  return a.top_k ? launch_fwd<float, true>(a, cluster, s) : launch_fwd<float, false>(a, cluster, s);
+  while (cluster > 1 && nvec < cluster * 256) cluster /= 2;
+  // a few rows, each over all CTAs of a cluster: twice the threads
+  const bool wide = cluster == kMaxCluster && (long long)a.rows * cluster < 2LL * sms && nvec >= cluster * 512;
+  auto launch = [&](auto t, auto topk) {
+    using T = decltype(t);
+    constexpr bool K = decltype(topk)::value;
+    return wide ? launch_fwd<T, K, 512>(a, cluster, s) : launch_fwd<T, K, 256>(a, cluster, s);
+  };
+  if (bf16) return a.top_k ? launch(__nv_bfloat16(), std::true_type()) : launch(__nv_bfloat16(), std::false_type());
+  return a.top_k ? launch(float(), std::true_type()) : launch(float(), std::false_type());
 }
 
 cudaError_t token_logprobs_backward_launch(const LogprobGradArgs& a, bool bf16, cudaStream_t s) {
