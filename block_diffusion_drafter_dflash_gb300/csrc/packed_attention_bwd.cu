@@ -16,20 +16,21 @@
 // block's own keys are the same places of the row tile's own key tile.
 //
 // One launch does the work, every CTA one of three kinds of item:
-//   context keys  (q head, 128 keys, split): for each row tile that sees them
-//                 S' = K Q', dP' = V dO'  (keys on the tensor-memory lanes),
-//                 dV += P' dO, dK += dS' Q, with P' and dS' written back to tensor
-//                 memory as the A operand; its share goes to memory as fp32 and a
-//                 last kernel adds the shares of heads and splits in order;
+//   context keys  (kv head, 128 keys, share): for each row tile that sees them,
+//                 of every head in turn, S' = K Q', dP' = V dO' (keys on the
+//                 tensor-memory lanes), dV += P' dO, dK += dS' Q, with P' and dS'
+//                 written back to tensor memory as the A operand; where several
+//                 CTAs share a key tile's work their sums go to memory as fp32 and
+//                 a last kernel adds them in order;
 //   rows          (q head, 128 rows): for each key tile S = Q K', dP = dO V',
 //                 dQ += dS K;
-//   own keys      (kv head, row tile): as context keys, over the G heads.
+//   own keys      (kv head, row tile): as context keys, over the tile's own rows.
 // S and dP are thus computed twice (7 products instead of 5), and nothing is
 // accumulated with atomics: the results do not change from run to run.
 //
-// In a CTA one thread loads tiles by TMA, one issues the MMAs, and eight warps
+// In a CTA one thread loads tiles by TMA, one issues the MMAs, and sixteen warps
 // turn S and dP into P and dS.  The MMA thread alternates so that the tensor
-// cores work on the other product while the eight warps work on one:
+// cores work on the other product while the warps work on one:
 //   keys:  dV(i) S(i+1) | dK(i) dP(i+1)      rows:  S(i+1) dP(i+1) dQ(i)
 // Each operand tile is staged once and read in both directions: K-major for S and
 // dP, MN-major as the B operand of the gradients.
@@ -355,46 +356,116 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
 }
 
 // ---------------------------------------------------------------- tensor-core pieces
-// Instruction descriptor, kind::f16: fp16 A and B, fp32 D, M x N (formats of
-// A and B zero; both K-major).
+// Shared-memory descriptors (128-byte swizzle, tiles of rows of 64 fp16): the
+// low word holds the address, which a step through the tile is added to, the
+// high word is the same for all: 8 rows are 1024 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// K-major: a row's values run along K.
+__device__ __forceinline__ uint32_t desc_k(const void* tile) { return (ptx::smem_u32(tile) >> 4) | (1u << 16); }
+// MN-major: a row's 64 values run along N, the rows along K; lbo: bytes to the
+// tile of the next 64 values.
+__device__ __forceinline__ uint32_t desc_mn(const void* tile, uint32_t lbo) {
+  return (ptx::smem_u32(tile) >> 4) | ((lbo >> 4) << 16);
+}
+// Instruction descriptor, kind::f16: fp16 A and B (formats zero), fp32 D, M x N, both K-major.
 constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] B[smem], fp16 in, fp32 out: A's rows on the lanes, two
-// consecutive K values to a 32-bit column.
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// A tile of rows of 64 fp16 (128-byte swizzle) as an MN-major operand: the 64
-// values of a row run along N, the rows along K.  lbo: bytes to the tile of the
-// next 64 values; 8 rows are 1024 bytes.
-__device__ __forceinline__ uint64_t smem_desc_mn(const void* tile, int lbo) {
-  const uint64_t addr = ptx::smem_u32(tile);
-  return ((addr >> 4) & 0x3FFFull) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-         (2ull << 61);
-}
-constexpr uint32_t kBMajorMN = 1u << 16;   // instruction descriptor: B is MN-major
+constexpr uint32_t kBMajorMN = 1u << 16;
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+// D[tmem] (+)= A[smem] B[smem]'
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]: A's rows on the lanes, two consecutive K values
+// to a 32-bit column.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// C (16 or 32) consecutive columns of this warp's lanes; tmem_ld_wait before use.
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  if constexpr (C == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The values of a load, tied to the wait so that no use moves before it.
+template <int C>
+__device__ __forceinline__ void tmem_values(const uint32_t* r, float* v) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    uint32_t x = r[i];
+    asm volatile("" : "+r"(x));
+    v[i] = __uint_as_float(x);
+  }
+}
+template <int C>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* v) {
+  if constexpr (C == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  }
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Box (x = column, y = row) of a tensor map into shared memory.  No cache
+// hint: the operands are read again and again, but exceed what L2 can keep.
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                   ptx::smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    ptx::smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
                : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -402,15 +473,30 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two fp32 values at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
 
-// 32 values as 16 columns of fp16 pairs from column `at` on and, with two
-// planes, their rounding residuals in the next 16: the 32 columns that the
+// C values as C / 2 columns of fp16 pairs from column `at` on and, with two
+// planes, their rounding residuals in the next C / 2: the C columns that the
 // values were read from.
-template <int PL>
+template <int PL, int C>
 __device__ __forceinline__ void put_pairs(uint32_t at, const float* v) {
-  uint32_t h[16], l[16];
+  uint32_t h[C / 2], l[C / 2];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < C / 2; ++j) {
     __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
     h[j] = *reinterpret_cast<uint32_t*>(&b);
     if (PL == 2) {
@@ -419,81 +505,81 @@ __device__ __forceinline__ void put_pairs(uint32_t at, const float* v) {
       l[j] = *reinterpret_cast<uint32_t*>(&r);
     }
   }
-  tmem_st16(at, h);
-  if (PL == 2) tmem_st16(at + 16, l);
+  tmem_st<C / 2>(at, h);
+  if (PL == 2) tmem_st<C / 2>(at + C / 2, l);
 }
 
 // ---------------------------------------------------------------- the gradient kernel
-// Warps 0..7 softmax (warp w: lanes 32 (w % 4), columns of half w / 4), warp 8
-// loads, warp 9 issues the MMAs.
-constexpr int kSoftWarps = 8;
+// Warps 0..15 softmax (warp w: lanes 32 (w % 4), a quarter of the columns w / 4),
+// warp 16 loads, warp 17 issues the MMAs.
+constexpr int kSoftWarps = 16;
 constexpr int kGradThreads = 32 * (kSoftWarps + 2);
 
+// Two streams of tiles pass the resident operands: the first feeds S and dK
+// (or dQ), the second dP and dV.  The first one's tiles are needed soonest and
+// freed last, so it has one stage more.
 template <int HD, int PL>
 struct GradCfg {
   static constexpr int kSub = HD / 64;
-  // N of a streamed tile and the stages that fit beside the resident operands
-  static constexpr int kN = PL == 2 && HD == 128 ? 64 : 128;
-  static constexpr int kStages = PL == 2 && HD == 128 ? 1 : 2;
+  static constexpr int kN = PL == 2 && HD == 128 ? 64 : 128;   // rows of a streamed tile
+  static constexpr int kS0 = PL == 2 && HD == 128 ? 2 : 3;
+  static constexpr int kS1 = kS0 - 1;
   static constexpr int kResTile = kRows * 128;             // 128 rows x 64 values
   static constexpr int kRes = PL * kSub * kResTile;        // one resident operand
   static constexpr int kStrTile = kN * 128;
-  static constexpr int kStr = PL * kSub * kStrTile;        // one streamed operand
-  static constexpr int kStat = 3 * kN * 4;                 // lse2, delta, anchors of a stage's rows
-  static constexpr int kOffStr = 2 * kRes;
-  static constexpr int kOffStat = kOffStr + kStages * 2 * kStr;
-  static constexpr int kOffBars = kOffStat + kStages * kStat;
-  static constexpr int kUsed = 1024 + kOffBars + 256;
+  static constexpr int kStr = PL * kSub * kStrTile;        // one streamed tile
+  static constexpr int kStat = kN * 4;                     // lse2 with the first stream, delta with the second
+  static constexpr int kOff0 = 2 * kRes;
+  static constexpr int kOff1 = kOff0 + kS0 * kStr;
+  static constexpr int kOffStat = kOff1 + kS1 * kStr;
+  static constexpr int kOffBars = kOffStat + (kS0 + kS1) * kStat;
+  static constexpr int kUsed = kOffBars + 256;
   // more than half of an SM's shared memory: the CTA takes all of tensor memory
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-  static constexpr int kHalf = kN / 2;                     // columns of S of one softmax warp
+  static constexpr int kCols = kN / 4;                     // columns of S of one softmax warp
+  static constexpr int kPitch = HD * 4 + 16;               // fp32 rows staged on their way out: no bank conflicts
   static constexpr uint32_t kTmem = 512;
+  static_assert(kBytes <= 227 * 1024 && 2 * kRows * kPitch <= kOffBars, "shared memory");
 };
 
 struct GradBars {
-  uint64_t res_full, full[2], freed[2], s_full, dp_full, p_ready, ds_ready, done;
+  uint64_t res_full, full0[3], freed0[3], full1[2], freed1[2], s_full, dp_full, p_ready, ds_ready, done;
   uint32_t tmem;
 };
 
 struct GradMaps {
-  CUtensorMap q, d_o, kc, vc, kb, vb;   // boxes of 64 values x 128 rows
+  CUtensorMap q, d_o, kc, vc, kb, vb;         // boxes of 64 values x 128 rows (resident)
   CUtensorMap qs, d_os, kcs, vcs, kbs, vbs;   // x kN rows (streamed)
 };
 
-template <typename T>
-__device__ __forceinline__ void store32(T* dst, const float* v) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 b = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
-        w[i] = *reinterpret_cast<uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+// First row tile whose last block is anchored behind position `pos`.
+__device__ __forceinline__ int first_tile_behind(const PackedBwdPlan& pl, int pos) {
+  int lo = 0, hi = pl.T;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.sorted[min((mid + 1) * pl.per, pl.N) - 1] > pos) hi = mid; else lo = mid + 1;
   }
+  return lo;
 }
+// CTAs that share the n streamed tiles of one context key tile.
+__device__ __forceinline__ int shares_of(const PackedBwdPlan& pl, int n) { return (n + pl.share - 1) / pl.share; }
 
 // S (+)= A B' over hd: A 128 resident rows, B kN streamed rows, both K-major.
+// With two planes the small products come first, while the sum is small.
 template <int HD, int PL>
-__device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* res, const uint8_t* str) {
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t res, uint32_t str) {
   using C = GradCfg<HD, PL>;
   constexpr uint32_t id = idesc_f16(kRows, C::kN);
   uint32_t acc = 0;
 #pragma unroll
-  for (int pr = 0; pr < (PL == 2 ? 3 : 1); ++pr) {   // hi hi, hi lo, lo hi
-    const int pa = pr == 2, pb = pr == 1;
+  for (int pr = (PL == 2 ? 0 : 2); pr < 3; ++pr) {   // hi lo, lo hi, hi hi
+    const int pa = pr == 1, pb = pr == 0;
 #pragma unroll
     for (int s = 0; s < C::kSub; ++s)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        ptx::mma_bf16(d, ptx::smem_desc_sw128(res + (pa * C::kSub + s) * C::kResTile) + 2 * k,
-                      ptx::smem_desc_sw128(str + (pb * C::kSub + s) * C::kStrTile) + 2 * k, id, acc);
+        mma_smem(d, res + ((pa * C::kSub + s) * C::kResTile >> 4) + 2 * k,
+                 str + ((pb * C::kSub + s) * C::kStrTile >> 4) + 2 * k, id, acc);
         acc = 1;
       }
   }
@@ -501,17 +587,18 @@ __device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* res, const
 // G (+)= A B: A the P or dS of 128 lanes in tensor memory (columns of `a` as
 // put_pairs left them), B kN streamed rows read along their values.
 template <int HD, int PL>
-__device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, const uint8_t* str, uint32_t accumulate) {
+__device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, uint32_t str, uint32_t accumulate) {
   using C = GradCfg<HD, PL>;
   constexpr uint32_t id = idesc_f16(kRows, HD) | kBMajorMN;
   uint32_t acc = accumulate;
 #pragma unroll
-  for (int pr = 0; pr < (PL == 2 ? 3 : 1); ++pr) {
-    const int pa = pr == 2, pb = pr == 1;
+  for (int pr = (PL == 2 ? 0 : 2); pr < 3; ++pr) {
+    const int pa = pr == 1, pb = pr == 0;
 #pragma unroll
     for (int k = 0; k < C::kN / 16; ++k) {
-      mma_tmem_a(d, a + (k >> 1) * 32 + pa * 16 + (k & 1) * 8,
-                 smem_desc_mn(str + pb * C::kSub * C::kStrTile + k * 2048, C::kStrTile), id, acc);
+      const int chunk = 16 * k / C::kCols, in = 16 * k % C::kCols;
+      mma_tmem(d, a + chunk * C::kCols + pa * (C::kCols / 2) + in / 2,
+               str + (pb * C::kSub * C::kStrTile >> 4) + k * (2048 >> 4), id, acc);
       acc = 1;
     }
   }
@@ -522,16 +609,73 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
                                                                       const __grid_constant__ PackedBwdTensors t,
                                                                       const __grid_constant__ GradMaps maps) {
   using C = GradCfg<HD, PL>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   GradBars* bars = reinterpret_cast<GradBars*>(sm + C::kOffBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  griddep_trigger();
+  if (ptx::smem_u32(sm) & 1023) {   // the swizzled tiles need it; no device places shared memory otherwise
+    if (tid == 0) report_status(pl.status, DFLASH_ERR_UNSUPPORTED);
+    return;
+  }
+
+  // ---- this CTA's item
+  const int G = pl.nq / pl.nkv, rows = pl.T * kRows, ctx = pl.KT * kRows;
+  constexpr int kPer = kRows / C::kN;        // streamed tiles of 128 rows
+  const int n_ctx = pl.KT * pl.nkv * pl.splits, n_rows = pl.T * pl.nq;
+  int kind, h, tile, share = 0;              // kind 0: context keys, 1: rows, 2: own keys (h: kv head unless 1)
+  int u0 = 0, u1, first = 0, whole = 0;      // streamed tiles [u0, u1)
+  {
+    int b = blockIdx.x;
+    if (b < n_ctx) {
+      // the first keys are seen by most: longest items first.  Streamed: the
+      // row tiles from `first` on (from `whole` on they see every key), head by head
+      kind = 0;
+      tile = b / (pl.nkv * pl.splits);
+      b -= tile * pl.nkv * pl.splits;
+      h = b / pl.splits;
+      share = b - h * pl.splits;
+      first = first_tile_behind(pl, tile * kRows);
+      const int n = (pl.T - first) * kPer * G, shares = shares_of(pl, n);
+      if (share >= shares) return;
+      u0 = (int)((long long)n * share / shares);
+      u1 = (int)((long long)n * (share + 1) / shares);
+      int hi = pl.T;
+      whole = first;
+      while (whole < hi) {   // first row tile whose first block is anchored behind the whole key tile
+        const int mid = (whole + hi) >> 1;
+        if (pl.sorted[mid * pl.per] >= (tile + 1) * kRows) hi = mid; else whole = mid + 1;
+      }
+    } else if (b < n_ctx + n_rows) {
+      // streamed: the context below the tile's largest anchor (`first` tiles), then the tile's own keys
+      kind = 1;
+      b -= n_ctx;
+      tile = pl.T - 1 - b / pl.nq;
+      h = b % pl.nq;
+      first = (pl.sorted[min((tile + 1) * pl.per, pl.N) - 1] + C::kN - 1) / C::kN;
+      u1 = first + kPer;
+    } else {
+      // streamed: the row tile, head by head
+      kind = 2;
+      b -= n_ctx + n_rows;
+      tile = b / pl.nkv;
+      h = b % pl.nkv;
+      u1 = G * kPer;
+    }
+  }
+  const int kvh = kind == 1 ? h / G : h, n = u1 - u0;
+  // head and first row of streamed tile u (kinds 0 and 2)
+  const int per_head = kind == 0 ? (pl.T - first) * kPer : kPer, row0 = (kind == 0 ? first : tile) * kRows;
 
   if (tid == 0) {
     ptx::mbar_init(&bars->res_full, 1);
+    for (int s = 0; s < 3; ++s) {
+      ptx::mbar_init(&bars->full0[s], 1);
+      ptx::mbar_init(&bars->freed0[s], 1);
+    }
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&bars->full[s], 1);
-      ptx::mbar_init(&bars->freed[s], 1);
+      ptx::mbar_init(&bars->full1[s], 1);
+      ptx::mbar_init(&bars->freed1[s], 1);
     }
     ptx::mbar_init(&bars->s_full, 1);
     ptx::mbar_init(&bars->dp_full, 1);
@@ -548,202 +692,147 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  griddep_wait();
-  griddep_trigger();
 
-  // ---- this CTA's item
-  const int G = pl.nq / pl.nkv, rows = pl.T * kRows, ctx = pl.KT * kRows;
-  constexpr int kPer = kRows / C::kN;        // streamed pieces of a 128-row tile
-  const int n_ctx = pl.KT * pl.nq * pl.splits, n_rows = pl.T * pl.nq;
-  int kind, h, tile, split = 0;              // kind 0: context keys, 1: rows, 2: own keys (h: kv head)
-  {
-    int b = blockIdx.x;
-    if (b < n_ctx) {                         // the first keys are seen by most: longest items first
-      kind = 0;
-      tile = b / (pl.nq * pl.splits);
-      b -= tile * pl.nq * pl.splits;
-      h = b / pl.splits;
-      split = b - h * pl.splits;
-    } else if (b < n_ctx + n_rows) {
-      kind = 1;
-      b -= n_ctx;
-      tile = pl.T - 1 - b / pl.nq;
-      h = b % pl.nq;
-    } else {
-      kind = 2;
-      b -= n_ctx + n_rows;
-      tile = b / pl.nkv;
-      h = b % pl.nkv;
-    }
-  }
-  const int kvh = kind == 2 ? h : h / G;
-  // streamed pieces [u0, u1): kind 0: of the rows; 1: of the context, then of
-  // the own keys; 2: of the row tile, for each head in turn
-  int u0 = 0, u1 = 0, ctx_pieces = 0;
-  if (kind == 0) {
-    // first row tile whose last block is anchored behind this tile's first key
-    int lo = 0, hi = pl.T;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (pl.sorted[min((mid + 1) * pl.per, pl.N) - 1] > tile * kRows) hi = mid; else lo = mid + 1;
-    }
-    const int n = (pl.T - lo) * kPer;
-    u0 = lo * kPer + (int)((long long)n * split / pl.splits);
-    u1 = lo * kPer + (int)((long long)n * (split + 1) / pl.splits);
-  } else if (kind == 1) {
-    const int last = pl.sorted[min((tile + 1) * pl.per, pl.N) - 1];   // its largest anchor
-    ctx_pieces = (last + C::kN - 1) / C::kN;
-    u1 = ctx_pieces + kPer;
-  } else {
-    u1 = G * kPer;
-  }
-  const int n = u1 - u0;
-  // streamed rows of piece u: (slab, first row) for kind 0 and 2 in [nq][planes][rows]
-  auto piece_head = [&](int u) { return kind == 0 ? h : h * G + u / kPer; };
-  auto piece_row = [&](int u) { return kind == 0 ? u * C::kN : tile * kRows + (u % kPer) * C::kN; };
-
-  uint8_t* str = sm + C::kOffStr;
-  auto stage = [&](int i) { return str + (i % C::kStages) * 2 * C::kStr; };
-  auto stats = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (i % C::kStages) * C::kStat); };
-  auto par = [&](int i) { return static_cast<uint32_t>(i / C::kStages) & 1u; };
+  auto str0 = [&](int i) { return sm + C::kOff0 + (i % C::kS0) * C::kStr; };
+  auto str1 = [&](int i) { return sm + C::kOff1 + (i % C::kS1) * C::kStr; };
+  auto lse_of = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (i % C::kS0) * C::kStat); };
+  auto delta_of = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (C::kS0 + i % C::kS1) * C::kStat); };
+  auto par0 = [](int i) { return static_cast<uint32_t>(i / C::kS0) & 1u; };
+  auto par1 = [](int i) { return static_cast<uint32_t>(i / C::kS1) & 1u; };
   const uint32_t tA = tmem, tB = tmem + 256;
-  // kind 0, 2: S in columns [0, kN), dP at 128, dV at 256, dK at 256 + HD.
+  // kinds 0, 2: S in columns [0, kN), dP at 128, dV at 256, dK at 256 + HD.
   // kind 1: S in two buffers at 0 and 128, dP at 256, dQ at 384.
   bool ok = true;
 
   if (warp == kSoftWarps) {
-    if (lane == 0 && n > 0) {   // ------------------------------------------------ loads
-      const uint64_t keep = ptx::policy_evict_last();
-      ptx::mbar_arrive_expect_tx(&bars->res_full, 2 * C::kRes);
-      const CUtensorMap* ma = kind == 0 ? &maps.kc : kind == 1 ? &maps.q : &maps.kb;
-      const CUtensorMap* mb = kind == 0 ? &maps.vc : kind == 1 ? &maps.d_o : &maps.vb;
-      const int slab = kind == 1 ? h : kvh, per = kind == 0 ? ctx : rows;
-      for (int p = 0; p < PL; ++p)
-        for (int s = 0; s < C::kSub; ++s) {
-          const int y = (slab * PL + p) * per + tile * kRows;
-          ptx::tma_load_2d(sm + (p * C::kSub + s) * C::kResTile, ma, &bars->res_full, 64 * s, y, keep);
-          ptx::tma_load_2d(sm + C::kRes + (p * C::kSub + s) * C::kResTile, mb, &bars->res_full, 64 * s, y, keep);
-        }
-      int issued = 0;
-      for (int i = 0; i < n && ok; ++i) {
-        const int u = u0 + i, b = i % C::kStages;
-        if (i >= C::kStages) ok = ptx::mbar_wait_sleep(&bars->freed[b], par(i - C::kStages), kBudget, pl.status);
-        if (!ok) break;
-        const CUtensorMap *m0, *m1;
-        int slab_rows, sl, y0;
-        if (kind == 1) {
-          const bool own = u >= ctx_pieces;
-          m0 = own ? &maps.kbs : &maps.kcs;
-          m1 = own ? &maps.vbs : &maps.vcs;
-          sl = kvh;
-          slab_rows = own ? rows : ctx;
-          y0 = own ? tile * kRows + (u - ctx_pieces) * C::kN : u * C::kN;
-          ptx::mbar_arrive_expect_tx(&bars->full[b], 2 * C::kStr);
-        } else {
-          m0 = &maps.qs;
-          m1 = &maps.d_os;
-          sl = piece_head(u);
-          slab_rows = rows;
-          y0 = piece_row(u);
-          ptx::mbar_arrive_expect_tx(&bars->full[b], 2 * C::kStr + C::kStat);
-          float* st = stats(i);
-          bulk_load(st, pl.lse2 + (size_t)sl * rows + y0, 4 * C::kN, &bars->full[b]);
-          bulk_load(st + C::kN, pl.delta + (size_t)sl * rows + y0, 4 * C::kN, &bars->full[b]);
-          bulk_load(st + 2 * C::kN, pl.row_anchor + y0, 4 * C::kN, &bars->full[b]);
-        }
-        uint8_t* dst = stage(i);
+    if (lane == 0) {   // ------------------------------------------------ loads
+      {
+        ptx::mbar_arrive_expect_tx(&bars->res_full, 2 * C::kRes);
+        const CUtensorMap* ma = kind == 0 ? &maps.kc : kind == 1 ? &maps.q : &maps.kb;
+        const CUtensorMap* mb = kind == 0 ? &maps.vc : kind == 1 ? &maps.d_o : &maps.vb;
         for (int p = 0; p < PL; ++p)
           for (int s = 0; s < C::kSub; ++s) {
-            const int y = (sl * PL + p) * slab_rows + y0;
-            ptx::tma_load_2d(dst + (p * C::kSub + s) * C::kStrTile, m0, &bars->full[b], 64 * s, y, keep);
-            ptx::tma_load_2d(dst + C::kStr + (p * C::kSub + s) * C::kStrTile, m1, &bars->full[b], 64 * s, y, keep);
+            const int y = (h * PL + p) * (kind == 0 ? ctx : rows) + tile * kRows;
+            tma_tile(sm + (p * C::kSub + s) * C::kResTile, ma, &bars->res_full, 64 * s, y);
+            tma_tile(sm + C::kRes + (p * C::kSub + s) * C::kResTile, mb, &bars->res_full, 64 * s, y);
           }
-        issued = i + 1;
+      }
+      int i0 = 0, i1 = 0;   // tiles issued of each stream
+      for (int i = 0; i < n && ok; ++i) {
+        const int u = u0 + i;
+        const CUtensorMap *m0 = &maps.qs, *m1 = &maps.d_os;
+        int slab, slab_rows = rows, y0;
+        if (kind == 1) {
+          const bool own = u >= first;
+          m0 = own ? &maps.kbs : &maps.kcs;
+          m1 = own ? &maps.vbs : &maps.vcs;
+          slab = kvh;
+          slab_rows = own ? rows : ctx;
+          y0 = own ? tile * kRows + (u - first) * C::kN : u * C::kN;
+        } else {
+          const int hh = u / per_head;
+          slab = h * G + hh;
+          y0 = row0 + (u - hh * per_head) * C::kN;
+        }
+        const uint32_t bytes = C::kStr + (kind == 1 ? 0 : C::kStat);
+        auto issue = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, float* st, const float* src) {
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          for (int p = 0; p < PL; ++p)
+            for (int s = 0; s < C::kSub; ++s)
+              tma_tile(dst + (p * C::kSub + s) * C::kStrTile, m, bar, 64 * s, (slab * PL + p) * slab_rows + y0);
+          if (kind != 1) bulk_load(st, src + (size_t)slab * rows + y0, C::kStat, bar);
+        };
+        if (i >= C::kS0) ok = ptx::mbar_wait_sleep(&bars->freed0[i % C::kS0], par0(i - C::kS0), kBudget, pl.status);
+        if (!ok) break;
+        issue(str0(i), m0, &bars->full0[i % C::kS0], lse_of(i), pl.lse2);
+        i0 = i + 1;
+        if (i >= C::kS1) ok = ptx::mbar_wait_sleep(&bars->freed1[i % C::kS1], par1(i - C::kS1), kBudget, pl.status);
+        if (!ok) break;
+        issue(str1(i), m1, &bars->full1[i % C::kS1], delta_of(i), pl.delta);
+        i1 = i + 1;
       }
       if (!ok) {   // a wait ran out: the copies in flight land before the CTA ends
         ptx::mbar_wait(&bars->res_full, 0, kBudget, nullptr);
-        for (int i = max(0, issued - C::kStages); i < issued; ++i)
-          ptx::mbar_wait(&bars->full[i % C::kStages], par(i), kBudget, nullptr);
+        for (int i = max(0, i0 - C::kS0); i < i0; ++i) ptx::mbar_wait(&bars->full0[i % C::kS0], par0(i), kBudget, nullptr);
+        for (int i = max(0, i1 - C::kS1); i < i1; ++i) ptx::mbar_wait(&bars->full1[i % C::kS1], par1(i), kBudget, nullptr);
       }
     }
   } else if (warp == kSoftWarps + 1) {
-    if (lane == 0 && n > 0) {   // ------------------------------------------------ MMAs
+    if (lane == 0) {   // ------------------------------------------------ MMAs
       auto wait = [&](uint64_t* b, uint32_t p) {
         ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status);
         ptx::tc_fence_after();
         return ok;
       };
-      const uint8_t *ra = sm, *rb = sm + C::kRes;
+      const uint32_t ra = desc_k(sm), rb = desc_k(sm + C::kRes);
+      const uint32_t k0 = desc_k(sm + C::kOff0), k1 = desc_k(sm + C::kOff1);
+      const uint32_t g0 = desc_mn(sm + C::kOff0, C::kStrTile), g1 = desc_mn(sm + C::kOff1, C::kStrTile);
+      auto o0 = [](int i) { return (uint32_t)(i % C::kS0) * (C::kStr >> 4); };
+      auto o1 = [](int i) { return (uint32_t)(i % C::kS1) * (C::kStr >> 4); };
       wait(&bars->res_full, 0);
       if (kind != 1) {
+        // resident K, V; streamed Q, dO
         const uint32_t tS = tA, tP = tA + 128, tV = tB, tK = tB + HD;
-        // ra = K, rb = V; a stage holds Q, dO
         auto scores = [&](int i) {
-          if (!wait(&bars->full[i % C::kStages], par(i))) return;
-          mma_scores<HD, PL>(tS, ra, stage(i));
+          if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
+          mma_scores<HD, PL>(tS, ra, k0 + o0(i));
           ptx::mma_commit(&bars->s_full);
+          return true;
         };
         auto dprob = [&](int i) {
-          mma_scores<HD, PL>(tP, rb, stage(i) + C::kStr);
+          if (!wait(&bars->full1[i % C::kS1], par1(i))) return false;
+          mma_scores<HD, PL>(tP, rb, k1 + o1(i));
           ptx::mma_commit(&bars->dp_full);
+          return true;
         };
-        if (ok) scores(0);
-        if (ok) dprob(0);
+        if (ok && scores(0)) dprob(0);
         for (int i = 0; i < n && ok; ++i) {
           if (!wait(&bars->p_ready, i & 1)) break;
-          mma_gradient<HD, PL>(tV, tS, stage(i) + C::kStr, i > 0);
-          if (C::kStages > 1 && i + 1 < n) {
-            scores(i + 1);
-            if (!ok) break;
-          }
+          mma_gradient<HD, PL>(tV, tS, g1 + o1(i), i > 0);
+          ptx::mma_commit(&bars->freed1[i % C::kS1]);
+          if (i + 1 < n && !scores(i + 1)) break;
           if (!wait(&bars->ds_ready, i & 1)) break;
-          mma_gradient<HD, PL>(tK, tP, stage(i), i > 0);
-          ptx::mma_commit(&bars->freed[i % C::kStages]);
-          if (i + 1 < n) {
-            if (C::kStages == 1) scores(i + 1);
-            if (ok) dprob(i + 1);
-          }
+          mma_gradient<HD, PL>(tK, tP, g0 + o0(i), i > 0);
+          ptx::mma_commit(&bars->freed0[i % C::kS0]);
+          if (i + 1 < n && !dprob(i + 1)) break;
         }
       } else {
+        // resident Q, dO; streamed K, V
         const uint32_t tP = tB, tQ = tB + 128;
-        // ra = Q, rb = dO; a stage holds K, V
         auto scores = [&](int i) {
-          if (!wait(&bars->full[i % C::kStages], par(i))) return;
-          mma_scores<HD, PL>(tA + (i & 1) * 128, ra, stage(i));
+          if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
+          mma_scores<HD, PL>(tA + (i & 1) * 128, ra, k0 + o0(i));
+          return true;
         };
         auto dprob = [&](int i) {
-          mma_scores<HD, PL>(tP, rb, stage(i) + C::kStr);
+          if (!wait(&bars->full1[i % C::kS1], par1(i))) return false;
+          mma_scores<HD, PL>(tP, rb, k1 + o1(i));
           ptx::mma_commit(&bars->s_full);
+          ptx::mma_commit(&bars->freed1[i % C::kS1]);
+          return true;
         };
-        if (ok) scores(0);
-        if (ok) dprob(0);
+        if (ok && scores(0)) dprob(0);
         for (int i = 0; i < n && ok; ++i) {
-          if (C::kStages > 1 && i + 1 < n) {
-            scores(i + 1);
-            if (!ok) break;
-          }
+          if (i + 1 < n && !scores(i + 1)) break;
           if (!wait(&bars->p_ready, i & 1)) break;   // dP(i) is in registers
-          if (C::kStages > 1 && i + 1 < n) dprob(i + 1);
+          if (i + 1 < n && !dprob(i + 1)) break;
           if (!wait(&bars->ds_ready, i & 1)) break;
-          mma_gradient<HD, PL>(tQ, tA + (i & 1) * 128, stage(i), i > 0);
-          ptx::mma_commit(&bars->freed[i % C::kStages]);
-          if (C::kStages == 1 && i + 1 < n) {
-            scores(i + 1);
-            if (ok) dprob(i + 1);
-          }
+          mma_gradient<HD, PL>(tQ, tA + (i & 1) * 128, g0 + o0(i), i > 0);
+          ptx::mma_commit(&bars->freed0[i % C::kS0]);
         }
       }
       ptx::mma_commit(&bars->done);
       if (!ok) ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTA does
     }
   } else {   // ---------------------------------------------------------------------- softmax
-    const int q4 = warp & 3, half = warp >> 2, me = 32 * q4 + lane;   // my lane of tensor memory
+    constexpr int NC = C::kCols;
+    const int q4 = warp & 3, part = warp >> 2, me = 32 * q4 + lane;   // my lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
-    const int c0 = half * C::kHalf;                                   // my first column
+    const int c0 = part * NC;                                         // my first column
     const Scales sc = load_scales(pl.scale);
-    const float sc2 = ldexpf(kLog2e * rsqrtf((float)HD), -sc.q - sc.k);   // the products' scales leave with it
-    const float f_dp = ldexpf(1.f, sc.dp - sc.o - sc.v);
     const float scale = rsqrtf((float)HD);
+    const float sc2 = ldexpf(kLog2e * scale, -sc.q - sc.k);   // the products' scales leave with it
+    const float f_dp = ldexpf(1.f, sc.dp - sc.o - sc.v);
     auto arrive = [&](uint64_t* b) {
       ptx::tc_fence_before();
       __syncwarp();
@@ -756,105 +845,134 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       return ok;
     };
     const int own = me / pl.block;            // block of my lane's row or key within its tile
+    // staged output rows: matrix m's row r at m * kRows * kPitch + r * kPitch
+    auto stage32 = [&](int m, int c, const float* v, bool wide) {   // 32 columns from c on
+      uint8_t* d = sm + (size_t)(m * kRows + me) * C::kPitch + c * (wide ? 4 : (int)sizeof(T));
+      if (wide || sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(d + 4 * j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            __nv_bfloat162 b = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+            w[i] = *reinterpret_cast<uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint4*>(d + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    };
+    // All rows staged, the first 128 threads send matrix 0's, the next 128 matrix
+    // 1's.  Every warp comes here, after a timeout too: the barrier needs them all.
+    auto send = [&](void* dst, uint32_t bytes) {
+      ptx::fence_proxy_async_shared();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");
+      if (dst) {
+        bulk_store(dst, sm + (size_t)tid * C::kPitch, bytes);
+        bulk_store_wait();
+      }
+    };
+    // place of a tile's row r in [N][block][heads][hd], or nullptr in padding
+    auto block_row = [&](void* base, int r, int heads, int head) -> void* {
+      const int b = r / pl.block, at = tile * pl.per + b;
+      if (b >= pl.per || at >= pl.N) return nullptr;
+      return static_cast<T*>(base) + (((size_t)pl.order[at] * pl.block + (r - b * pl.block)) * heads + head) * HD;
+    };
+    constexpr int kGroups = HD / 32;          // 32-column groups of a gradient row
     if (kind != 1) {
       const uint32_t tS = tA + lanes + c0, tP = tA + 128 + lanes + c0;
       const int key = tile * kRows + me;
+      int in_head = u0 % per_head;            // streamed tile within its head
       for (int i = 0; i < n; ++i) {
-        if (!wait(&bars->full[i % C::kStages], par(i))) break;        // the rows' statistics
-        const float* lse2 = stats(i) + c0;
-        const float* delta = lse2 + C::kN;
-        const int* anchor = reinterpret_cast<const int*>(lse2 + 2 * C::kN);
-        const int r0 = piece_row(u0 + i) + c0 - (kind == 2 ? tile * kRows : 0);   // first row (within the tile: own keys)
-        // rows below a boundary: only tiles that one crosses compare
-        const bool compare = kind == 2 || reinterpret_cast<const int*>(stats(i) + 2 * C::kN)[0] < (tile + 1) * kRows;
-        if (!wait(&bars->s_full, i & 1)) break;
-        float p[C::kHalf];
-#pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32) {
-          ptx::tmem_ld32(tS + c, p + c);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(lse2 + c + j);
-            p[c + j] = ex2(fmaf(p[c + j], sc2, -l.x));
-            p[c + j + 1] = ex2(fmaf(p[c + j + 1], sc2, -l.y));
-            p[c + j + 2] = ex2(fmaf(p[c + j + 2], sc2, -l.z));
-            p[c + j + 3] = ex2(fmaf(p[c + j + 3], sc2, -l.w));
-          }
-          if (compare) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const bool seen = kind == 0 ? anchor[c + j] > key
-                                          : static_cast<unsigned>(r0 + c + j - own * pl.block) < static_cast<unsigned>(pl.block);
-              if (!seen) p[c + j] = 0.f;
-            }
-          }
-          put_pairs<PL>(tS + c, p + c);
+        const int r0 = row0 + in_head * C::kN + c0;   // my first column's row
+        const bool compare = kind == 2 || r0 < whole * kRows;
+        if (++in_head == per_head) in_head = 0;
+        if (!wait(&bars->full0[i % C::kS0], par0(i)) || !wait(&bars->s_full, i & 1)) break;
+        const float* lse2 = lse_of(i) + c0;
+        float p[NC];
+        {
+          uint32_t raw[NC];
+          tmem_ld<NC>(tS, raw);
+          tmem_ld_wait();
+          tmem_values<NC>(raw, p);
         }
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(lse2 + j);
+          const float2 a = fma2(make_float2(p[j], p[j + 1]), make_float2(sc2, sc2), make_float2(-l.x, -l.y));
+          const float2 b = fma2(make_float2(p[j + 2], p[j + 3]), make_float2(sc2, sc2), make_float2(-l.z, -l.w));
+          p[j] = ex2(a.x);
+          p[j + 1] = ex2(a.y);
+          p[j + 2] = ex2(b.x);
+          p[j + 3] = ex2(b.y);
+        }
+        if (compare) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const bool seen = kind == 0 ? __ldg(pl.row_anchor + r0 + j) > key
+                                        : static_cast<unsigned>(r0 + j - row0 - own * pl.block) < static_cast<unsigned>(pl.block);
+            if (!seen) p[j] = 0.f;
+          }
+        }
+        put_pairs<PL, NC>(tS, p);
         tmem_st_wait();
         arrive(&bars->p_ready);
-        if (!wait(&bars->dp_full, i & 1)) break;
-#pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32) {
-          float d[32];
-          ptx::tmem_ld32(tP + c, d);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(delta + c + j);
-            d[j] = p[c + j] * fmaf(d[j], f_dp, -x.x);
-            d[j + 1] = p[c + j + 1] * fmaf(d[j + 1], f_dp, -x.y);
-            d[j + 2] = p[c + j + 2] * fmaf(d[j + 2], f_dp, -x.z);
-            d[j + 3] = p[c + j + 3] * fmaf(d[j + 3], f_dp, -x.w);
-          }
-          put_pairs<PL>(tP + c, d);
+        if (!wait(&bars->full1[i % C::kS1], par1(i)) || !wait(&bars->dp_full, i & 1)) break;
+        const float* delta = delta_of(i) + c0;
+        float d[NC];
+        {
+          uint32_t raw[NC];
+          tmem_ld<NC>(tP, raw);
+          tmem_ld_wait();
+          tmem_values<NC>(raw, d);
         }
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(delta + j);
+          const float2 f = make_float2(f_dp, f_dp);
+          const float2 a = mul2(make_float2(p[j], p[j + 1]), fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y)));
+          const float2 b = mul2(make_float2(p[j + 2], p[j + 3]),
+                                fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w)));
+          d[j] = a.x;
+          d[j + 1] = a.y;
+          d[j + 2] = b.x;
+          d[j + 3] = b.y;
+        }
+        put_pairs<PL, NC>(tP, d);
         tmem_st_wait();
         arrive(&bars->ds_ready);
       }
-      // ---- dV and dK of my key, half of the columns each
-      if (n > 0) wait(&bars->done, 0);
+      // ---- dV and dK of my key: the warps of a lane quarter take the 32-column groups of both in turn
+      wait(&bars->done, 0);
       if (ok) {
         const int e_v = -kPExp - sc.o, e_k = -kPExp - sc.dp - sc.q;
-        constexpr int kCols = HD / 2;
-        float* pk = nullptr;
-        float* pv = nullptr;
-        T* bk = nullptr;
-        T* bv = nullptr;
-        if (kind == 0) {
-          if (key < pl.S) {
-            const size_t o = (((size_t)h * pl.splits + split) * pl.S + key) * HD + half * kCols;
-            pk = pl.dk_part + o;
-            pv = pl.dv_part + o;
-          }
-        } else {
-          const int at = tile * pl.per + own;
-          if (own < pl.per && at < pl.N) {
-            const size_t o = (((size_t)pl.order[at] * pl.block + (me - own * pl.block)) * pl.nkv + kvh) * HD + half * kCols;
-            bk = static_cast<T*>(t.d_k_blk) + o;
-            bv = static_cast<T*>(t.d_v_blk) + o;
-          }
-        }
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          float v[32] = {}, k[32] = {};
-          if (n > 0) {
-            ptx::tmem_ld32(tB + lanes + half * kCols + c, v);
-            ptx::tmem_ld32(tB + lanes + HD + half * kCols + c, k);
-          }
+        for (int x = 0; x < 2 * kGroups / 4; ++x) {
+          const int gq = x * 4 + part, m = gq / kGroups, c = gq % kGroups * 32;   // matrix 0: dK, 1: dV
+          uint32_t raw[32];
+          float v[32];
+          tmem_ld<32>(tB + lanes + (m ? 0 : HD) + c, raw);
+          tmem_ld_wait();
+          tmem_values<32>(raw, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            k[j] = ldexpf(k[j] * scale, e_k);
-            v[j] = ldexpf(v[j], e_v);
-          }
-          if (pk) {
-            store32(pk + c, k);
-            store32(pv + c, v);
-          }
-          if (bk) {
-            store32(bk + c, k);
-            store32(bv + c, v);
-          }
+          for (int j = 0; j < 32; ++j) v[j] = m ? ldexpf(v[j], e_v) : ldexpf(v[j] * scale, e_k);
+          stage32(m, c, v, kind == 0);
         }
       }
+      void* dst = nullptr;
+      if (ok && tid < 2 * kRows) {
+        const int r = tid % kRows;
+        const bool v = tid >= kRows;
+        if (kind == 0) {
+          if (tile * kRows + r < pl.S)
+            dst = (v ? pl.dv_part : pl.dk_part) + (((size_t)h * pl.splits + share) * pl.S + tile * kRows + r) * HD;
+        } else {
+          dst = block_row(v ? t.d_v_blk : t.d_k_blk, r, pl.nkv, kvh);
+        }
+      }
+      send(dst, HD * (kind == 0 ? 4 : (int)sizeof(T)));
     } else {
       const uint32_t tP = tB + lanes + c0;
       const int r = tile * kRows + me;
@@ -863,53 +981,57 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       for (int i = 0; i < n; ++i) {
         if (!wait(&bars->s_full, i & 1)) break;
         const uint32_t tS = tA + (i & 1) * 128 + lanes + c0;
-        // columns [first, first + count) of mine are seen
-        int first = 0, count;
-        if (i < ctx_pieces) {
+        // columns [from, from + count) of mine are seen
+        int from = 0, count;
+        if (i < first) {
           count = anchor - i * C::kN - c0;
         } else {
-          first = own * pl.block - (i - ctx_pieces) * C::kN - c0;
+          from = own * pl.block - (i - first) * C::kN - c0;
           count = pl.block;
         }
-        const bool all = __all_sync(0xffffffffu, i < ctx_pieces && count >= C::kHalf);
-        float d[C::kHalf];
-#pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32) ptx::tmem_ld32(tP + c, d + c);
+        const bool all = __all_sync(0xffffffffu, i < first && count >= NC);
+        float d[NC], s[NC];
+        {
+          uint32_t raw[NC], raw2[NC];
+          tmem_ld<NC>(tP, raw);
+          tmem_ld<NC>(tS, raw2);
+          tmem_ld_wait();
+          tmem_values<NC>(raw, d);
+          tmem_values<NC>(raw2, s);
+        }
         arrive(&bars->p_ready);   // dP may be overwritten
 #pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32) {
-          float s[32];
-          ptx::tmem_ld32(tS + c, s);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = ex2(fmaf(s[j], sc2, -lse2)) * fmaf(d[c + j], f_dp, -delta);
-          if (!all) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < first || c + j >= first + count) s[j] = 0.f;
-          }
-          put_pairs<PL>(tS + c, s);
+        for (int j = 0; j < NC; j += 2) {
+          const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(sc2, sc2), make_float2(-lse2, -lse2));
+          const float2 b = fma2(make_float2(d[j], d[j + 1]), make_float2(f_dp, f_dp), make_float2(-delta, -delta));
+          const float2 x = mul2(make_float2(ex2(a.x), ex2(a.y)), b);
+          s[j] = x.x;
+          s[j + 1] = x.y;
         }
+        if (!all) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (j < from || j >= from + count) s[j] = 0.f;
+        }
+        put_pairs<PL, NC>(tS, s);
         tmem_st_wait();
         arrive(&bars->ds_ready);
       }
       wait(&bars->done, 0);
       if (ok) {
         const int e_q = -kPExp - sc.dp - sc.k;
-        constexpr int kCols = HD / 2;
-        const int at = tile * pl.per + own;
-        T* dst = nullptr;
-        if (own < pl.per && at < pl.N)
-          dst = static_cast<T*>(t.d_q) + (((size_t)pl.order[at] * pl.block + (me - own * pl.block)) * pl.nq + h) * HD +
-                half * kCols;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
+        if (part < kGroups) {
+          uint32_t raw[32];
           float v[32];
-          ptx::tmem_ld32(tB + 128 + lanes + half * kCols + c, v);
+          tmem_ld<32>(tB + 128 + lanes + part * 32, raw);
+          tmem_ld_wait();
+          tmem_values<32>(raw, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = ldexpf(v[j] * scale, e_q);
-          if (dst) store32(dst + c, v);
+          stage32(0, part * 32, v, false);
         }
       }
+      send(ok && tid < kRows ? block_row(t.d_q, tid, pl.nq, h) : nullptr, HD * (int)sizeof(T));
     }
   }
   ptx::tc_fence_before();
@@ -921,39 +1043,40 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 }
 
 // ---------------------------------------------------------------- context gradients from their shares
-// d_k_ctx and d_v_ctx [S][nkv][hd]: the shares of a kv head's q heads and their
-// splits, added in order; 4 values a thread.
-template <typename T>
+// d_k_ctx and d_v_ctx [S][nkv][hd]: a key tile's shares added in order, 4
+// values a thread.  grid (key tiles x parts of a tile, kv heads).
+template <typename T, int HD, int PL>
 __global__ void __launch_bounds__(256) reduce_ctx_kernel(PackedBwdPlan pl, T* dk, T* dv) {
   griddep_wait();
   griddep_trigger();
-  const int q = pl.hd / 4, shares = pl.nq / pl.nkv * pl.splits;
-  const long long total = (long long)pl.S * pl.nkv * q;
-  const size_t slab = (size_t)pl.S * pl.hd;
-  for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long long)gridDim.x * 256) {
-    const int d = (int)(e % q) * 4;
-    const long long r = e / q;
-    const int s = (int)(r % pl.S), h = (int)(r / pl.S);   // consecutive threads along a share's rows
-    const size_t src = (size_t)h * shares * slab + (size_t)s * pl.hd + d;
-    float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-    for (int i = 0; i < shares; ++i) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(pl.dk_part + src + i * slab));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(pl.dv_part + src + i * slab));
-      k.x += a.x; k.y += a.y; k.z += a.z; k.w += a.w;
-      v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
-    }
-    const size_t dst = ((size_t)s * pl.nkv + h) * pl.hd + d;
-    auto put = [&](T* o, float4 x) {
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(o) = x;
-      } else {
-        __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-        *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-      }
-    };
-    put(dk + dst, k);
-    put(dv + dst, v);
+  constexpr int Q = HD / 4, kParts = kRows * Q / 256;
+  const int tile = blockIdx.x / kParts, h = blockIdx.y;
+  __shared__ int s_shares;
+  if (threadIdx.x == 0)
+    s_shares = shares_of(pl, (pl.T - first_tile_behind(pl, tile * kRows)) * (kRows / GradCfg<HD, PL>::kN) * (pl.nq / pl.nkv));
+  __syncthreads();
+  const int shares = s_shares, e = blockIdx.x % kParts * 256 + threadIdx.x;
+  const int s = tile * kRows + e / Q, d = e % Q * 4;
+  if (s >= pl.S) return;
+  const size_t slab = (size_t)pl.S * HD, src = (size_t)h * pl.splits * slab + (size_t)s * HD + d;
+  float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+  for (int i = 0; i < shares; ++i) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(pl.dk_part + src + i * slab));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(pl.dv_part + src + i * slab));
+    k.x += a.x; k.y += a.y; k.z += a.z; k.w += a.w;
+    v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
   }
+  const size_t dst = ((size_t)s * pl.nkv + h) * HD + d;
+  auto put = [&](T* o, float4 x) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(o) = x;
+    } else {
+      __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+      *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    }
+  };
+  put(dk + dst, k);
+  put(dv + dst, v);
 }
 
 // ---------------------------------------------------------------- lse of the forward
@@ -998,15 +1121,13 @@ cudaError_t run_grad(const PackedBwdPlan& pl, const PackedBwdTensors& t, int sms
   if (!enc(&m.q, &m.qs, pl.q, q_rows) || !enc(&m.d_o, &m.d_os, pl.d_o, q_rows) || !enc(&m.kc, &m.kcs, pl.kc, c_rows) ||
       !enc(&m.vc, &m.vcs, pl.vc, c_rows) || !enc(&m.kb, &m.kbs, pl.kb, b_rows) || !enc(&m.vb, &m.vbs, pl.vb, b_rows))
     return cudaErrorInvalidValue;
-  const int items = pl.KT * pl.nq * pl.splits + pl.T * pl.nq + pl.T * pl.nkv;
+  const int items = pl.KT * pl.nkv * pl.splits + pl.T * pl.nq + pl.T * pl.nkv;
   e = launch_pdl(packed_grad_kernel<T, HD, PL>, dim3(items), dim3(kGradThreads), C::kBytes, s, pl, t, m);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (pl.S > 0) {
-    const long long quads = (long long)pl.S * pl.nkv * (HD / 4);
-    const int g = (int)std::min<long long>((quads + 255) / 256, (long long)sms * 16);
-    e = launch_pdl(reduce_ctx_kernel<T>, dim3(g), dim3(256), 0, s, pl, static_cast<T*>(t.d_k_ctx),
-                   static_cast<T*>(t.d_v_ctx));
+    e = launch_pdl(reduce_ctx_kernel<T, HD, PL>, dim3(pl.KT * (kRows * HD / 4 / 256), pl.nkv), dim3(256), 0, s, pl,
+                   static_cast<T*>(t.d_k_ctx), static_cast<T*>(t.d_v_ctx));
     if (e != cudaSuccess) return e;
     ++*launches;
   }
@@ -1027,8 +1148,13 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   p.per = kRows / block;
   p.T = (N + p.per - 1) / p.per;
   p.KT = (S + kRows - 1) / kRows;
-  // enough context items to fill the GPU twice, at least one row tile each
-  p.splits = std::max(1, std::min(p.T, (2 * sms + std::max(1, nq * p.KT) - 1) / std::max(1, nq * p.KT)));
+  // Streamed tiles of one context item: with anchors spread over the sequence
+  // there are about G T KT nkv / 2 of them; two items an SM or more, at most 64
+  // tiles each.
+  const int per = kRows / (f32 && hd == 128 ? GradCfg<128, 2>::kN : kRows);
+  const long long all = (long long)(nq / nkv) * p.T * per;   // of the first key tile
+  p.share = (int)std::max(2LL, std::min(64LL, all * p.KT * nkv / 2 / (2 * sms)));
+  p.splits = (int)((all + p.share - 1) / p.share);
   const size_t rows = (size_t)p.T * kRows, ctx = (size_t)std::max(p.KT, 1) * kRows;
   char* c = static_cast<char*>(ws);
   size_t at = 0;
@@ -1053,7 +1179,7 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   p.vc = reinterpret_cast<__half*>(take(pe * ctx * nkv * hd));
   p.kb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
   p.vb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
-  const size_t part = 4 * (size_t)nq * p.splits * S * hd;
+  const size_t part = 4 * (size_t)nkv * p.splits * S * hd;
   p.dk_part = reinterpret_cast<float*>(take(part));
   p.dv_part = reinterpret_cast<float*>(take(part));
   p.bytes = at;

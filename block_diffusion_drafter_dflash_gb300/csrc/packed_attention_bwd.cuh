@@ -18,7 +18,8 @@ struct PackedBwdPlan {
   int per;                // blocks in a row tile
   int T;                  // row tiles
   int KT;                 // 128-key tiles of the context
-  int splits;             // CTAs that share one (q head, context key tile)'s row tiles
+  int share;              // streamed tiles that one CTA takes of a (kv head, context key tile)
+  int splits;             // CTAs that may share one
   int parts;              // CTAs that look for the operands' ranges
   int32_t* status;
   float* part;            // [parts][kRangeValues] their maxima
@@ -34,7 +35,7 @@ struct PackedBwdPlan {
   __half* vc;
   __half* kb;             // [nkv][planes][T*128][hd]
   __half* vb;
-  float* dk_part;         // [nq*splits][S][hd] this head's and split's share of d_k_ctx
+  float* dk_part;         // [nkv][splits][S][hd] each share's sum of d_k_ctx
   float* dv_part;
   size_t bytes;
 };
