@@ -510,12 +510,13 @@ __device__ __forceinline__ void put_pairs(uint32_t at, const float* v) {
 }
 
 // ---------------------------------------------------------------- the gradient kernel
-// Warps 0..15 softmax (warp w: lanes 32 (w % 4), a quarter of the columns w / 4),
+// Warps 0..15 softmax (warp w: lanes 32 (w % 4), a quarter w / 4 of the columns),
 // warp 16 loads, warp 17 issues the MMAs.
 constexpr int kSoftWarps = 16;
+constexpr int kParts = kSoftWarps / 4;             // warps of a lane quarter
 constexpr int kGradThreads = 32 * (kSoftWarps + 2);
 
-// Two streams of tiles pass the resident operands: the first feeds S and dK
+// Two streams of tiles pass the two resident operands: the first feeds S and dK
 // (or dQ), the second dP and dV.  The first one's tiles are needed soonest and
 // freed last, so it has one stage more.
 template <int HD, int PL>
@@ -533,17 +534,29 @@ struct GradCfg {
   static constexpr int kOff1 = kOff0 + kS0 * kStr;
   static constexpr int kOffStat = kOff1 + kS1 * kStr;
   static constexpr int kOffBars = kOffStat + (kS0 + kS1) * kStat;
-  static constexpr int kUsed = kOffBars + 256;
+  static constexpr int kUsed = kOffBars + 160;
   // more than half of an SM's shared memory: the CTA takes all of tensor memory
   static constexpr int kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-  static constexpr int kCols = kN / 4;                     // columns of S of one softmax warp
+  static constexpr int kCols = kN / kParts;                // columns of S of one softmax warp
   static constexpr int kPitch = HD * 4 + 16;               // fp32 rows staged on their way out: no bank conflicts
+  // tensor memory.  Keys: S at 0, dP at 128, dV at 256, dK behind it.  Rows: S in
+  // two buffers at 0 and 128, dP at 256, dQ at 384.
+  static constexpr int kColP = 128, kColV = 256, kColK = kColV + HD, kColPRows = 256, kColQ = 384;
   static constexpr uint32_t kTmem = 512;
-  static_assert(kBytes <= 227 * 1024 && 2 * kRows * kPitch <= kOffBars, "shared memory");
+  static_assert(kBytes <= 227 * 1024 && 2 * kRows * kPitch <= kOffStat, "shared memory");
 };
 
+// A barrier's waiters have to look at a phase before the next but one
+// completes.  Keys: what completes phase i + 1 of s_full, dp_full, p_ready and
+// ds_ready waits, through the MMA thread or the warps, for every waiter of
+// phase i.  A stage of the first stream is loaded again after dK, that is after
+// all warps have left it (ds_ready); the tile of one of the second, which MMAs
+// alone read, after dV, but its delta, which the warps read, after dK too: its
+// phase completes only then.
+// Rows: S and dP of tile i + 1 wait for the warps' loads of tile i (p_ready) and
+// not for their dS, so ds_ready alternates between two barriers.
 struct GradBars {
-  uint64_t res_full, full0[3], freed0[3], full1[2], freed1[2], s_full, dp_full, p_ready, ds_ready, done;
+  uint64_t res_full, full0[3], freed0[3], full1[2], freed1[2], s_full, dp_full, p_ready, ds_ready[2], done;
   uint32_t tmem;
 };
 
@@ -669,18 +682,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 
   if (tid == 0) {
     ptx::mbar_init(&bars->res_full, 1);
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < C::kS0; ++s) {
       ptx::mbar_init(&bars->full0[s], 1);
       ptx::mbar_init(&bars->freed0[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::kS1; ++s) {
       ptx::mbar_init(&bars->full1[s], 1);
       ptx::mbar_init(&bars->freed1[s], 1);
     }
     ptx::mbar_init(&bars->s_full, 1);
     ptx::mbar_init(&bars->dp_full, 1);
+    ptx::mbar_init(&bars->ds_ready[0], kSoftWarps);
+    ptx::mbar_init(&bars->ds_ready[1], kSoftWarps);
     ptx::mbar_init(&bars->p_ready, kSoftWarps);
-    ptx::mbar_init(&bars->ds_ready, kSoftWarps);
     ptx::mbar_init(&bars->done, 1);
     ptx::fence_mbar_init();
   }
@@ -699,9 +713,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
   auto delta_of = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (C::kS0 + i % C::kS1) * C::kStat); };
   auto par0 = [](int i) { return static_cast<uint32_t>(i / C::kS0) & 1u; };
   auto par1 = [](int i) { return static_cast<uint32_t>(i / C::kS1) & 1u; };
-  const uint32_t tA = tmem, tB = tmem + 256;
-  // kinds 0, 2: S in columns [0, kN), dP at 128, dV at 256, dK at 256 + HD.
-  // kind 1: S in two buffers at 0 and 128, dP at 256, dQ at 384.
   bool ok = true;
 
   if (warp == kSoftWarps) {
@@ -734,27 +745,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           slab = h * G + hh;
           y0 = row0 + (u - hh * per_head) * C::kN;
         }
-        const uint32_t bytes = C::kStr + (kind == 1 ? 0 : C::kStat);
-        auto issue = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, float* st, const float* src) {
-          ptx::mbar_arrive_expect_tx(bar, bytes);
+        auto issue = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar) {
           for (int p = 0; p < PL; ++p)
             for (int s = 0; s < C::kSub; ++s)
               tma_tile(dst + (p * C::kSub + s) * C::kStrTile, m, bar, 64 * s, (slab * PL + p) * slab_rows + y0);
-          if (kind != 1) bulk_load(st, src + (size_t)slab * rows + y0, C::kStat, bar);
         };
         if (i >= C::kS0) ok = ptx::mbar_wait_sleep(&bars->freed0[i % C::kS0], par0(i - C::kS0), kBudget, pl.status);
         if (!ok) break;
-        issue(str0(i), m0, &bars->full0[i % C::kS0], lse_of(i), pl.lse2);
+        uint64_t* bar = &bars->full0[i % C::kS0];
+        ptx::mbar_arrive_expect_tx(bar, C::kStr + (kind == 1 ? 0 : C::kStat));
+        issue(str0(i), m0, bar);
+        if (kind != 1) bulk_load(lse_of(i), pl.lse2 + (size_t)slab * rows + y0, C::kStat, bar);
         i0 = i + 1;
         if (i >= C::kS1) ok = ptx::mbar_wait_sleep(&bars->freed1[i % C::kS1], par1(i - C::kS1), kBudget, pl.status);
         if (!ok) break;
-        issue(str1(i), m1, &bars->full1[i % C::kS1], delta_of(i), pl.delta);
+        bar = &bars->full1[i % C::kS1];
+        ptx::mbar_arrive_expect_tx(bar, C::kStr + (kind == 1 ? 0 : C::kStat));
+        issue(str1(i), m1, bar);
         i1 = i + 1;
+        if (kind != 1) {
+          const int j = i - C::kS1;   // the last tile whose delta was there
+          if (j >= 0) ok = ptx::mbar_wait_sleep(&bars->freed0[j % C::kS0], par0(j), kBudget, pl.status);
+          if (!ok) break;
+          bulk_load(delta_of(i), pl.delta + (size_t)slab * rows + y0, C::kStat, bar);
+        }
       }
       if (!ok) {   // a wait ran out: the copies in flight land before the CTA ends
         ptx::mbar_wait(&bars->res_full, 0, kBudget, nullptr);
         for (int i = max(0, i0 - C::kS0); i < i0; ++i) ptx::mbar_wait(&bars->full0[i % C::kS0], par0(i), kBudget, nullptr);
-        for (int i = max(0, i1 - C::kS1); i < i1; ++i) ptx::mbar_wait(&bars->full1[i % C::kS1], par1(i), kBudget, nullptr);
+        for (int i = max(0, i1 - C::kS1); i < i1; ++i)   // (the last may wait for a delta that was not sent)
+          ptx::mbar_wait(&bars->full1[i % C::kS1], par1(i), kBudget / 8, nullptr);
       }
     }
   } else if (warp == kSoftWarps + 1) {
@@ -772,7 +792,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       wait(&bars->res_full, 0);
       if (kind != 1) {
         // resident K, V; streamed Q, dO
-        const uint32_t tS = tA, tP = tA + 128, tV = tB, tK = tB + HD;
+        const uint32_t tS = tmem, tP = tmem + C::kColP, tV = tmem + C::kColV, tK = tmem + C::kColK;
         auto scores = [&](int i) {
           if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
           mma_scores<HD, PL>(tS, ra, k0 + o0(i));
@@ -791,33 +811,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           mma_gradient<HD, PL>(tV, tS, g1 + o1(i), i > 0);
           ptx::mma_commit(&bars->freed1[i % C::kS1]);
           if (i + 1 < n && !scores(i + 1)) break;
-          if (!wait(&bars->ds_ready, i & 1)) break;
+          if (!wait(&bars->ds_ready[0], i & 1)) break;
           mma_gradient<HD, PL>(tK, tP, g0 + o0(i), i > 0);
           ptx::mma_commit(&bars->freed0[i % C::kS0]);
           if (i + 1 < n && !dprob(i + 1)) break;
         }
       } else {
         // resident Q, dO; streamed K, V
-        const uint32_t tP = tB, tQ = tB + 128;
         auto scores = [&](int i) {
           if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
-          mma_scores<HD, PL>(tA + (i & 1) * 128, ra, k0 + o0(i));
+          mma_scores<HD, PL>(tmem + (i & 1) * 128, ra, k0 + o0(i));
           return true;
         };
         auto dprob = [&](int i) {
           if (!wait(&bars->full1[i % C::kS1], par1(i))) return false;
-          mma_scores<HD, PL>(tP, rb, k1 + o1(i));
+          mma_scores<HD, PL>(tmem + C::kColPRows, rb, k1 + o1(i));
           ptx::mma_commit(&bars->s_full);
           ptx::mma_commit(&bars->freed1[i % C::kS1]);
           return true;
         };
         if (ok && scores(0)) dprob(0);
         for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n && !scores(i + 1)) break;
+          if (i + 1 < n && !scores(i + 1)) break;    // over dS(i - 1), which the last dQ has taken
           if (!wait(&bars->p_ready, i & 1)) break;   // dP(i) is in registers
           if (i + 1 < n && !dprob(i + 1)) break;
-          if (!wait(&bars->ds_ready, i & 1)) break;
-          mma_gradient<HD, PL>(tQ, tA + (i & 1) * 128, g0 + o0(i), i > 0);
+          if (!wait(&bars->ds_ready[i & 1], (i >> 1) & 1)) break;
+          mma_gradient<HD, PL>(tmem + C::kColQ, tmem + (i & 1) * 128, g0 + o0(i), i > 0);
           ptx::mma_commit(&bars->freed0[i % C::kS0]);
         }
       }
@@ -882,7 +901,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
     };
     constexpr int kGroups = HD / 32;          // 32-column groups of a gradient row
     if (kind != 1) {
-      const uint32_t tS = tA + lanes + c0, tP = tA + 128 + lanes + c0;
+      const uint32_t tS = tmem + lanes + c0, tP = tS + C::kColP;
       const int key = tile * kRows + me;
       int in_head = u0 % per_head;            // streamed tile within its head
       for (int i = 0; i < n; ++i) {
@@ -942,18 +961,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         }
         put_pairs<PL, NC>(tP, d);
         tmem_st_wait();
-        arrive(&bars->ds_ready);
+        arrive(&bars->ds_ready[0]);
       }
       // ---- dV and dK of my key: the warps of a lane quarter take the 32-column groups of both in turn
       wait(&bars->done, 0);
       if (ok) {
         const int e_v = -kPExp - sc.o, e_k = -kPExp - sc.dp - sc.q;
 #pragma unroll
-        for (int x = 0; x < 2 * kGroups / 4; ++x) {
-          const int gq = x * 4 + part, m = gq / kGroups, c = gq % kGroups * 32;   // matrix 0: dK, 1: dV
+        for (int x = 0; x < 2 * kGroups / kParts; ++x) {
+          const int gq = x * kParts + part, m = gq / kGroups, c = gq % kGroups * 32;   // matrix 0: dK, 1: dV
           uint32_t raw[32];
           float v[32];
-          tmem_ld<32>(tB + lanes + (m ? 0 : HD) + c, raw);
+          tmem_ld<32>(tmem + lanes + (m ? C::kColV : C::kColK) + c, raw);
           tmem_ld_wait();
           tmem_values<32>(raw, v);
 #pragma unroll
@@ -974,13 +993,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       }
       send(dst, HD * (kind == 0 ? 4 : (int)sizeof(T)));
     } else {
-      const uint32_t tP = tB + lanes + c0;
       const int r = tile * kRows + me;
       const float lse2 = pl.lse2[(size_t)h * rows + r], delta = pl.delta[(size_t)h * rows + r];
       const int anchor = pl.row_anchor[r];
       for (int i = 0; i < n; ++i) {
         if (!wait(&bars->s_full, i & 1)) break;
-        const uint32_t tS = tA + (i & 1) * 128 + lanes + c0;
+        const uint32_t tS = tmem + lanes + (i & 1) * 128 + c0;
         // columns [from, from + count) of mine are seen
         int from = 0, count;
         if (i < first) {
@@ -993,7 +1011,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         float d[NC], s[NC];
         {
           uint32_t raw[NC], raw2[NC];
-          tmem_ld<NC>(tP, raw);
+          tmem_ld<NC>(tmem + lanes + C::kColPRows + c0, raw);
           tmem_ld<NC>(tS, raw2);
           tmem_ld_wait();
           tmem_values<NC>(raw, d);
@@ -1015,20 +1033,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         }
         put_pairs<PL, NC>(tS, s);
         tmem_st_wait();
-        arrive(&bars->ds_ready);
+        arrive(&bars->ds_ready[i & 1]);
       }
       wait(&bars->done, 0);
       if (ok) {
         const int e_q = -kPExp - sc.dp - sc.k;
-        if (part < kGroups) {
+#pragma unroll
+        for (int c = part * 32; c < HD; c += kParts * 32) {
           uint32_t raw[32];
           float v[32];
-          tmem_ld<32>(tB + 128 + lanes + part * 32, raw);
+          tmem_ld<32>(tmem + lanes + C::kColQ + c, raw);
           tmem_ld_wait();
           tmem_values<32>(raw, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = ldexpf(v[j] * scale, e_q);
-          stage32(0, part * 32, v, false);
+          stage32(0, c, v, false);
         }
       }
       send(ok && tid < kRows ? block_row(t.d_q, tid, pl.nq, h) : nullptr, HD * (int)sizeof(T));

@@ -194,6 +194,26 @@ def test_zero_gradient_and_operands():
         assert all(bool((t == 0).all()) for t in grads)
 
 
+def test_many_calls_in_a_row():
+    """A wait that runs out takes 0.2 s and sets the status: none does in hundreds of back-to-back calls of many
+    work items, and all of them give the same bits."""
+    df = _df()
+    S, N, g, nq, nkv, hd = 2048, 256, 16, 16, 4, 128
+    anchors = anchors_of(N, S, 4)
+    ops = operands(S, N, g, nq, nkv, hd, torch.bfloat16, 21, "cuda")
+    d_out = torch.randn(ops[0].shape, device="cuda")
+    out, lse, first, ws = run(ops, anchors, d_out)
+    a = torch.tensor(anchors, dtype=torch.int32, device="cuda")
+    grads = [torch.full_like(t, math.nan) for t in ops]
+    statuses = []
+    for _ in range(10):
+        for _ in range(40):
+            df.dflash_packed_block_attention_backward(*ops, a, out, lse, d_out, *grads, ws)
+        statuses.append(df.dflash_packed_attention_status(ws))
+        assert all(torch.equal(x, y) for x, y in zip(first, grads))
+    assert statuses == [0] * 10
+
+
 def test_anchors_outside_the_sequence_are_clamped_and_flagged():
     df = _df()
     S, N, g, nq, nkv, hd = 64, 3, 4, 4, 2, 64
