@@ -90,38 +90,24 @@ __device__ __forceinline__ Scales scales_of(const float* m) {
 __device__ __forceinline__ Scales load_scales(const int32_t* p) { return Scales{p[0], p[1], p[2], p[3], p[4]}; }
 
 // ---------------------------------------------------------------- loads
-// E (2 or 4) consecutive values, in one load where their address allows it.
-template <int E>
-__device__ __forceinline__ void load_values(const float* p, float* v) {
-  if (reinterpret_cast<uintptr_t>(p) % (4 * E) == 0) {
-    if constexpr (E == 4) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = __ldcs(reinterpret_cast<const float2*>(p));
-      v[0] = x.x, v[1] = x.y;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = p[e];
-  }
+__device__ __forceinline__ void unpack16(uint4 r, float* v, float) {
+  v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
 }
-template <int E>
-__device__ __forceinline__ void load_values(const __nv_bfloat16* p, float* v) {
-  if (reinterpret_cast<uintptr_t>(p) % (2 * E) == 0) {
-    uint32_t w[E / 2];
-    if constexpr (E == 4) {
-      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(p));
-      w[0] = x.x, w[1] = x.y;
-    } else {
-      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-    }
+__device__ __forceinline__ void unpack16(uint4 r, float* v, __nv_bfloat16) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-  } else {
+  for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// The 16 bytes at p; `aligned`: whether its tensor starts on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* p, bool aligned) {
+  if (aligned) return *reinterpret_cast<const uint4*>(p);
+  constexpr int E = 16 / sizeof(T);
+  alignas(16) T v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __bfloat162float(p[e]);
-  }
+  for (int e = 0; e < E; ++e) v[e] = p[e];
+  return *reinterpret_cast<const uint4*>(v);
 }
 
 // ---------------------------------------------------------------- anchors in order, ranges of the operands
@@ -151,42 +137,73 @@ __device__ void rank_blocks(const PackedBwdPlan& pl, const int32_t* anchors, int
   }
 }
 
-// Largest value (and, where NORM, largest norm of a row) of `rows` rows of
-// HD values; a warp takes four rows at a time.
+// Largest value (and, where NORM, largest norm of a row) of `rows` rows of HD
+// values.  A warp has eight 16-byte loads a lane in flight; the eight sums of
+// squares are reduced together, half of them handed to the other lanes at each
+// step.
 template <typename T, int HD, bool NORM>
 __device__ __forceinline__ void range_rows(const T* x, long long rows, int part, int parts, float& mx, float& nm) {
-  constexpr int E = HD / 32, U = 4;
-  const int lane = threadIdx.x & 31;
-  const long long warps = (long long)parts * (kRangeThreads / 32);
-  for (long long r0 = ((long long)part * (kRangeThreads / 32) + (threadIdx.x >> 5)) * U; r0 < rows; r0 += warps * U) {
-    float v[U][E] = {};
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u < rows) load_values<E>(x + (size_t)(r0 + u) * HD + E * lane, v[u]);
+  constexpr int E = 16 / sizeof(T), L = HD / E, U = 8;   // values of a load, lanes of a row
+  constexpr int kRowsPer = 32 / L * U;
+  const int lane = threadIdx.x & 31, sub = lane / L, col = lane % L * E;
+  const bool aligned = aligned16(x);
+  const long long step = (long long)parts * (kRangeThreads / 32) * kRowsPer;
+  for (long long r0 = ((long long)part * (kRangeThreads / 32) + (threadIdx.x >> 5)) * kRowsPer; r0 < rows; r0 += step) {
+    uint4 raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float sq = 0.f;
+      const long long r = r0 + u * (32 / L) + sub;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (r < rows) raw[u] = load16(x + (size_t)r * HD + col, aligned);
+    }
+    float sq[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[E];
+      unpack16(raw[u], v, T());
+      sq[u] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        mx = fmaxf(mx, fabsf(v[u][e]));
-        if (NORM) sq = fmaf(v[u][e], v[u][e], sq);
+        mx = fmaxf(mx, fabsf(v[e]));
+        if (NORM) sq[u] = fmaf(v[e], v[e], sq[u]);
       }
-      if (NORM) {
+    }
+    if (NORM) {
+      int n = U;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        if (sq > 1.0e-30f && sq < 1.0e36f) {
-          nm = fmaxf(nm, sqrtf(sq));
-        } else {   // zeros, or squares outside fp32's range: over the row's largest value
-          float top = 0.f, s2 = 0.f;
+      for (int o = L / 2; o; o >>= 1) {
+        if (n > 1) {
+          n /= 2;
 #pragma unroll
-          for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(v[u][e]));
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (top > 0.f) {
+          for (int j = 0; j < U / 2; ++j)
+            if (j < n) {
+              const bool up = lane & o;
+              const float keep = up ? sq[j + n] : sq[j], send = up ? sq[j] : sq[j + n];
+              sq[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        } else {
+          sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], o);
+        }
+      }
+      float top = sq[0], low = sq[0];   // (every row's sum is in some lane; n is 1 for all shapes: L >= 8)
+      for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      }
+      if (low > 1.0e-30f && top < 1.0e36f) {
+        nm = fmaxf(nm, sqrtf(top));
+      } else {   // zeros, or squares outside fp32's range: each row over its largest value
 #pragma unroll
-            for (int e = 0; e < E; ++e) s2 = fmaf(v[u][e] / top, v[u][e] / top, s2);
-            for (int o = 16; o; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-            nm = fmaxf(nm, top * sqrtf(s2));
-          }
+        for (int u = 0; u < U; ++u) {
+          float v[E], m = 0.f, s2 = 0.f;
+          unpack16(raw[u], v, T());
+#pragma unroll
+          for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(v[e]));
+          for (int o = L / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+          for (int e = 0; e < E; ++e) s2 = m > 0.f ? fmaf(v[e] / m, v[e] / m, s2) : 0.f;
+          for (int o = L / 2; o; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+          nm = fmaxf(nm, m * sqrtf(s2));
         }
       }
     }
@@ -231,44 +248,64 @@ __global__ void __launch_bounds__(kRangeThreads) range_kernel(PackedBwdPlan pl, 
 }
 
 // ---------------------------------------------------------------- operand layout
-// E = hd / 32 values of a lane times `scale`, as one or two fp16 planes `plane`
-// apart; v becomes what the planes hold.
-template <int E>
-__device__ __forceinline__ void put_planes(__half* dst, size_t plane, int planes, float scale, float* v) {
-  __half2 h[E / 2], l[E / 2];
+// Eight values of a lane from 16 bytes of T (bf16) or 32 (fp32).
+template <typename T>
+struct Values8 {
+  uint4 raw[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, bool aligned) {
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float x = v[e] * scale, y = v[e + 1] * scale;
-    h[e / 2] = __floats2half2_rn(x, y);
-    float2 f = __half22float2(h[e / 2]);
-    l[e / 2] = __floats2half2_rn(x - f.x, y - f.y);
-    v[e] = f.x;
-    v[e + 1] = f.y;
-    if (planes == 2) {
-      f = __half22float2(l[e / 2]);
-      v[e] += f.x;
-      v[e + 1] += f.y;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = load16(p + i * (16 / sizeof(T)), aligned);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) unpack16(raw[i], v + i * (16 / (int)sizeof(T)), T());
+  }
+};
+
+// Eight values times `scale` as one or two fp16 planes `plane` apart; v becomes
+// what the planes hold.
+template <int PL>
+__device__ __forceinline__ void put_planes(__half* dst, size_t plane, float scale, float* v) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float x = v[2 * j] * scale, y = v[2 * j + 1] * scale;
+    const __half2 a = __floats2half2_rn(x, y);
+    h[j] = *reinterpret_cast<const uint32_t*>(&a);
+    float2 f = __half22float2(a);
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+    if (PL == 2) {
+      const __half2 b = __floats2half2_rn(x - f.x, y - f.y);
+      l[j] = *reinterpret_cast<const uint32_t*>(&b);
+      f = __half22float2(b);
+      v[2 * j] += f.x;
+      v[2 * j + 1] += f.y;
     }
   }
-  auto put = [&](__half* d, const __half2* x) {
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(x);
-    else
-      *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(x);
-  };
-  put(dst, h);
-  if (planes == 2) put(dst + plane, l);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (PL == 2) *reinterpret_cast<uint4*>(dst + plane) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// One warp per row: query rows (with D and lse), then the blocks' own keys and
+// A warp takes a few heads of a row at a time (32 * 8 / hd of them side by side,
+// kPackUnroll times): query rows (with D and lse), then the blocks' own keys and
 // values, then the context's.  Bound by HBM: q, out and d_out are read once.
-template <typename T, int HD>
+constexpr int kPackUnroll = 2;
+template <int HD> __host__ __device__ constexpr int pack_heads() { return 256 / HD * kPackUnroll; }
+
+template <typename T, int HD, int PL>
 __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedBwdTensors t) {
   griddep_wait();
   griddep_trigger();
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31, g = pl.block, rows = pl.T * kRows, ctx = pl.KT * kRows;
-  const long long n_q = (long long)rows * pl.nq, n_b = (long long)rows * pl.nkv, n_c = (long long)ctx * pl.nkv;
+  constexpr int L = HD / 8, R = 32 / L, U = kPackUnroll, H = pack_heads<HD>();
+  const int lane = threadIdx.x & 31, sub = lane / L, col = lane % L * 8;
+  const int g = pl.block, rows = pl.T * kRows, ctx = pl.KT * kRows;
+  const int q_groups = (pl.nq + H - 1) / H, k_groups = (pl.nkv + H - 1) / H;
+  const long long n_q = (long long)rows * q_groups, n_b = (long long)rows * k_groups, n_c = (long long)ctx * k_groups;
   const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
   // the CTAs' maxima become the scales
   __shared__ float s_max[kRangeValues];
@@ -294,6 +331,7 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
   __syncthreads();
   const float f_q = pow2(s_sc.q), f_k = pow2(s_sc.k), f_v = pow2(s_sc.v), f_o = pow2(s_sc.o);
   const int e_d = s_sc.dp - s_sc.o;   // D is summed over the scaled d_out
+  const bool al_q = aligned16(t.q), al_g = aligned16(t.d_out), al_o = aligned16(t.out);
   // block and position of a row; -1: padding
   auto place = [&](int r, int& n, int& i) {
     const int k = r % kRows, b = k / g, at = (r / kRows) * pl.per + b;
@@ -302,55 +340,102 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
     return at;
   };
   for (long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n_q + n_b + n_c; w += warps) {
-    float a[E] = {}, b[E] = {}, c[E] = {};
     if (w < n_q) {
-      const int h = (int)(w % pl.nq), r = (int)(w / pl.nq);
+      const int r = (int)(w / q_groups), h0 = (int)(w - (long long)r * q_groups) * H + sub;
       int n, i;
       const int at = place(r, n, i);
-      float d = 0.f, l = INFINITY;
-      if (n >= 0) {
-        const size_t row = ((size_t)n * g + i) * pl.nq + h, o = row * HD + E * lane;
-        load_values<E>(static_cast<const T*>(t.q) + o, a);
-        load_values<E>(t.d_out + o, b);
-        load_values<E>(t.out + o, c);
-        l = fmaf(t.lse[row], kLog2e, -(float)kPExp);
-      }
-      const size_t dst = ((size_t)h * pl.planes * rows + r) * HD + E * lane, plane = (size_t)rows * HD;
-      put_planes<E>(pl.q + dst, plane, pl.planes, f_q, a);
-      put_planes<E>(pl.d_o + dst, plane, pl.planes, f_o, b);
-      // D from d_out as the products see it: its rounding then cancels in dp - D as exactly as d_out itself would
+      const size_t row = ((size_t)(n < 0 ? 0 : n) * g + i) * pl.nq;
+      Values8<T> q[U];
+      Values8<float> go[U], oo[U];
+      float l[U];
 #pragma unroll
-      for (int e = 0; e < E; ++e) d = fmaf(b[e], c[e], d);
-      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (lane == 0) {
-        pl.lse2[(size_t)h * rows + r] = l;
-        pl.delta[(size_t)h * rows + r] = ldexpf(d, e_d);
-        if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : 0;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R;
+        if (n >= 0 && h < pl.nq) {
+          const size_t o = (row + h) * HD + col;
+          q[u].load(static_cast<const T*>(t.q) + o, al_q);
+          go[u].load(t.d_out + o, al_g);
+          oo[u].load(t.out + o, al_o);
+          l[u] = fmaf(t.lse[row + h], kLog2e, -(float)kPExp);
+        } else {
+          q[u].zero();
+          go[u].zero();
+          oo[u].zero();
+          l[u] = INFINITY;
+        }
       }
-    } else if (w < n_q + n_b) {
-      const long long u = w - n_q;
-      const int h = (int)(u % pl.nkv), r = (int)(u / pl.nkv);
-      int n, i;
-      place(r, n, i);
-      if (n >= 0) {
-        const size_t o = (((size_t)n * g + i) * pl.nkv + h) * HD + E * lane;
-        load_values<E>(static_cast<const T*>(t.k_blk) + o, a);
-        load_values<E>(static_cast<const T*>(t.v_blk) + o, b);
+      float d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R;
+        float a[8], b[8], c[8];
+        q[u].get(a);
+        go[u].get(b);
+        oo[u].get(c);
+        d[u] = 0.f;
+        if (h < pl.nq) {
+          const size_t dst = ((size_t)h * PL * rows + r) * HD + col, plane = (size_t)rows * HD;
+          put_planes<PL>(pl.q + dst, plane, f_q, a);
+          put_planes<PL>(pl.d_o + dst, plane, f_o, b);
+          // D from d_out as the products see it: its rounding then cancels in dp - D as exactly as d_out itself would
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[u] = fmaf(b[e], c[e], d[u]);
+        }
       }
-      const size_t dst = ((size_t)h * pl.planes * rows + r) * HD + E * lane, plane = (size_t)rows * HD;
-      put_planes<E>(pl.kb + dst, plane, pl.planes, f_k, a);
-      put_planes<E>(pl.vb + dst, plane, pl.planes, f_v, b);
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
+      if (col == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int h = h0 + u * R;
+          if (h < pl.nq) {
+            pl.lse2[(size_t)h * rows + r] = l[u];
+            pl.delta[(size_t)h * rows + r] = ldexpf(d[u], e_d);
+            if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : 0;
+          }
+        }
+      }
     } else {
-      const long long u = w - n_q - n_b;
-      const int h = (int)(u % pl.nkv), r = (int)(u / pl.nkv);
-      if (r < pl.S) {
-        const size_t o = ((size_t)r * pl.nkv + h) * HD + E * lane;
-        load_values<E>(static_cast<const T*>(t.k_ctx) + o, a);
-        load_values<E>(static_cast<const T*>(t.v_ctx) + o, b);
+      const bool blk = w < n_q + n_b;
+      const long long x = blk ? w - n_q : w - n_q - n_b;
+      const int r = (int)(x / k_groups), h0 = (int)(x - (long long)r * k_groups) * H + sub, slab = blk ? rows : ctx;
+      long long row = -1;   // of [tokens][nkv]
+      if (blk) {
+        int n, i;
+        place(r, n, i);
+        if (n >= 0) row = ((long long)n * g + i) * pl.nkv;
+      } else if (r < pl.S) {
+        row = (long long)r * pl.nkv;
       }
-      const size_t dst = ((size_t)h * pl.planes * ctx + r) * HD + E * lane, plane = (size_t)ctx * HD;
-      put_planes<E>(pl.kc + dst, plane, pl.planes, f_k, a);
-      put_planes<E>(pl.vc + dst, plane, pl.planes, f_v, b);
+      const T* k = static_cast<const T*>(blk ? t.k_blk : t.k_ctx);
+      const T* v = static_cast<const T*>(blk ? t.v_blk : t.v_ctx);
+      const bool al_k = aligned16(k), al_v = aligned16(v);
+      Values8<T> ks[U], vs[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R;
+        if (row >= 0 && h < pl.nkv) {
+          ks[u].load(k + (size_t)(row + h) * HD + col, al_k);
+          vs[u].load(v + (size_t)(row + h) * HD + col, al_v);
+        } else {
+          ks[u].zero();
+          vs[u].zero();
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * R;
+        float a[8], b[8];
+        ks[u].get(a);
+        vs[u].get(b);
+        if (h < pl.nkv) {
+          const size_t dst = ((size_t)h * PL * slab + r) * HD + col, plane = (size_t)slab * HD;
+          put_planes<PL>((blk ? pl.kb : pl.kc) + dst, plane, f_k, a);
+          put_planes<PL>((blk ? pl.vb : pl.vc) + dst, plane, f_v, b);
+        }
+      }
     }
   }
 }
@@ -1127,9 +1212,10 @@ cudaError_t run_grad(const PackedBwdPlan& pl, const PackedBwdTensors& t, int sms
                              dim3(kRangeThreads), 0, s, pl, t);
   if (e != cudaSuccess) return e;
   ++*launches;
-  const long long warps = (long long)rows * (pl.nq + pl.nkv) + (long long)ctx * pl.nkv;
+  auto heads = [](int n) { return (n + pack_heads<HD>() - 1) / pack_heads<HD>(); };
+  const long long warps = (long long)rows * (heads(pl.nq) + heads(pl.nkv)) + (long long)ctx * heads(pl.nkv);
   const int grid = (int)std::min<long long>((warps + 7) / 8, (long long)sms * 8);
-  e = launch_pdl(pack_bwd_kernel<T, HD>, dim3(grid), dim3(256), 0, s, pl, t);
+  e = launch_pdl(pack_bwd_kernel<T, HD, PL>, dim3(grid), dim3(256), 0, s, pl, t);
   if (e != cudaSuccess) return e;
   ++*launches;
   GradMaps m;
