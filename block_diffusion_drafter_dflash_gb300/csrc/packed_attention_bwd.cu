@@ -458,6 +458,12 @@ constexpr uint32_t idesc_f16(int M, int N) {
 }
 constexpr uint32_t kBMajorMN = 1u << 16;
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
 // D[tmem] (+)= A[smem] B[smem]'
 __device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -574,24 +580,29 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-// C values as C / 2 columns of fp16 pairs from column `at` on and, with two
-// planes, their rounding residuals in the next C / 2: the C columns that the
-// values were read from.
-template <int PL, int C>
-__device__ __forceinline__ void put_pairs(uint32_t at, const float* v) {
-  uint32_t h[C / 2], l[C / 2];
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+// C values as C / 2 registers of fp16 pairs.
+template <int C>
+__device__ __forceinline__ void pairs_of(const float* v, uint32_t* h) {
 #pragma unroll
-  for (int j = 0; j < C / 2; ++j) {
-    __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-    h[j] = *reinterpret_cast<uint32_t*>(&b);
-    if (PL == 2) {
-      const float2 f = __half22float2(b);
-      __half2 r = __floats2half2_rn(v[2 * j] - f.x, v[2 * j + 1] - f.y);
-      l[j] = *reinterpret_cast<uint32_t*>(&r);
-    }
-  }
+  for (int j = 0; j < C / 2; ++j) h[j] = as_u32(__floats2half2_rn(v[2 * j], v[2 * j + 1]));
+}
+// The pairs into C / 2 columns from `at` on and, with two planes, the values'
+// rounding residuals into the next C / 2: the C columns that the values were read
+// from.
+template <int PL, int C>
+__device__ __forceinline__ void put_pairs(uint32_t at, const uint32_t* h, const float* v) {
   tmem_st<C / 2>(at, h);
-  if (PL == 2) tmem_st<C / 2>(at + C / 2, l);
+  if (PL == 2) {
+    uint32_t l[C / 2];
+#pragma unroll
+    for (int j = 0; j < C / 2; ++j) {
+      const float2 f = __half22float2(as_half2(h[j]));
+      l[j] = as_u32(__floats2half2_rn(v[2 * j] - f.x, v[2 * j + 1] - f.y));
+    }
+    tmem_st<C / 2>(at + C / 2, l);
+  }
 }
 
 // ---------------------------------------------------------------- the gradient kernel
@@ -794,8 +805,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 
   auto str0 = [&](int i) { return sm + C::kOff0 + (i % C::kS0) * C::kStr; };
   auto str1 = [&](int i) { return sm + C::kOff1 + (i % C::kS1) * C::kStr; };
-  auto lse_of = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (i % C::kS0) * C::kStat); };
-  auto delta_of = [&](int i) { return reinterpret_cast<float*>(sm + C::kOffStat + (C::kS0 + i % C::kS1) * C::kStat); };
+  auto lse_of = [&](int i) { return sm + C::kOffStat + (i % C::kS0) * C::kStat; };
+  auto delta_of = [&](int i) { return sm + C::kOffStat + (C::kS0 + i % C::kS1) * C::kStat; };
   auto par0 = [](int i) { return static_cast<uint32_t>(i / C::kS0) & 1u; };
   auto par1 = [](int i) { return static_cast<uint32_t>(i / C::kS1) & 1u; };
   bool ok = true;
@@ -863,71 +874,124 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       }
     }
   } else if (warp == kSoftWarps + 1) {
-    if (lane == 0) {   // ------------------------------------------------ MMAs
-      auto wait = [&](uint64_t* b, uint32_t p) {
+    // ------------------------------------------------ MMAs
+    // The whole warp runs this, so that what it computes is uniform; one elected
+    // lane issues each group of MMAs with the commits behind it.
+    auto wait = [&](uint64_t* b, uint32_t p) {
+      if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(b, p))) {
         ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status);
-        ptx::tc_fence_after();
-        return ok;
-      };
-      const uint32_t ra = desc_k(sm), rb = desc_k(sm + C::kRes);
-      const uint32_t k0 = desc_k(sm + C::kOff0), k1 = desc_k(sm + C::kOff1);
-      const uint32_t g0 = desc_mn(sm + C::kOff0, C::kStrTile), g1 = desc_mn(sm + C::kOff1, C::kStrTile);
-      auto o0 = [](int i) { return (uint32_t)(i % C::kS0) * (C::kStr >> 4); };
-      auto o1 = [](int i) { return (uint32_t)(i % C::kS1) * (C::kStr >> 4); };
-      wait(&bars->res_full, 0);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      ptx::tc_fence_after();
+      return ok;
+    };
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t ra = desc_k(sm), rb = desc_k(sm + C::kRes);
+    const uint32_t k0 = desc_k(sm + C::kOff0), k1 = desc_k(sm + C::kOff1);
+    const uint32_t g0 = desc_mn(sm + C::kOff0, C::kStrTile), g1 = desc_mn(sm + C::kOff1, C::kStrTile);
+    constexpr uint32_t kStep = C::kStr >> 4;
+    // a stage of each stream: this tile's, and the next one's with its phase
+    int s0 = 0, s1 = 0, n0 = 0, n1 = 0;
+    uint32_t ph0 = 0, ph1 = 0;
+    auto arrived0 = [&] { return wait(&bars->full0[n0], ph0); };
+    auto arrived1 = [&] { return wait(&bars->full1[n1], ph1); };
+    auto next0 = [&] { if (++n0 == C::kS0) n0 = 0, ph0 ^= 1; };
+    auto next1 = [&] { if (++n1 == C::kS1) n1 = 0, ph1 ^= 1; };
+    // The next tiles are waited for before what the warps are still at, so that
+    // the MMAs of both products go out together (with a single stage the next
+    // tile of the second stream comes only after dV).
+    constexpr bool kAhead = C::kS1 > 1;
+    if (wait(&bars->res_full, 0) && arrived0() && arrived1()) {
       if (kind != 1) {
         // resident K, V; streamed Q, dO
-        const uint32_t tS = tmem, tP = tmem + C::kColP, tV = tmem + C::kColV, tK = tmem + C::kColK;
-        auto scores = [&](int i) {
-          if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
-          mma_scores<HD, PL>(tS, ra, k0 + o0(i));
+        const uint32_t tS = tm, tP = tm + C::kColP, tV = tm + C::kColV, tK = tm + C::kColK;
+        if (elect()) {
+          mma_scores<HD, PL>(tS, ra, k0);
           ptx::mma_commit(&bars->s_full);
-          return true;
-        };
-        auto dprob = [&](int i) {
-          if (!wait(&bars->full1[i % C::kS1], par1(i))) return false;
-          mma_scores<HD, PL>(tP, rb, k1 + o1(i));
+          mma_scores<HD, PL>(tP, rb, k1);
           ptx::mma_commit(&bars->dp_full);
-          return true;
-        };
-        if (ok && scores(0)) dprob(0);
-        for (int i = 0; i < n && ok; ++i) {
+        }
+        __syncwarp();
+        next0();
+        next1();
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n;
+          if (more && !arrived0()) break;
           if (!wait(&bars->p_ready, i & 1)) break;
-          mma_gradient<HD, PL>(tV, tS, g1 + o1(i), i > 0);
-          ptx::mma_commit(&bars->freed1[i % C::kS1]);
-          if (i + 1 < n && !scores(i + 1)) break;
+          if (elect()) {
+            mma_gradient<HD, PL>(tV, tS, g1 + s1 * kStep, i > 0);
+            ptx::mma_commit(&bars->freed1[s1]);
+            if (more) {
+              mma_scores<HD, PL>(tS, ra, k0 + n0 * kStep);
+              ptx::mma_commit(&bars->s_full);
+            }
+          }
+          __syncwarp();
+          if (more && kAhead && !arrived1()) break;
           if (!wait(&bars->ds_ready[0], i & 1)) break;
-          mma_gradient<HD, PL>(tK, tP, g0 + o0(i), i > 0);
-          ptx::mma_commit(&bars->freed0[i % C::kS0]);
-          if (i + 1 < n && !dprob(i + 1)) break;
+          if (elect()) {
+            mma_gradient<HD, PL>(tK, tP, g0 + s0 * kStep, i > 0);
+            ptx::mma_commit(&bars->freed0[s0]);
+          }
+          __syncwarp();
+          if (more) {
+            if (!kAhead && !arrived1()) break;
+            if (elect()) {
+              mma_scores<HD, PL>(tP, rb, k1 + n1 * kStep);
+              ptx::mma_commit(&bars->dp_full);
+            }
+            __syncwarp();
+          }
+          s0 = n0;
+          s1 = n1;
+          next0();
+          next1();
         }
       } else {
         // resident Q, dO; streamed K, V
-        auto scores = [&](int i) {
-          if (!wait(&bars->full0[i % C::kS0], par0(i))) return false;
-          mma_scores<HD, PL>(tmem + (i & 1) * 128, ra, k0 + o0(i));
-          return true;
-        };
-        auto dprob = [&](int i) {
-          if (!wait(&bars->full1[i % C::kS1], par1(i))) return false;
-          mma_scores<HD, PL>(tmem + C::kColPRows, rb, k1 + o1(i));
+        const uint32_t tP = tm + C::kColPRows;
+        if (elect()) {
+          mma_scores<HD, PL>(tm, ra, k0);
+          mma_scores<HD, PL>(tP, rb, k1);
           ptx::mma_commit(&bars->s_full);
-          ptx::mma_commit(&bars->freed1[i % C::kS1]);
-          return true;
-        };
-        if (ok && scores(0)) dprob(0);
-        for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n && !scores(i + 1)) break;    // over dS(i - 1), which the last dQ has taken
+          ptx::mma_commit(&bars->freed1[0]);
+        }
+        __syncwarp();
+        next0();
+        next1();
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n;
+          if (more) {
+            if (!arrived0()) break;
+            if (elect()) mma_scores<HD, PL>(tm + (~i & 1) * 128, ra, k0 + n0 * kStep);   // over dS(i - 1), which the last dQ has taken
+            __syncwarp();
+            if (!arrived1()) break;
+          }
           if (!wait(&bars->p_ready, i & 1)) break;   // dP(i) is in registers
-          if (i + 1 < n && !dprob(i + 1)) break;
+          if (more) {
+            if (elect()) {
+              mma_scores<HD, PL>(tP, rb, k1 + n1 * kStep);
+              ptx::mma_commit(&bars->s_full);
+              ptx::mma_commit(&bars->freed1[n1]);
+            }
+            __syncwarp();
+          }
           if (!wait(&bars->ds_ready[i & 1], (i >> 1) & 1)) break;
-          mma_gradient<HD, PL>(tmem + C::kColQ, tmem + (i & 1) * 128, g0 + o0(i), i > 0);
-          ptx::mma_commit(&bars->freed0[i % C::kS0]);
+          if (elect()) {
+            mma_gradient<HD, PL>(tm + C::kColQ, tm + (i & 1) * 128, g0 + s0 * kStep, i > 0);
+            ptx::mma_commit(&bars->freed0[s0]);
+          }
+          __syncwarp();
+          s0 = n0;
+          s1 = n1;
+          next0();
+          next1();
         }
       }
-      ptx::mma_commit(&bars->done);
-      if (!ok) ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTA does
     }
+    if (elect()) ptx::mma_commit(&bars->done);
+    __syncwarp();
+    if (!ok) ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTA does
   } else {   // ---------------------------------------------------------------------- softmax
     constexpr int NC = C::kCols;
     const int q4 = warp & 3, part = warp >> 2, me = 32 * q4 + lane;   // my lane of tensor memory
@@ -943,8 +1007,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       if (lane == 0) ptx::mbar_arrive(b);
     };
     auto wait = [&](uint64_t* b, uint32_t p) {
-      ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status);
-      ok = __all_sync(0xffffffffu, ok);
+      if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(b, p))) {
+        ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status);
+        ok = __all_sync(0xffffffffu, ok);
+      }
       ptx::tc_fence_after();
       return ok;
     };
@@ -989,12 +1055,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       const uint32_t tS = tmem + lanes + c0, tP = tS + C::kColP;
       const int key = tile * kRows + me;
       int in_head = u0 % per_head;            // streamed tile within its head
+      int s0 = 0, s1 = 0;                     // stages of the two streams and their phases
+      uint32_t ph0 = 0, ph1 = 0;
+      // The columns' lse2 and delta are read ahead, while the warps wait for S and
+      // dP: MMAs with both operands in shared memory take its whole bandwidth,
+      // and a load in the middle of the arithmetic waits for them.
+      float4 st[NC / 4];
+      auto load_stats = [&](int slot) {
+        const float4* x = reinterpret_cast<const float4*>(sm + C::kOffStat + slot * C::kStat) + c0 / 4;
+#pragma unroll
+        for (int j = 0; j < NC / 4; ++j) st[j] = x[j];
+      };
+      if (wait(&bars->full0[0], 0)) load_stats(0);
       for (int i = 0; i < n; ++i) {
         const int r0 = row0 + in_head * C::kN + c0;   // my first column's row
         const bool compare = kind == 2 || r0 < whole * kRows;
         if (++in_head == per_head) in_head = 0;
-        if (!wait(&bars->full0[i % C::kS0], par0(i)) || !wait(&bars->s_full, i & 1)) break;
-        const float* lse2 = lse_of(i) + c0;
+        if (!wait(&bars->s_full, i & 1)) break;
+        // P: as the fp16 pairs that enter dV and, with two planes, as fp32
+        uint32_t pairs[NC / 2];
         float p[NC];
         {
           uint32_t raw[NC];
@@ -1004,7 +1083,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         }
 #pragma unroll
         for (int j = 0; j < NC; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(lse2 + j);
+          const float4 l = st[j / 4];
           const float2 a = fma2(make_float2(p[j], p[j + 1]), make_float2(sc2, sc2), make_float2(-l.x, -l.y));
           const float2 b = fma2(make_float2(p[j + 2], p[j + 3]), make_float2(sc2, sc2), make_float2(-l.z, -l.w));
           p[j] = ex2(a.x);
@@ -1020,11 +1099,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
             if (!seen) p[j] = 0.f;
           }
         }
-        put_pairs<PL, NC>(tS, p);
+        pairs_of<NC>(p, pairs);
+        put_pairs<PL, NC>(tS, pairs, p);
         tmem_st_wait();
         arrive(&bars->p_ready);
-        if (!wait(&bars->full1[i % C::kS1], par1(i)) || !wait(&bars->dp_full, i & 1)) break;
-        const float* delta = delta_of(i) + c0;
+        if (!wait(&bars->full1[s1], ph1)) break;
+        load_stats(C::kS0 + s1);
+        if (++s1 == C::kS1) s1 = 0, ph1 ^= 1;
+        if (!wait(&bars->dp_full, i & 1)) break;
+        uint32_t hi[NC / 2];
         float d[NC];
         {
           uint32_t raw[NC];
@@ -1032,21 +1115,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           tmem_ld_wait();
           tmem_values<NC>(raw, d);
         }
+        const float2 f = make_float2(f_dp, f_dp);
 #pragma unroll
         for (int j = 0; j < NC; j += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(delta + j);
-          const float2 f = make_float2(f_dp, f_dp);
-          const float2 a = mul2(make_float2(p[j], p[j + 1]), fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y)));
-          const float2 b = mul2(make_float2(p[j + 2], p[j + 3]),
-                                fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w)));
-          d[j] = a.x;
-          d[j + 1] = a.y;
-          d[j + 2] = b.x;
-          d[j + 3] = b.y;
+          const float4 x = st[j / 4];
+          const float2 a = fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y));
+          const float2 b = fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w));
+          if (PL == 1) {   // at most 1, and P at most 2^14: their product in fp16
+            hi[j / 2] = as_u32(__hmul2(as_half2(pairs[j / 2]), __floats2half2_rn(a.x, a.y)));
+            hi[j / 2 + 1] = as_u32(__hmul2(as_half2(pairs[j / 2 + 1]), __floats2half2_rn(b.x, b.y)));
+          } else {
+            const float2 u = mul2(make_float2(p[j], p[j + 1]), a), v = mul2(make_float2(p[j + 2], p[j + 3]), b);
+            d[j] = u.x, d[j + 1] = u.y, d[j + 2] = v.x, d[j + 3] = v.y;
+          }
         }
-        put_pairs<PL, NC>(tP, d);
+        if (PL == 2) pairs_of<NC>(d, hi);
+        put_pairs<PL, NC>(tP, hi, d);
         tmem_st_wait();
         arrive(&bars->ds_ready[0]);
+        if (++s0 == C::kS0) s0 = 0, ph0 ^= 1;
+        if (i + 1 < n) {
+          if (!wait(&bars->full0[s0], ph0)) break;
+          load_stats(s0);
+        }
       }
       // ---- dV and dK of my key: the warps of a lane quarter take the 32-column groups of both in turn
       wait(&bars->done, 0);
@@ -1116,7 +1207,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           for (int j = 0; j < NC; ++j)
             if (j < from || j >= from + count) s[j] = 0.f;
         }
-        put_pairs<PL, NC>(tS, s);
+        uint32_t hi[NC / 2];
+        pairs_of<NC>(s, hi);
+        put_pairs<PL, NC>(tS, hi, s);
         tmem_st_wait();
         arrive(&bars->ds_ready[i & 1]);
       }
