@@ -48,6 +48,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "gemm.cuh"
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
           if (h < pl.nq) {
             pl.lse2[(size_t)h * rows + r] = l[u];
             pl.delta[(size_t)h * rows + r] = ldexpf(d[u], e_d);
-            if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : 0;
+            if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : INT_MAX;
           }
         }
       }
@@ -582,6 +583,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
+// Zero but for columns [from, to) of C.
+template <int C>
+__device__ __forceinline__ void keep_columns(float* v, int from, int to) {
+  const uint32_t below = from <= 0 ? 0u : from >= 32 ? ~0u : (1u << from) - 1;
+  const uint32_t bits = (to <= 0 ? 0u : to >= 32 ? ~0u : (1u << to) - 1) & ~below;
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (!(bits >> j & 1)) v[j] = 0.f;
+}
 // C values as C / 2 registers of fp16 pairs.
 template <int C>
 __device__ __forceinline__ void pairs_of(const float* v, uint32_t* h) {
@@ -1072,6 +1082,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         const bool compare = kind == 2 || r0 < whole * kRows;
         if (++in_head == per_head) in_head = 0;
         if (!wait(&bars->s_full, i & 1)) break;
+        const int anchor = kind == 0 && compare ? __ldg(pl.row_anchor + r0 + lane % NC) : 0;   // of column `lane`
         // P: as the fp16 pairs that enter dV and, with two planes, as fp32
         uint32_t pairs[NC / 2];
         float p[NC];
@@ -1092,12 +1103,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           p[j + 3] = ex2(b.y);
         }
         if (compare) {
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const bool seen = kind == 0 ? __ldg(pl.row_anchor + r0 + j) > key
-                                        : static_cast<unsigned>(r0 + j - row0 - own * pl.block) < static_cast<unsigned>(pl.block);
-            if (!seen) p[j] = 0.f;
+          int from = own * pl.block - (r0 - row0), to = from + pl.block;   // own keys: my block's rows
+          if (kind == 0) {   // the rows from the first one anchored behind my key on (anchors ascend)
+            from = 0;
+            to = NC;
+#pragma unroll 1
+            for (int step = NC / 2; step; step /= 2)
+              if (__shfl_sync(0xffffffffu, anchor, from + step - 1) <= key) from += step;
+            if (__shfl_sync(0xffffffffu, anchor, from) <= key) ++from;
           }
+          keep_columns<NC>(p, from, to);
         }
         pairs_of<NC>(p, pairs);
         put_pairs<PL, NC>(tS, pairs, p);
@@ -1202,11 +1217,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           s[j] = x.x;
           s[j + 1] = x.y;
         }
-        if (!all) {
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (j < from || j >= from + count) s[j] = 0.f;
-        }
+        if (!all) keep_columns<NC>(s, from, from + count);
         uint32_t hi[NC / 2];
         pairs_of<NC>(s, hi);
         put_pairs<PL, NC>(tS, hi, s);

@@ -26,7 +26,7 @@ struct PackedBwdPlan {
   int32_t* scale;         // [5] exponents of the powers of two the operands are scaled by (Scales)
   int32_t* order;         // [N] block of each sorted place
   int32_t* sorted;        // [N] anchors in ascending order
-  int32_t* row_anchor;    // [T*128] anchor of the row's block (0 in padding)
+  int32_t* row_anchor;    // [T*128] anchor of the row's block (INT_MAX in padding)
   float* lse2;            // [nq][T*128] lse log2(e) - kPExp, +inf in padding
   float* delta;           // [nq][T*128] sum_d d_out out, scaled as dp
   __half* q;              // [nq][planes][T*128][hd], zero in padding (d_o, kb and vb too)
