@@ -127,15 +127,18 @@ __device__ __forceinline__ S square_sum(const uint4* r, bool bf16) {
   return s;
 }
 
-// Sum of one double per thread, in every thread of warp 0's lane 0 (fixed order).
+// Sum of one double per thread, in thread 0, in a fixed order.  The warps' double
+// units are few, so one warp adds for all.
 __device__ __forceinline__ double block_sum(double v, double* sh) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  sh[threadIdx.x] = v;
   __syncthreads();
   double t = 0.0;
-  for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
-  __syncthreads();
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += sh[threadIdx.x + 32 * w];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
   return t;
 }
 
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_square_sum_kernel(c
                                                                               double* partial, int accumulate) {
   griddep_wait();
   griddep_trigger();
-  __shared__ double sh[kThreads / 32];
+  __shared__ double sh[kThreads];
   double sum = 0.0;
   for (long long c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const Entry& e = t.e[find_entry(t, c)];
@@ -180,14 +183,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
                                                                          int in_place) {
   griddep_wait();
   griddep_trigger();
-  __shared__ double sh[kThreads / 32];
+  __shared__ double sh[kThreads];
+  __shared__ float s_factor;   // negative: no clipping
   double v = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) v += partial[i];
-  const double norm = sqrt(block_sum(v, sh));
-  if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = (float)norm;
-  const bool clip = norm > (double)max_norm && norm <= 1.7976931348623157e308;   // false for NaN and infinity
+  v = block_sum(v, sh);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(v);
+    if (blockIdx.x == 0 && norm_out) *norm_out = (float)norm;
+    const bool over = norm > (double)max_norm && norm <= 1.7976931348623157e308;   // false for NaN and infinity
+    s_factor = over ? (float)((double)max_norm / norm) : -1.f;
+  }
+  __syncthreads();
+  const float f = s_factor;
+  const bool clip = f >= 0.f;
   if (!clip && in_place) return;
-  const float f = clip ? (float)((double)max_norm / norm) : 1.f;
   for (long long c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const Entry& e = t.e[find_entry(t, c)];
     const bool bf16 = e.first & 1;

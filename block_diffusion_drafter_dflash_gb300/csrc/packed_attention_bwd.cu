@@ -72,6 +72,12 @@ struct Scales {
   int q, k, v, o, dp;
 };
 __device__ __forceinline__ float pow2(int e) { return ldexpf(1.f, e); }
+// v 2^e in two exact steps, each within fp32's range.
+struct Pow2 {
+  float a, b;
+  __device__ __forceinline__ explicit Pow2(int e) : a(pow2(e / 2)), b(pow2(e - e / 2)) {}
+  __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
+};
 // The exponent that brings m into [2^14, 2^15), within what a float holds.
 __device__ __forceinline__ int scale_exp(float m) {
   if (!(m > 0.f) || isinf(m)) return 0;
@@ -158,6 +164,7 @@ __device__ __forceinline__ void range_rows(const T* x, long long rows, int part,
       if (r < rows) raw[u] = load16(x + (size_t)r * HD + col, aligned);
     }
     float sq[U];
+    bool odd = false;   // a square may have left fp32's range
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[E];
@@ -168,6 +175,7 @@ __device__ __forceinline__ void range_rows(const T* x, long long rows, int part,
         mx = fmaxf(mx, fabsf(v[e]));
         if (NORM) sq[u] = fmaf(v[e], v[e], sq[u]);
       }
+      if (NORM) odd |= !(sq[u] < 1.0e36f) || (sq[u] < 1.0e-30f && (raw[u].x | raw[u].y | raw[u].z | raw[u].w) != 0);
     }
     if (NORM) {
       int n = U;
@@ -186,14 +194,9 @@ __device__ __forceinline__ void range_rows(const T* x, long long rows, int part,
           sq[0] += __shfl_xor_sync(0xffffffffu, sq[0], o);
         }
       }
-      float top = sq[0], low = sq[0];   // (every row's sum is in some lane; n is 1 for all shapes: L >= 8)
-      for (int o = 16; o; o >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-      }
-      if (low > 1.0e-30f && top < 1.0e36f) {
-        nm = fmaxf(nm, sqrtf(top));
-      } else {   // zeros, or squares outside fp32's range: each row over its largest value
+      if (!__any_sync(0xffffffffu, odd)) {   // (every row's sum is in some lane; n is 1 for all shapes: L >= 8)
+        nm = fmaxf(nm, sqrtf(sq[0]));
+      } else {   // each row over its largest value
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float v[E], m = 0.f, s2 = 0.f;
@@ -330,6 +333,21 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
     }
   }
   __syncthreads();
+  // Each key tile's first row tile whose last block is anchored behind the tile's
+  // first key, and first one whose first block is anchored behind all its keys.
+  for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < pl.KT; j += gridDim.x * blockDim.x) {
+    int lo = 0, hi = pl.T;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pl.sorted[min((mid + 1) * pl.per, pl.N) - 1] > j * kRows) hi = mid; else lo = mid + 1;
+    }
+    const int first = lo;
+    for (hi = pl.T; lo < hi;) {
+      const int mid = (lo + hi) >> 1;
+      if (pl.sorted[mid * pl.per] >= (j + 1) * kRows) hi = mid; else lo = mid + 1;
+    }
+    pl.seen_by[j] = make_int2(first, lo);
+  }
   const float f_q = pow2(s_sc.q), f_k = pow2(s_sc.k), f_v = pow2(s_sc.v), f_o = pow2(s_sc.o);
   const int e_d = s_sc.dp - s_sc.o;   // D is summed over the scaled d_out
   const bool al_q = aligned16(t.q), al_g = aligned16(t.d_out), al_o = aligned16(t.out);
@@ -556,8 +574,9 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_u32(src)), "r"(bytes)
                : "memory");
 }
+// Until this thread's stores have left shared memory.
 __device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -671,15 +690,6 @@ struct GradMaps {
   CUtensorMap qs, d_os, kcs, vcs, kbs, vbs;   // x kN rows (streamed)
 };
 
-// First row tile whose last block is anchored behind position `pos`.
-__device__ __forceinline__ int first_tile_behind(const PackedBwdPlan& pl, int pos) {
-  int lo = 0, hi = pl.T;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.sorted[min((mid + 1) * pl.per, pl.N) - 1] > pos) hi = mid; else lo = mid + 1;
-  }
-  return lo;
-}
 // CTAs that share the n streamed tiles of one context key tile.
 __device__ __forceinline__ int shares_of(const PackedBwdPlan& pl, int n) { return (n + pl.share - 1) / pl.share; }
 
@@ -754,17 +764,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       b -= tile * pl.nkv * pl.splits;
       h = b / pl.splits;
       share = b - h * pl.splits;
-      first = first_tile_behind(pl, tile * kRows);
+      const int2 seen = pl.seen_by[tile];
+      first = seen.x;
+      whole = seen.y;
       const int n = (pl.T - first) * kPer * G, shares = shares_of(pl, n);
       if (share >= shares) return;
       u0 = (int)((long long)n * share / shares);
       u1 = (int)((long long)n * (share + 1) / shares);
-      int hi = pl.T;
-      whole = first;
-      while (whole < hi) {   // first row tile whose first block is anchored behind the whole key tile
-        const int mid = (whole + hi) >> 1;
-        if (pl.sorted[mid * pl.per] >= (tile + 1) * kRows) hi = mid; else whole = mid + 1;
-      }
     } else if (b < n_ctx + n_rows) {
       // streamed: the context below the tile's largest anchor (`first` tiles), then the tile's own keys
       kind = 1;
@@ -1157,7 +1163,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       // ---- dV and dK of my key: the warps of a lane quarter take the 32-column groups of both in turn
       wait(&bars->done, 0);
       if (ok) {
-        const int e_v = -kPExp - sc.o, e_k = -kPExp - sc.dp - sc.q;
+        const Pow2 to_v(-kPExp - sc.o), to_k(-kPExp - sc.dp - sc.q);
 #pragma unroll
         for (int x = 0; x < 2 * kGroups / kParts; ++x) {
           const int gq = x * kParts + part, m = gq / kGroups, c = gq % kGroups * 32;   // matrix 0: dK, 1: dV
@@ -1167,7 +1173,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           tmem_ld_wait();
           tmem_values<32>(raw, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = m ? ldexpf(v[j], e_v) : ldexpf(v[j] * scale, e_k);
+          for (int j = 0; j < 32; ++j) v[j] = m ? to_v(v[j]) : to_k(v[j] * scale);
           stage32(m, c, v, kind == 0);
         }
       }
@@ -1226,7 +1232,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       }
       wait(&bars->done, 0);
       if (ok) {
-        const int e_q = -kPExp - sc.dp - sc.k;
+        const Pow2 to_q(-kPExp - sc.dp - sc.k);
 #pragma unroll
         for (int c = part * 32; c < HD; c += kParts * 32) {
           uint32_t raw[32];
@@ -1235,7 +1241,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           tmem_ld_wait();
           tmem_values<32>(raw, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = ldexpf(v[j] * scale, e_q);
+          for (int j = 0; j < 32; ++j) v[j] = to_q(v[j] * scale);
           stage32(0, c, v, false);
         }
       }
@@ -1261,7 +1267,7 @@ __global__ void __launch_bounds__(256) reduce_ctx_kernel(PackedBwdPlan pl, T* dk
   const int tile = blockIdx.x / kParts, h = blockIdx.y;
   __shared__ int s_shares;
   if (threadIdx.x == 0)
-    s_shares = shares_of(pl, (pl.T - first_tile_behind(pl, tile * kRows)) * (kRows / GradCfg<HD, PL>::kN) * (pl.nq / pl.nkv));
+    s_shares = shares_of(pl, (pl.T - pl.seen_by[tile].x) * (kRows / GradCfg<HD, PL>::kN) * (pl.nq / pl.nkv));
   __syncthreads();
   const int shares = s_shares, e = blockIdx.x % kParts * 256 + threadIdx.x;
   const int s = tile * kRows + e / Q, d = e % Q * 4;
@@ -1325,7 +1331,10 @@ cudaError_t run_grad(const PackedBwdPlan& pl, const PackedBwdTensors& t, int sms
   GradMaps m;
   const int q_rows = pl.nq * PL * rows, b_rows = pl.nkv * PL * rows, c_rows = pl.nkv * PL * std::max(ctx, kRows);
   auto enc = [&](CUtensorMap* a, CUtensorMap* b, const __half* p, int n) {   // a copy of 16-bit values, whatever they are
-    return encode_activation_map(a, p, HD, n, HD, kRows) && encode_activation_map(b, p, HD, n, HD, C::kN);
+    if (!encode_activation_map(a, p, HD, n, HD, kRows)) return false;
+    if (C::kN != kRows) return encode_activation_map(b, p, HD, n, HD, C::kN);
+    *b = *a;
+    return true;
   };
   if (!enc(&m.q, &m.qs, pl.q, q_rows) || !enc(&m.d_o, &m.d_os, pl.d_o, q_rows) || !enc(&m.kc, &m.kcs, pl.kc, c_rows) ||
       !enc(&m.vc, &m.vcs, pl.vc, c_rows) || !enc(&m.kb, &m.kbs, pl.kb, b_rows) || !enc(&m.vb, &m.vbs, pl.vb, b_rows))
@@ -1374,11 +1383,12 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   };
   const size_t pe = 2 * (size_t)p.planes;
   p.status = reinterpret_cast<int32_t*>(take(4));
-  p.parts = 2 * sms;
+  p.parts = sms;   // one CTA of the range kernel an SM
   p.part = reinterpret_cast<float*>(take(4 * (size_t)p.parts * kRangeValues));
   p.scale = reinterpret_cast<int32_t*>(take(4 * 5));
   p.order = reinterpret_cast<int32_t*>(take(4 * (size_t)N));
   p.sorted = reinterpret_cast<int32_t*>(take(4 * (size_t)N));
+  p.seen_by = reinterpret_cast<int2*>(take(8 * (size_t)std::max(p.KT, 1)));
   p.row_anchor = reinterpret_cast<int32_t*>(take(4 * rows));
   p.lse2 = reinterpret_cast<float*>(take(4 * rows * nq));
   p.delta = reinterpret_cast<float*>(take(4 * rows * nq));

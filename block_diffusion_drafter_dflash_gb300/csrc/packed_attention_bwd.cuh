@@ -26,6 +26,7 @@ struct PackedBwdPlan {
   int32_t* scale;         // [5] exponents of the powers of two the operands are scaled by (Scales)
   int32_t* order;         // [N] block of each sorted place
   int32_t* sorted;        // [N] anchors in ascending order
+  int2* seen_by;          // [KT] first row tile that sees some of the key tile, and all of it
   int32_t* row_anchor;    // [T*128] anchor of the row's block (INT_MAX in padding)
   float* lse2;            // [nq][T*128] lse log2(e) - kPExp, +inf in padding
   float* delta;           // [nq][T*128] sum_d d_out out, scaled as dp
