@@ -29,9 +29,14 @@ __all__ = ["DFlashError", "Model", "Cache", "lib", "dflash_model_create", "dflas
            "dflash_packed_block_attention_backward"]
 
 
-def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+# The current stream's handle without a Stream object (microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:

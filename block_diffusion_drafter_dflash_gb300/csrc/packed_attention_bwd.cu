@@ -1366,12 +1366,15 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   p.per = kRows / block;
   p.T = (N + p.per - 1) / p.per;
   p.KT = (S + kRows - 1) / kRows;
-  // Streamed tiles of one context item: with anchors spread over the sequence
-  // there are about G T KT nkv / 2 of them; two items an SM or more, at most 64
-  // tiles each.
+  // Streamed tiles of one context item.  An item costs about as much as three
+  // tiles before and after them, and its sums a trip through memory, so items are
+  // long where there are enough of them to go round: `all` tiles for the first key
+  // tile, half as many on average, half an item an SM.  (Cases of 16 x 8 and 32 x 8
+  // key tiles and kv heads: 7 -> 135 and 1231 us, 18 -> 114 and 1002, 36 -> 109 and
+  // 926, 128 -> 109 and 876; of 8 x 2: 3 -> 32 us, 12 -> 53.)
   const int per = kRows / (f32 && hd == 128 ? GradCfg<128, 2>::kN : kRows);
-  const long long all = (long long)(nq / nkv) * p.T * per;   // of the first key tile
-  p.share = (int)std::max(2LL, std::min(64LL, all * p.KT * nkv / 2 / (2 * sms)));
+  const long long all = (long long)(nq / nkv) * p.T * per;
+  p.share = (int)std::max(3LL, std::min(128LL, all * p.KT * nkv / sms));
   p.splits = (int)((all + p.share - 1) / p.share);
   const size_t rows = (size_t)p.T * kRows, ctx = (size_t)std::max(p.KT, 1) * kRows;
   char* c = static_cast<char*>(ws);
