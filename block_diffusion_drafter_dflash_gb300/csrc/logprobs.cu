@@ -20,10 +20,10 @@
 // of terms of one sign, so nothing cancels.
 //
 // Top k.  Each warp keeps its k largest (value, id) keys sorted over its
-// lanes.  After the first batch of loads the CTA sorts its threads' maxima: the
-// k-th of them, a value that k logits are known to reach, is the bar that the
-// rest has to reach (with 4096 logits or more behind it hardly more than k
-// pass).  A batch whose maximum is below the bar costs the top k nothing beyond
+// lanes.  After the first batch of loads, and again after the fourth, the
+// sixteenth and so on, the CTA sorts its threads' maxima: the k-th of them, a
+// value that k logits are known to reach, is the bar that the rest has to reach
+// (hardly more than k of all logits so far do).  A batch whose maximum is below the bar costs the top k nothing beyond
 // that maximum, which the softmax needs anyway.  Lists are merged in pairs
 // (elementwise maximum of one list with the other reversed, then a bitonic
 // merge).
@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LogprobArgs a, float
   };
   uint4 next[kFwdVec];
   load_batch(i0, next);
-  for (int base = i0; base < i1; base += NT * kFwdVec) {
+  int batch = 0, raise = 0;   // the bar is set by batch 0 and raised by 3, 15, 63, ...
+  for (int base = i0; base < i1; base += NT * kFwdVec, ++batch) {
     uint4 r[kFwdVec];
 #pragma unroll
     for (int j = 0; j < kFwdVec; ++j) r[j] = next[j];
@@ -337,8 +338,9 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LogprobArgs a, float
     st.s += ds.x + ds.y;
     st.t += dt.x + dt.y;
     if constexpr (TOPK) {
-      if (base == i0) {   // the bar: the k-th of the threads' maxima
-        s_max[warp][lane] = sort_desc(bm);
+      if (batch == raise) {   // the bar: the k-th of the threads' maxima so far
+        raise = 4 * raise + 3;
+        s_max[warp][lane] = sort_desc(st.m);
         __syncthreads();
 #pragma unroll
         for (int half = kWarps / 2; half; half >>= 1) {
@@ -346,8 +348,10 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(LogprobArgs a, float
           __syncthreads();
         }
         const float bar = s_max[0][k - 1];
-        // below -inf's key nothing is a logit (0: no bar, where fewer than k threads hold one)
-        top.thr = bar == -INFINITY ? 0 : make_key(bar, -1) & 0xffffffff00000000ull;
+        __syncthreads();
+        // (no bar where fewer than k threads hold a logit above -inf)
+        const unsigned long long key = bar == -INFINITY ? 0 : make_key(bar, -1) & 0xffffffff00000000ull;
+        if (key > top.thr) top.thr = key;
       }
       if (__any_sync(kAll, reaches(bm, top.thr))) {
 #pragma unroll
@@ -550,14 +554,18 @@ cudaError_t launch_bwd(const LogprobGradArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t token_logprobs_launch(const LogprobArgs& a, bool bf16, int sms, cudaStream_t s) {
-  // enough CTAs to fill the GPU a few times over, as far as clusters go, and
-  // at least one vector a thread
-  int cluster = 1;
-  while (cluster < kMaxCluster && (long long)a.rows * cluster < 2LL * sms) cluster *= 2;
+  // One CTA an SM at most, two vectors a thread at least, in clusters: a row
+  // alone is spread over eight SMs (151,936 fp32 logits, 20 alternatives: 27.0 us on
+  // one, 11.4 on eight), 77 rows of 32,003 over two each (13.9 on one, 11.7 on two,
+  // 12.9 on eight), 1,000 logits stay on one (4.4 us, 7.8 on eight).
   const int nvec = a.vocab / (bf16 ? 8 : 4);
-  while (cluster > 1 && nvec < cluster * 256) cluster /= 2;
-  // a few rows, each over all CTAs of a cluster: twice the threads
-  const bool wide = cluster == kMaxCluster && (long long)a.rows * cluster < 2LL * sms && nvec >= cluster * 512;
+  int cluster = 1;
+  while (cluster < kMaxCluster && (long long)a.rows * cluster * 8 <= 5LL * sms && nvec >= 1024 * cluster) cluster *= 2;
+  // 512 threads a CTA where there are few CTAs and enough to do for them (one row
+  // of 151,936: 9.0 us against 11.4 with 256 threads; 150 rows: 24.7 against 34.5;
+  // 600 rows: 68.6 against 61.4).  With bf16 logits they pay only for a handful of
+  // rows (one: 9.1 against 11.2, 16: 17.7 against 14.4).
+  const bool wide = nvec >= 1024 * cluster && (long long)a.rows * cluster <= (bf16 ? sms / 2 : 2 * sms);
   auto launch = [&](auto t, auto topk) {
     using T = decltype(t);
     constexpr bool K = decltype(topk)::value;
