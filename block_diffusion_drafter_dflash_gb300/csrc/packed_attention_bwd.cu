@@ -909,6 +909,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
     // a stage of each stream: this tile's, and the next one's with its phase
     int s0 = 0, s1 = 0, n0 = 0, n1 = 0;
     uint32_t ph0 = 0, ph1 = 0;
+    auto wait2 = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+      const bool x = ptx::mbar_try_wait(a, pa), y = ptx::mbar_try_wait(b, pb);
+      if (__all_sync(0xffffffffu, x && y)) {
+        ptx::tc_fence_after();
+        return ok;
+      }
+      return wait(a, pa) && wait(b, pb);
+    };
     auto arrived0 = [&] { return wait(&bars->full0[n0], ph0); };
     auto arrived1 = [&] { return wait(&bars->full1[n1], ph1); };
     auto next0 = [&] { if (++n0 == C::kS0) n0 = 0, ph0 ^= 1; };
@@ -932,8 +940,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         next1();
         for (int i = 0; i < n; ++i) {
           const bool more = i + 1 < n;
-          if (more && !arrived0()) break;
-          if (!wait(&bars->p_ready, i & 1)) break;
+          if (more ? !wait2(&bars->full0[n0], ph0, &bars->p_ready, i & 1) : !wait(&bars->p_ready, i & 1)) break;
           if (elect()) {
             mma_gradient<HD, PL>(tV, tS, g1 + s1 * kStep, i > 0);
             ptx::mma_commit(&bars->freed1[s1]);
@@ -943,8 +950,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
             }
           }
           __syncwarp();
-          if (more && kAhead && !arrived1()) break;
-          if (!wait(&bars->ds_ready[0], i & 1)) break;
+          if (more && kAhead ? !wait2(&bars->full1[n1], ph1, &bars->ds_ready[0], i & 1) : !wait(&bars->ds_ready[0], i & 1)) break;
           if (elect()) {
             mma_gradient<HD, PL>(tK, tP, g0 + s0 * kStep, i > 0);
             ptx::mma_commit(&bars->freed0[s0]);
@@ -977,15 +983,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         next1();
         for (int i = 0; i < n; ++i) {
           const bool more = i + 1 < n;
-          if (more) {
-            if (!arrived0()) break;
-            if (elect()) mma_scores<HD, PL>(tm + (~i & 1) * 128, ra, k0 + n0 * kStep);   // over dS(i - 1), which the last dQ has taken
-            __syncwarp();
-            if (!arrived1()) break;
-          }
-          if (!wait(&bars->p_ready, i & 1)) break;   // dP(i) is in registers
+          // (S goes over dS(i - 1), which the last dQ has taken, dP over dP(i) once it is in registers)
+          if (more ? !wait2(&bars->full0[n0], ph0, &bars->full1[n1], ph1) : false) break;
+          if (!wait(&bars->p_ready, i & 1)) break;
           if (more) {
             if (elect()) {
+              mma_scores<HD, PL>(tm + (~i & 1) * 128, ra, k0 + n0 * kStep);
               mma_scores<HD, PL>(tP, rb, k1 + n1 * kStep);
               ptx::mma_commit(&bars->s_full);
               ptx::mma_commit(&bars->freed1[n1]);
