@@ -1581,7 +1581,8 @@ int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_ho
   try {
     std::vector<ClipTensor> t(n_tensors);
     std::vector<std::pair<uintptr_t, uintptr_t>> outs;   // byte ranges written
-    outs.reserve(n_tensors);
+    outs.reserve(n_tensors + 1);
+    outs.emplace_back(reinterpret_cast<uintptr_t>(norm_dev), reinterpret_cast<uintptr_t>(norm_dev) + sizeof(float));
     for (int i = 0; i < n_tensors; ++i) {
       if (numel_host[i] < 0 || numel_host[i] > (int64_t(1) << 48))
         return fail(DFLASH_ERR_SHAPE, "tensor %d has %lld elements", i, (long long)numel_host[i]);
@@ -1602,7 +1603,7 @@ int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_ho
     std::sort(outs.begin(), outs.end());
     for (size_t i = 1; i < outs.size(); ++i)
       if (outs[i].first < outs[i - 1].second)
-        return fail(DFLASH_ERR_INVALID_ARG, "two tensors to be written overlap (one tensor given twice?)");
+        return fail(DFLASH_ERR_INVALID_ARG, "what is to be written overlaps (one tensor given twice?)");
     for (int i = 0; i < n_tensors; ++i) {
       if (!t[i].numel || t[i].in == t[i].out) continue;
       const uintptr_t b = reinterpret_cast<uintptr_t>(t[i].in), e = b + t[i].numel * (t[i].bf16 ? 2 : 4);

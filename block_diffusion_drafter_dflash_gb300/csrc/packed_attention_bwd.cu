@@ -39,7 +39,8 @@
 // bf16, scaled by powers of two so that its range holds them: q, k, v and d_out
 // each by the power that brings its largest value to 2^14 .. 2^15, P (at most 1) by
 // 2^14, and ds by what the largest norms of d_out's and v's rows allow it
-// (|dp| <= |d_out_r| |v_j|).  The scales are folded into factors that are there
+// (|dp| <= |d_out_r| |v_j|; for dQ, whose sums are one row's, by the row's own
+// norm of d_out).  The scales are folded into factors that are there
 // anyway, and powers of two are exact.  bf16 tensors take one plane: the operands
 // are then exact but for d_out, and d_out, P and ds are rounded by 2^-12 of
 // themselves, an eighth of the rounding of the bf16 gradients.  fp32 tensors
@@ -63,6 +64,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr long long kBudget = 400000000LL;
 constexpr int kOpExp = 14;           // an operand's largest value lies in [2^14, 2^15)
 constexpr int kPExp = 14;            // P is held times 2^14
+constexpr int kRowExpMax = 40;       // more than d_out's fp16 can tell a row from zero
 constexpr int kRangeValues = 6;      // largest |q|, |k|, |v|, |d_out|, and largest norm of a row of v, d_out
 constexpr int kRangeThreads = 512;
 
@@ -83,6 +85,8 @@ __device__ __forceinline__ int scale_exp(float m) {
   if (!(m > 0.f) || isinf(m)) return 0;
   return max(-120, min(120, kOpExp - ilogbf(m)));
 }
+// The e with n < 2^e.
+__device__ __forceinline__ int norm_exp(float n) { return n > 0.f && !isinf(n) ? ilogbf(n) + 1 : 0; }
 __device__ __forceinline__ Scales scales_of(const float* m) {
   Scales s;
   s.q = scale_exp(m[0]);
@@ -90,7 +94,6 @@ __device__ __forceinline__ Scales scales_of(const float* m) {
   s.v = scale_exp(m[2]);
   s.o = scale_exp(m[3]);
   // |dp - D| <= 2 |d_out| |v| by the rows' norms
-  auto norm_exp = [](float n) { return n > 0.f && !isinf(n) ? ilogbf(n) + 1 : 0; };
   s.dp = -(norm_exp(m[4]) + norm_exp(m[5]) + 1);
   return s;
 }
@@ -228,12 +231,20 @@ __global__ void __launch_bounds__(kRangeThreads) range_kernel(PackedBwdPlan pl, 
   const int part = blockIdx.x - rank_ctas, parts = pl.parts;
   float m[kRangeValues] = {};
   float none = 0.f;
-  const long long qr = (long long)pl.N * pl.block * pl.nq, br = (long long)pl.N * pl.block * pl.nkv,
-                  cr = (long long)pl.S * pl.nkv;
+  // context rows that no block sees are not read, whatever they hold
+  __shared__ int s_seen[kRangeThreads / 32];
+  int seen = 0;
+  for (int n = threadIdx.x; n < pl.N; n += kRangeThreads) seen = max(seen, t.anchors[n]);
+  seen = __reduce_max_sync(0xffffffffu, min(seen, pl.S));
+  if ((threadIdx.x & 31) == 0) s_seen[threadIdx.x >> 5] = seen;
+  const long long qr = (long long)pl.N * pl.block * pl.nq, br = (long long)pl.N * pl.block * pl.nkv;
   range_rows<T, HD, false>(static_cast<const T*>(t.q), qr, part, parts, m[0], none);
   range_rows<float, HD, true>(t.d_out, qr, part, parts, m[3], m[5]);
   range_rows<T, HD, false>(static_cast<const T*>(t.k_blk), br, part, parts, m[1], none);
   range_rows<T, HD, true>(static_cast<const T*>(t.v_blk), br, part, parts, m[2], m[4]);
+  __syncthreads();
+  seen = __reduce_max_sync(0xffffffffu, s_seen[threadIdx.x % (kRangeThreads / 32)]);
+  const long long cr = (long long)seen * pl.nkv;
   range_rows<T, HD, false>(static_cast<const T*>(t.k_ctx), cr, part, parts, m[1], none);
   range_rows<T, HD, true>(static_cast<const T*>(t.v_ctx), cr, part, parts, m[2], m[4]);
   __shared__ float sh[kRangeThreads / 32][kRangeValues];
@@ -348,8 +359,10 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
     }
     pl.seen_by[j] = make_int2(first, lo);
   }
+  const int seen = pl.N ? pl.sorted[pl.N - 1] : 0;   // context rows that some block sees
   const float f_q = pow2(s_sc.q), f_k = pow2(s_sc.k), f_v = pow2(s_sc.v), f_o = pow2(s_sc.o);
   const int e_d = s_sc.dp - s_sc.o;   // D is summed over the scaled d_out
+  const int e_o = norm_exp(s_max[5]) + s_sc.o;   // |d_out_r| 2^o < 2^e_o
   const bool al_q = aligned16(t.q), al_g = aligned16(t.d_out), al_o = aligned16(t.out);
   // block and position of a row; -1: padding
   auto place = [&](int r, int& n, int& i) {
@@ -383,7 +396,7 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
           l[u] = INFINITY;
         }
       }
-      float d[U];
+      float d[U], n2[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = h0 + u * R;
@@ -391,20 +404,23 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
         q[u].get(a);
         go[u].get(b);
         oo[u].get(c);
-        d[u] = 0.f;
+        d[u] = n2[u] = 0.f;
         if (h < pl.nq) {
           const size_t dst = ((size_t)h * PL * rows + r) * HD + col, plane = (size_t)rows * HD;
           put_planes<PL>(pl.q + dst, plane, f_q, a);
           put_planes<PL>(pl.d_o + dst, plane, f_o, b);
           // D from d_out as the products see it: its rounding then cancels in dp - D as exactly as d_out itself would
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[u] = fmaf(b[e], c[e], d[u]);
+          for (int e = 0; e < 8; ++e) d[u] = fmaf(b[e], c[e], d[u]), n2[u] = fmaf(b[e], b[e], n2[u]);
         }
       }
 #pragma unroll
       for (int o = L / 2; o; o >>= 1)
 #pragma unroll
-        for (int u = 0; u < U; ++u) d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
+        for (int u = 0; u < U; ++u) {
+          d[u] += __shfl_xor_sync(0xffffffffu, d[u], o);
+          n2[u] += __shfl_xor_sync(0xffffffffu, n2[u], o);
+        }
       if (col == 0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -412,6 +428,9 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
           if (h < pl.nq) {
             pl.lse2[(size_t)h * rows + r] = l[u];
             pl.delta[(size_t)h * rows + r] = ldexpf(d[u], e_d);
+            // |d_out_r| 2^o < 2^(floor(log2(n2) / 2) + 1)
+            const int below = n2[u] > 0.f ? e_o - (ilogbf(n2[u]) >> 1) - 1 : 0;
+            pl.row_scale[(size_t)h * rows + r] = pow2(max(0, min(kRowExpMax, below)));
             if (h == 0) pl.row_anchor[r] = n >= 0 ? pl.sorted[at] : INT_MAX;
           }
         }
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(256) pack_bwd_kernel(PackedBwdPlan pl, PackedB
         int n, i;
         place(r, n, i);
         if (n >= 0) row = ((long long)n * g + i) * pl.nkv;
-      } else if (r < pl.S) {
+      } else if (r < seen) {
         row = (long long)r * pl.nkv;
       }
       const T* k = static_cast<const T*>(blk ? t.k_blk : t.k_ctx);
@@ -1194,7 +1213,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       send(dst, HD * (kind == 0 ? 4 : (int)sizeof(T)));
     } else {
       const int r = tile * kRows + me;
-      const float lse2 = pl.lse2[(size_t)h * rows + r], delta = pl.delta[(size_t)h * rows + r];
+      // dQ's sums are a row's own, and so is the scale of its ds: rows of small d_out keep their bits
+      const float up = pl.row_scale[(size_t)h * rows + r], f_row = f_dp * up;
+      const float lse2 = pl.lse2[(size_t)h * rows + r], delta = pl.delta[(size_t)h * rows + r] * up;
       const int anchor = pl.row_anchor[r];
       for (int i = 0; i < n; ++i) {
         if (!wait(&bars->s_full, i & 1)) break;
@@ -1221,7 +1242,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < NC; j += 2) {
           const float2 a = fma2(make_float2(s[j], s[j + 1]), make_float2(sc2, sc2), make_float2(-lse2, -lse2));
-          const float2 b = fma2(make_float2(d[j], d[j + 1]), make_float2(f_dp, f_dp), make_float2(-delta, -delta));
+          const float2 b = fma2(make_float2(d[j], d[j + 1]), make_float2(f_row, f_row), make_float2(-delta, -delta));
           const float2 x = mul2(make_float2(ex2(a.x), ex2(a.y)), b);
           s[j] = x.x;
           s[j + 1] = x.y;
@@ -1236,6 +1257,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       wait(&bars->done, 0);
       if (ok) {
         const Pow2 to_q(-kPExp - sc.dp - sc.k);
+        const float down = scale / up;
 #pragma unroll
         for (int c = part * 32; c < HD; c += kParts * 32) {
           uint32_t raw[32];
@@ -1244,7 +1266,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           tmem_ld_wait();
           tmem_values<32>(raw, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = to_q(v[j] * scale);
+          for (int j = 0; j < 32; ++j) v[j] = to_q(v[j] * down);
           stage32(0, c, v, false);
         }
       }
@@ -1398,6 +1420,7 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   p.row_anchor = reinterpret_cast<int32_t*>(take(4 * rows));
   p.lse2 = reinterpret_cast<float*>(take(4 * rows * nq));
   p.delta = reinterpret_cast<float*>(take(4 * rows * nq));
+  p.row_scale = reinterpret_cast<float*>(take(4 * rows * nq));
   p.q = reinterpret_cast<__half*>(take(pe * rows * nq * hd));
   p.d_o = reinterpret_cast<__half*>(take(pe * rows * nq * hd));
   p.kc = reinterpret_cast<__half*>(take(pe * ctx * nkv * hd));

@@ -30,6 +30,7 @@ struct PackedBwdPlan {
   int32_t* row_anchor;    // [T*128] anchor of the row's block (INT_MAX in padding)
   float* lse2;            // [nq][T*128] lse log2(e) - kPExp, +inf in padding
   float* delta;           // [nq][T*128] sum_d d_out out, scaled as dp
+  float* row_scale;       // [nq][T*128] power of two that the row's ds may be larger by in dQ
   __half* q;              // [nq][planes][T*128][hd], zero in padding (d_o, kb and vb too)
   __half* d_o;
   __half* kc;             // [nkv][planes][KT*128][hd]

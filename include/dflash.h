@@ -401,9 +401,11 @@ int32_t dflash_packed_block_attention_lse(const void* q_dev, const void* k_ctx_d
  *   workspace   >= dflash_packed_attention_backward_workspace_bytes(...) bytes,
  *               256-byte aligned; its first int32 is the call's status word
  *               (dflash_packed_attention_status)
- * Operands have to be finite: a NaN or an infinity spreads to gradients that
- * do not depend on it.  Operands, P and ds enter their products as scaled fp16
- * (fp32 operands: as hi/lo pairs of it, 22 bits), sums are fp32.  The same
+ * Operands that some block sees have to be finite: a NaN or an infinity
+ * spreads to gradients that do not depend on it.  Operands, P and ds enter their products as scaled fp16
+ * (fp32 operands: as hi/lo pairs of it, 22 bits), sums are fp32: what is
+ * 2^-28 of a tensor's largest value (of 1, for P) or less loses bits, and below
+ * 2^-39 counts as 0.  Context rows that no block sees are not read.  The same
  * call gives the same bits on the same device.  n_blocks = 0 zeroes
  * d_k_ctx and d_v_ctx.  The forward's limits, and 2^31 rows of laid-out
  * operands.  The workspace size depends on the current device's SM count. */
@@ -480,7 +482,7 @@ int32_t dflash_token_logprobs_backward(const void* logits_dev, int32_t dtype, in
  *   numel_host  elements of each tensor (contiguous; 0 is skipped, its pointers
  *               may be NULL);  dtype_host  DFLASH_DTYPE_* of each
  *   max_norm    >= 0; infinity in place computes the norm alone
- *   norm_dev    fp32 [1]: the norm before clipping
+ *   norm_dev    fp32 [1]: the norm before clipping; in no tensor that is written
  *   workspace   >= dflash_clip_workspace_bytes() bytes, 8-byte aligned
  * The host arrays are read before the call returns.  Sums of squares are kept
  * in double, so finite gradients of any size have a finite norm (norm_dev

@@ -185,6 +185,47 @@ def test_operands_far_from_one(dtype):
             assert torch.equal(got, w * 2.0 ** e)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_far_smaller_than_others(dtype):
+    """Rows whose d_out is 2^-12 .. 1 of the others': each row's d_q is as precise as if it were alone (d_out's
+    fp16 planes hold 2^-40 of their largest, 2^-28 of the smallest rows', below their own rounding)."""
+    S, N, g, nq, nkv, hd = 300, 30, 6, 4, 2, 64
+    anchors = anchors_of(N, S, 8)
+    ops = operands(S, N, g, nq, nkv, hd, dtype, 12, "cuda")
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    base = torch.randn(ops[0].shape, generator=gen, device="cuda")
+    scale = torch.exp2(-torch.randint(0, 13, (N, g, nq, 1), generator=gen, device="cuda").float())
+    grads = run(ops, anchors, base * scale)[2]
+    ref = [t.double() for t in ops]
+    want = backward_reference(*ref, anchors, base.double())
+    tol = tolerances(ref, anchors, base.double(), want, dtype)
+    worst = float(((grads[0].double() / scale - want[0]).abs() / tol[0]).max())
+    print(f"worst {worst:.2f} of its tolerance")
+    assert worst <= 1.0
+    want = backward_reference(*ref, anchors, (base * scale).double())
+    tol = tolerances(ref, anchors, (base * scale).double(), want, dtype)
+    for got, w, t in zip(grads[1:], want[1:], tol[1:]):
+        assert float(((got.double() - w).abs() / t).max()) <= 1.0
+
+
+def test_context_that_no_block_sees_is_not_read():
+    """Context rows from the last anchor on hold NaN and infinities: their gradients are 0, the others' bits stay."""
+    S, N, g, nq, nkv, hd = 700, 20, 8, 4, 2, 128
+    anchors = [a % 301 for a in anchors_of(N, S, 3)] + [300]
+    ops = operands(S, N + 1, g, nq, nkv, hd, torch.bfloat16, 12, "cuda")
+    d_out = torch.randn(ops[0].shape, device="cuda")
+    out, lse, want, ws = run(ops, anchors, d_out)
+    df = _df()
+    for x in (math.nan, math.inf, -math.inf):
+        for t in ops[1:3]:
+            t[300:] = x
+        got = [torch.full_like(t, math.nan) for t in ops]
+        df.dflash_packed_block_attention_backward(*ops, torch.tensor(anchors, dtype=torch.int32, device="cuda"), out, lse,
+                                                  d_out, *got, ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert bool((got[1][300:] == 0).all()) and bool((got[2][300:] == 0).all())
+
+
 def test_zero_gradient_and_operands():
     S, N, g, nq, nkv, hd = 100, 9, 4, 4, 2, 64
     anchors = anchors_of(N, S, 8)

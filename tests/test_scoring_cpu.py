@@ -55,7 +55,7 @@ def test_logprob_gradient_refusals(L, kw, code):  # noqa: F811
     assert _backward(L, **kw) == code
 
 
-def _clip(L, tensors, out=None, max_norm=1.0, norm=P, ws=P, ws_bytes=1 << 20, n=None):
+def _clip(L, tensors, out=None, max_norm=1.0, norm=P + 4096, ws=P, ws_bytes=1 << 20, n=None):
     """tensors: (address, numel, dtype)"""
     k = len(tensors)
     ptrs = (ctypes.c_void_p * k)(*[t[0] for t in tensors])
@@ -76,6 +76,8 @@ def _clip(L, tensors, out=None, max_norm=1.0, norm=P, ws=P, ws_bytes=1 << 20, n=
     ([(P, 4, 0), (P + 64, 4, 0)], dict(out=[P + 72, P + 256]), -1),     # an output over another's input
     ([(P, 4, 0)], dict(out=[P + 4]), -1),                      # an output over its own input, shifted
     ([(P, 4, 0)], dict(out=[None]), -1),
+    ([(P, 4, 0)], dict(norm=P + 12), -1),                      # the norm inside a gradient
+    ([(P, 4, 0)], dict(out=[P + 64], norm=P + 4), -1),
 ])
 def test_clip_refusals(L, tensors, kw, code):  # noqa: F811
     assert _clip(L, tensors, **kw) == code
