@@ -5,8 +5,11 @@
 //
 // Two kernels over the same list of tensors.  The first reads every gradient
 // once; the second reads and writes them, walking the list backwards so that
-// what the first read last is still in L2 (126 MB; a drafter's few megabytes
-// stay there altogether).  Both are bound by HBM.
+// what the first read last is still in L2 (129 MB; a drafter's few megabytes
+// stay there altogether).  Both are bound by HBM: 1.05 G bf16 gradients (an
+// 8B-shaped drafter's five layers and fusion) take 296 us for the norm (7.1 TB/s) and 660 us
+// to scale (6.4 TB/s of reads and writes); 1.9 M fp32 ones 9.5 us in all, two
+// launches' latency.
 //
 // The list travels in the launch's parameters (up to kMaxTensors a launch,
 // longer lists take several launches): no table in device memory, so a call

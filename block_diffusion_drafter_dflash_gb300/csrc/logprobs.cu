@@ -9,7 +9,11 @@
 //   dx_v = (1/T) [ g_lp (1[v = tok] - p_v) - g_H p_v (ln p_v + H) ].
 //
 // Both are bound by HBM: the forward reads every logit once, the gradient
-// reads and writes every logit once.
+// reads and writes every logit once.  Measured on rows of 151,936 logits: 480 fp32
+// rows with 5 alternatives 49.2 us (5.9 TB/s), 2,048 bf16 rows 101 us (6.1 TB/s),
+// their gradient 177 us (7.0 TB/s of reads and writes); one fp32 row with 20
+// alternatives 9.1 us, which is latency: the launch, 37 KB to each of eight SMs,
+// the bar's and the lists' sorts and the cluster's two barriers.
 //
 // Forward.  A row is one cluster of C CTAs, each taking a C-th of it (C = 1
 // where the rows alone fill the GPU, up to 8 for a single row being served),
@@ -23,8 +27,10 @@
 // lanes.  After the first batch of loads, and again after the fourth, the
 // sixteenth and so on, the CTA sorts its threads' maxima: the k-th of them, a
 // value that k logits are known to reach, is the bar that the rest has to reach
-// (hardly more than k of all logits so far do).  A batch whose maximum is below the bar costs the top k nothing beyond
-// that maximum, which the softmax needs anyway.  Lists are merged in pairs
+// (hardly more than k of all logits so far do).  A batch whose maximum is below
+// the bar costs the top k nothing beyond that maximum, which the softmax needs
+// anyway: 600 fp32 rows of 151,936 with 20 alternatives take 61 us (78 with the
+// bar set by the first batch alone; a copy's rate allows 54).  Lists are merged in pairs
 // (elementwise maximum of one list with the other reversed, then a bitonic
 // merge).
 #include <cooperative_groups.h>
