@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
   // ---- this CTA's item
   const int G = pl.nq / pl.nkv, rows = pl.T * kRows, ctx = pl.KT * kRows;
   constexpr int kPer = kRows / C::kN;        // streamed tiles of 128 rows
-  const int n_ctx = pl.KT * pl.nkv * pl.splits, n_rows = pl.T * pl.nq;
+  const int n_ctx = pl.KT * pl.nkv * pl.splits, n_own = pl.T * pl.nkv;
   int kind, h, tile, share = 0;              // kind 0: context keys, 1: rows, 2: own keys (h: kv head unless 1)
   int u0 = 0, u1, first = 0, whole = 0;      // streamed tiles [u0, u1)
   {
@@ -800,10 +800,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       if (share >= shares) return;
       u0 = (int)((long long)n * share / shares);
       u1 = (int)((long long)n * (share + 1) / shares);
-    } else if (b < n_ctx + n_rows) {
-      // streamed: the context below the tile's largest anchor (`first` tiles), then the tile's own keys
+    } else if (b >= n_ctx + n_own) {
+      // streamed: the context below the tile's largest anchor (`first` tiles), then
+      // the tile's own keys.  The shortest items end the launch.
       kind = 1;
-      b -= n_ctx;
+      b -= n_ctx + n_own;
       tile = pl.T - 1 - b / pl.nq;
       h = b % pl.nq;
       first = (pl.sorted[min((tile + 1) * pl.per, pl.N) - 1] + C::kN - 1) / C::kN;
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
     } else {
       // streamed: the row tile, head by head
       kind = 2;
-      b -= n_ctx + n_rows;
+      b -= n_ctx;
       tile = b / pl.nkv;
       h = b % pl.nkv;
       u1 = G * kPer;
