@@ -479,7 +479,9 @@ _CLIP_DTYPES = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}
 
 def _scratch(nbytes: int, stream=None) -> torch.Tensor:
     """Device scratch of the caching allocator, ordered with the stream the call runs on."""
-    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
