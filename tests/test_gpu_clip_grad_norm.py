@@ -156,3 +156,22 @@ def test_wrapper_refusals():
             df.dflash_clip_grad_norm(grads, most, norm)
     with pytest.raises(df.DFlashError):
         df.dflash_clip_grad_norm([g], 1.0, norm, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """A tensor of more than 2^31 values, a short one before and behind it."""
+    n, reps = 1 << 20, 2049
+    base = _grads([n], 3, dtypes=(torch.bfloat16,))[0]
+    big, ends = base.repeat(reps), _grads([77, 300], 4)
+    assert big.numel() > 2 ** 31
+    grads = [ends[0], big, ends[1]]
+    before = [ends[0].clone(), ends[1].clone()]
+    want = float(torch.sqrt(reps * base.double().square().sum() + sum(g.double().square().sum() for g in before)))
+    norm = _clip(grads, 1.0)
+    assert abs(float(norm) - want) <= 34 * U * want
+    first = big[:n].clone()
+    assert bool((big.view(reps, n) == first).all())
+    for b, a in zip((base, *before), (first, ends[0], ends[1])):
+        w = b.double() / want
+        assert bool(((a.double() - w).abs() <= w.abs() * (36 * U + (2.0 ** -8 * 1.01 if a.dtype == torch.bfloat16 else 0))
+                     + 1e-40).all())

@@ -255,6 +255,28 @@ def test_many_calls_in_a_row():
     assert statuses == [0] * 10
 
 
+def test_two_streams_at_once():
+    """Calls that overlap in time, each with its own workspace: the bits of each alone."""
+    df = _df()
+    cases = [(900, 96, 8, 16, 4, 128, torch.bfloat16), (700, 80, 6, 8, 2, 64, torch.float32)]
+    jobs = []
+    for i, (S, N, g, nq, nkv, hd, dtype) in enumerate(cases):
+        anchors = anchors_of(N, S, 40 + i)
+        ops = operands(S, N, g, nq, nkv, hd, dtype, 50 + i, "cuda")
+        d_out = torch.randn(ops[0].shape, device="cuda")
+        out, lse, want, ws = run(ops, anchors, d_out)
+        a = torch.tensor(anchors, dtype=torch.int32, device="cuda")
+        jobs.append((torch.cuda.Stream(), ops, a, out, lse, d_out, want, [torch.full_like(t, math.nan) for t in ops], ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, ops, a, out, lse, d_out, _, got, ws in jobs:
+            df.dflash_packed_block_attention_backward(*ops, a, out, lse, d_out, *got, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, _, _, _, want, got, ws in jobs:
+        assert df.dflash_packed_attention_status(ws) == 0
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_anchors_outside_the_sequence_are_clamped_and_flagged():
     df = _df()
     S, N, g, nq, nkv, hd = 64, 3, 4, 4, 2, 64

@@ -281,3 +281,41 @@ def test_side_stream_and_graph_replay():
     step()
     assert all(torch.equal(a, b) for a, b in zip(outs, again)) and not torch.equal(again[0], first[0])
     _check(x, list(range(R)), 0.9, 4, again[:5])
+
+
+def test_largest_row_count_and_vocabulary():
+    R, V, k = 65535, 5, 3
+    x = _logits(R, V, torch.float32, 3)
+    tokens = np.random.default_rng(4).integers(-1, V + 1, R).tolist()
+    _check(x, tokens, 0.9, k, _run(x, tokens, 0.9, k))
+    for dtype in (torch.float32, torch.bfloat16):
+        x = _logits(1, 1 << 24, dtype, 5)
+        _check(x, [1 << 23], 1.0, 32, _run(x, [1 << 23], 1.0, 32))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: 64 rows repeated give the same bits wherever they lie, forward and gradient (in place)."""
+    df = _df()
+    V, n, reps = 151936, 64, 222
+    base = _logits(n, V, torch.bfloat16, 9)
+    x = base.repeat(reps, 1)
+    assert x.numel() > 2 ** 31
+    tokens = np.random.default_rng(4).integers(0, V, n).tolist()
+    tok = torch.tensor(tokens * reps, dtype=torch.int32, device="cuda")
+    f = lambda: torch.full((n * reps,), 777.0, device="cuda")
+    lp, h, lse = f(), f(), f()
+    ids = torch.full((n * reps, 2), 777, dtype=torch.int32, device="cuda")
+    top = torch.full((n * reps, 2), 777.0, device="cuda")
+    df.dflash_token_logprobs(x, tok, 1.0, lp, entropy=h, lse=lse, top_ids=ids, top_logprobs=top)
+    for t in (lp, h, lse, ids, top):
+        assert bool((t.view(reps, n, -1) == t[:n].view(n, -1)).all())
+    _check(base, tokens, 1.0, 2, [t[:n] for t in (lp, h, lse, ids, top)])
+    g = torch.linspace(-1, 1, n, device="cuda").repeat(reps)
+    df.dflash_token_logprobs_backward(x, tok, 1.0, lse, x, d_logprob=g)
+    first = x[:n].clone()
+    assert all(torch.equal(x[i * n:(i + 1) * n], first) for i in range(reps))
+    xd = base[:4].double().cpu().numpy()
+    a = g[:4].double().cpu().numpy()
+    want = logprob_grad_reference(xd, tokens[:4], 1.0, a, None)
+    assert np.all(np.abs(first[:4].double().cpu().numpy() - want)
+                  <= _grad_tol(xd, tokens[:4], 1.0, a, None, want, torch.bfloat16))
