@@ -55,7 +55,9 @@
 // are then exact but for d_out, and d_out, P and ds are rounded by 2^-12 of
 // themselves, an eighth of the rounding of the bf16 gradients.  fp32 tensors
 // take each operand, P and ds included, as a hi + lo pair (22 bits) and each
-// product as three MMAs (hi hi, hi lo, lo hi).  Every sum and the softmax are fp32.
+// product as three MMAs (hi hi, hi lo, lo hi).  Every sum and the softmax are fp32;
+// the tensor cores' sums truncate (by 2e-8 a step of 16 rows, measured, all to the
+// same side), so those of fp32 tensors are kept short.
 #include <cuda.h>
 
 #include <algorithm>
@@ -694,9 +696,14 @@ struct GradCfg {
   static constexpr int kCols = kN / kParts;                // columns of S of one softmax warp
   static constexpr int kPitch = HD * 4 + 16;               // fp32 rows staged on their way out: no bank conflicts
   // tensor memory.  Keys: S at 0, dP at 128, dV at 256, dK behind it.  Rows: S in
-  // two buffers at 0 and 128, dP at 256, dQ at 384.
-  static constexpr int kColP = 128, kColV = 256, kColK = kColV + HD, kColPRows = 256, kColQ = 384;
+  // two buffers at 0 and kN, dP behind them, dQ behind that.  With two planes the
+  // small products (hi lo and lo hi) have sums of their own where there is room, kLo
+  // columns further (0: none): the tensor cores truncate a sum at each step, and so
+  // the large one takes a third of the steps.
+  static constexpr int kColP = 128, kColV = 256, kColK = kColV + HD, kLoKeys = PL == 2 && HD == 64 ? 2 * HD : 0;
+  static constexpr int kColPRows = 2 * kN, kColQ = kN == 64 ? 256 : 384, kLoRows = PL == 2 ? HD : 0;
   static constexpr uint32_t kTmem = 512;
+  static_assert(kColK + kLoKeys + HD <= 512 && kColQ + kLoRows + HD <= 512 && kColPRows + kN <= kColQ, "tensor memory");
   static_assert(kBytes <= 227 * 1024 && 2 * kRows * kPitch <= kOffStat, "shared memory");
 };
 
@@ -743,8 +750,9 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t res, uint32_t st
   }
 }
 // G (+)= A B: A the P or dS of 128 lanes in tensor memory (columns of `a` as
-// put_pairs left them), B kN streamed rows read along their values.
-template <int HD, int PL>
+// put_pairs left them), B kN streamed rows read along their values.  LO: columns
+// from G to its sum of small products.
+template <int HD, int PL, int LO>
 __device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, uint32_t str, uint32_t accumulate) {
   using C = GradCfg<HD, PL>;
   constexpr uint32_t id = idesc_f16(kRows, HD) | kBMajorMN;
@@ -752,10 +760,11 @@ __device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, uint32_t st
 #pragma unroll
   for (int pr = (PL == 2 ? 0 : 2); pr < 3; ++pr) {
     const int pa = pr == 1, pb = pr == 0;
+    if (LO && pr == 2) acc = accumulate;
 #pragma unroll
     for (int k = 0; k < C::kN / 16; ++k) {
       const int chunk = 16 * k / C::kCols, in = 16 * k % C::kCols;
-      mma_tmem(d, a + chunk * C::kCols + pa * (C::kCols / 2) + in / 2,
+      mma_tmem(LO && pr < 2 ? d + LO : d, a + chunk * C::kCols + pa * (C::kCols / 2) + in / 2,
                str + (pb * C::kSub * C::kStrTile >> 4) + k * (2048 >> 4), id, acc);
       acc = 1;
     }
@@ -972,7 +981,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           const bool more = i + 1 < n;
           if (more ? !wait2(&bars->full0[n0], ph0, &bars->p_ready, i & 1) : !wait(&bars->p_ready, i & 1)) break;
           if (elect()) {
-            mma_gradient<HD, PL>(tV, tS, g1 + s1 * kStep, i > 0);
+            mma_gradient<HD, PL, C::kLoKeys>(tV, tS, g1 + s1 * kStep, i > 0);
             ptx::mma_commit(&bars->freed1[s1]);
             if (more) {
               mma_scores<HD, PL>(tS, ra, k0 + n0 * kStep);
@@ -982,7 +991,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           __syncwarp();
           if (more && kAhead ? !wait2(&bars->full1[n1], ph1, &bars->ds_ready[0], i & 1) : !wait(&bars->ds_ready[0], i & 1)) break;
           if (elect()) {
-            mma_gradient<HD, PL>(tK, tP, g0 + s0 * kStep, i > 0);
+            mma_gradient<HD, PL, C::kLoKeys>(tK, tP, g0 + s0 * kStep, i > 0);
             ptx::mma_commit(&bars->freed0[s0]);
           }
           __syncwarp();
@@ -1018,7 +1027,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           if (!wait(&bars->p_ready, i & 1)) break;
           if (more) {
             if (elect()) {
-              mma_scores<HD, PL>(tm + (~i & 1) * 128, ra, k0 + n0 * kStep);
+              mma_scores<HD, PL>(tm + (~i & 1) * C::kN, ra, k0 + n0 * kStep);
               mma_scores<HD, PL>(tP, rb, k1 + n1 * kStep);
               ptx::mma_commit(&bars->s_full);
               ptx::mma_commit(&bars->freed1[n1]);
@@ -1027,7 +1036,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           }
           if (!wait(&bars->ds_ready[i & 1], (i >> 1) & 1)) break;
           if (elect()) {
-            mma_gradient<HD, PL>(tm + C::kColQ, tm + (i & 1) * 128, g0 + s0 * kStep, i > 0);
+            mma_gradient<HD, PL, C::kLoRows>(tm + C::kColQ, tm + (i & 1) * C::kN, g0 + s0 * kStep, i > 0);
             ptx::mma_commit(&bars->freed0[s0]);
           }
           __syncwarp();
@@ -1064,6 +1073,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       return ok;
     };
     const int own = me / pl.block;            // block of my lane's row or key within its tile
+    // 32 columns of a gradient, with the small products' sum `lo` columns further (0: none)
+    auto read_sum = [&](uint32_t at, int lo, float* v) {
+      uint32_t raw[32];
+      tmem_ld<32>(at, raw);
+      tmem_ld_wait();
+      tmem_values<32>(raw, v);
+      if (lo) {
+        float small[32];
+        tmem_ld<32>(at + lo, raw);
+        tmem_ld_wait();
+        tmem_values<32>(raw, small);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += small[j];
+      }
+    };
     // staged output rows: matrix m's row r at m * kRows * kPitch + r * kPitch
     auto stage32 = [&](int m, int c, const float* v, bool wide) {   // 32 columns from c on
       uint8_t* d = sm + (size_t)(m * kRows + me) * C::kPitch + c * (wide ? 4 : (int)sizeof(T));
@@ -1200,11 +1224,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 #pragma unroll
         for (int x = 0; x < 2 * kGroups / kParts; ++x) {
           const int gq = x * kParts + part, m = gq / kGroups, c = gq % kGroups * 32;   // matrix 0: dK, 1: dV
-          uint32_t raw[32];
           float v[32];
-          tmem_ld<32>(tmem + lanes + (m ? C::kColV : C::kColK) + c, raw);
-          tmem_ld_wait();
-          tmem_values<32>(raw, v);
+          read_sum(tmem + lanes + (m ? C::kColV : C::kColK) + c, C::kLoKeys, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = m ? to_v(v[j]) : to_k(v[j] * scale);
           stage32(m, c, v, kind == 0);
@@ -1230,7 +1251,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       const int anchor = pl.row_anchor[r];
       for (int i = 0; i < n; ++i) {
         if (!wait(&bars->s_full, i & 1)) break;
-        const uint32_t tS = tmem + lanes + (i & 1) * 128 + c0;
+        const uint32_t tS = tmem + lanes + (i & 1) * C::kN + c0;
         // columns [from, from + count) of mine are seen
         int from = 0, count;
         if (i < first) {
@@ -1271,11 +1292,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         const float down = scale / up;
 #pragma unroll
         for (int c = part * 32; c < HD; c += kParts * 32) {
-          uint32_t raw[32];
           float v[32];
-          tmem_ld<32>(tmem + lanes + C::kColQ + c, raw);
-          tmem_ld_wait();
-          tmem_values<32>(raw, v);
+          read_sum(tmem + lanes + C::kColQ + c, C::kLoRows, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = to_q(v[j] * down);
           stage32(0, c, v, false);
@@ -1410,7 +1428,13 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   // 926, 128 -> 109 and 876; of 8 x 2: 3 -> 32 us, 12 -> 53.)
   const int per = kRows / (f32 && hd == 128 ? GradCfg<128, 2>::kN : kRows);
   const long long all = (long long)(nq / nkv) * p.T * per;
-  p.share = (int)std::max(3LL, std::min(128LL, all * p.KT * nkv / sms));
+  // fp32 tensors: at most 96 steps of 16 rows on a sum that the tensor cores truncate
+  // at each (12 tiles of 8 with head size 64, where the small products have sums of
+  // their own, else 8 of 12).  200 blocks of 16 in 3,000 positions, 8 / 2 heads of 64
+  // and of 128: 12 -> 2.0e-6 of the gradients' norm and 140 us, 31 -> 5.4e-6 and 133;
+  // 8 -> 2.0e-6 and 323 us, 63 -> 1.6e-5 and 262 (1.9e-6 with plain fp32 sums).
+  const long long most = !f32 ? 128 : hd == 64 ? 12 : 8;
+  p.share = (int)std::max(3LL, std::min(most, all * p.KT * nkv / sms));
   p.splits = (int)((all + p.share - 1) / p.share);
   const size_t rows = (size_t)p.T * kRows, ctx = (size_t)std::max(p.KT, 1) * kRows;
   char* c = static_cast<char*>(ws);

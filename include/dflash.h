@@ -405,7 +405,9 @@ int32_t dflash_packed_block_attention_lse(const void* q_dev, const void* k_ctx_d
  * spreads to gradients that do not depend on it.  Operands, P and ds enter their products as scaled fp16
  * (fp32 operands: as hi/lo pairs of it, 22 bits), sums are fp32: what is
  * 2^-28 of a tensor's largest value (of 1, for P) or less loses bits, and below
- * 2^-39 counts as 0.  Context rows that no block sees are not read.  The same
+ * 2^-39 counts as 0.  The tensor cores truncate their sums, so that fp32
+ * gradients are good to about 2e-6 of their norm with contexts of a few
+ * thousand positions (d_q loses in proportion to longer ones).  Context rows that no block sees are not read.  The same
  * call gives the same bits on the same device.  n_blocks = 0 zeroes
  * d_k_ctx and d_v_ctx.  The forward's limits, and 2^31 rows of laid-out
  * operands.  The workspace size depends on the current device's SM count. */

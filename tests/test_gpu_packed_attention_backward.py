@@ -185,6 +185,29 @@ def test_operands_far_from_one(dtype):
             assert torch.equal(got, w * 2.0 ** e)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_long_sums_of_fp32_tensors(hd):
+    """Tensor-core sums truncate: by at most 2^-23 of the sum a step, 2^-24 on average.  96 steps at most follow one
+    another in the context's gradients and (3,000 / 128 + 1) * 8 or (3,000 / 64 + 1) * 4 in d_q's large products: 200;
+    e^ and lse add 2^-20 of independent terms, d_q's sums of both signs shrink with the square root."""
+    S, N, g, nq, nkv = 3000, 200, 16, 8, 2
+    anchors = anchors_of(N, S, 13)
+    ops = operands(S, N, g, nq, nkv, hd, torch.float32, 14, "cuda")
+    d_out = torch.randn(ops[0].shape, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    ref = [t.double() for t in ops]
+    out, lse, _ = forward_reference(*ref, anchors)
+    df = _df()
+    grads = [torch.full_like(t, math.nan) for t in ops]
+    ws = df.dflash_packed_attention_backward_workspace(N, g, S, nq, nkv, hd, torch.float32)
+    df.dflash_packed_block_attention_backward(*ops, torch.tensor(anchors, dtype=torch.int32, device="cuda"), out.float().contiguous(),
+                                              lse.float().contiguous(), d_out, *grads, ws)
+    for name, got, w in zip(("d_q", "d_k_ctx", "d_v_ctx", "d_k_blk", "d_v_blk"), grads,
+                            backward_reference(*ref, anchors, d_out.double())):
+        err = float((got.double() - w).norm() / w.norm())
+        print(f"{name}: rel {err:.2e}")
+        assert err <= 96 * 2.0 ** -24 + 2.0 ** -20, name
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_rows_far_smaller_than_others(dtype):
     """Rows whose d_out is 2^-12 .. 1 of the others': each row's d_q is as precise as if it were alone (d_out's
