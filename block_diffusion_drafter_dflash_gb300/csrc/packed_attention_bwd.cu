@@ -1199,9 +1199,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           const float4 x = st[j / 4];
           const float2 a = fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y));
           const float2 b = fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w));
-          if (PL == 1) {   // at most 1, and P at most 2^14: their product in fp16
-            hi[j / 2] = as_u32(__hmul2(as_half2(pairs[j / 2]), __floats2half2_rn(a.x, a.y)));
-            hi[j / 2 + 1] = as_u32(__hmul2(as_half2(pairs[j / 2 + 1]), __floats2half2_rn(b.x, b.y)));
+          if (PL == 1) {
+            // P 2^14 from its pairs, dp - D (at most 1) in fp32 until their product is rounded: as fp16 it would be
+            // 0 below 2^-25, and blocks of small d_out would lose what the 2^14 gives them.  (P kept in fp32 instead
+            // spills: 1,393 us for the training shape, 860 so.)
+            const float2 u = mul2(__half22float2(as_half2(pairs[j / 2])), a);
+            const float2 v = mul2(__half22float2(as_half2(pairs[j / 2 + 1])), b);
+            hi[j / 2] = as_u32(__floats2half2_rn(u.x, u.y));
+            hi[j / 2 + 1] = as_u32(__floats2half2_rn(v.x, v.y));
           } else {
             const float2 u = mul2(make_float2(p[j], p[j + 1]), a), v = mul2(make_float2(p[j + 2], p[j + 3]), b);
             d[j] = u.x, d[j + 1] = u.y, d[j + 2] = v.x, d[j + 3] = v.y;
