@@ -1482,8 +1482,9 @@ int32_t check_logprobs(int rows, int vocab, float temperature, int32_t dtype, in
   if (rows < 0) return fail(DFLASH_ERR_INVALID_ARG, "rows %d < 0", rows);
   if (rows > 65535) return fail(DFLASH_ERR_SHAPE, "%d logits rows > 65535", rows);
   if (vocab <= 0 || vocab > (1 << 24)) return fail(DFLASH_ERR_SHAPE, "vocab %d outside [1, 2^24]", vocab);
-  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
-    return fail(DFLASH_ERR_INVALID_ARG, "temperature must be positive and finite, and so its reciprocal");
+  // log2(e) / T, the scale of the exponents, is the first to leave fp32
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(logprob_scale2(temperature)))
+    return fail(DFLASH_ERR_INVALID_ARG, "temperature must be positive and finite, and so log2(e) / temperature");
   if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", dtype);
   if (rows > 1 && row_stride < vocab)
     return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld < vocab %d", (long long)row_stride, vocab);

@@ -451,7 +451,7 @@ cudaError_t launch_fwd(const LogprobArgs& a, int cluster, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOPK, NT>, a, kLog2e / a.temperature, 1.f / a.temperature);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOPK, NT>, a, logprob_scale2(a.temperature), 1.f / a.temperature);
 }
 
 // ---------------------------------------------------------------- gradient

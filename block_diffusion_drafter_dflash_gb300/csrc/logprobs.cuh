@@ -12,6 +12,9 @@ namespace dflash {
 
 constexpr int kMaxTopK = 32;   // alternatives a row may ask for: one per lane of a warp
 
+// The factor of a logit in the exponent of 2.
+inline float logprob_scale2(float temperature) { return 1.4426950408889634f / temperature; }
+
 struct LogprobArgs {
   const void* logits;       // [rows] rows of vocab logits, row_stride elements apart
   int64_t row_stride;

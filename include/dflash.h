@@ -446,8 +446,8 @@ int32_t dflash_packed_attention_status(const void* workspace, dflash_stream_t st
  * Masked logits (-inf, or the type's lowest value) have probability 0.  A row
  * of -inf alone has lse -inf, log probabilities -inf and entropy 0.  A row
  * with a NaN or +inf gives NaN, its top_ids being those of its largest logits
- * that are numbers (-1 where there are none left).  rows <= 65535; 0 < T and
- * 1/T < inf; rows = 0 launches nothing. */
+ * that are numbers (-1 where there are none left).  rows <= 65535; 0 < T < inf
+ * and log2(e) / T < inf (T from 4.24e-39 on); rows = 0 launches nothing. */
 int32_t dflash_token_logprobs(const void* logits_dev, int32_t dtype, int64_t row_stride, const int32_t* tokens_dev,
                               int32_t rows, int32_t vocab, float temperature, int32_t top_k, float* logprob_dev,
                               float* entropy_dev, float* lse_dev, int32_t* top_ids_dev, float* top_logprobs_dev,

@@ -319,3 +319,16 @@ def test_offsets_past_32_bits():
     want = logprob_grad_reference(xd, tokens[:4], 1.0, a, None)
     assert np.all(np.abs(first[:4].double().cpu().numpy() - want)
                   <= _grad_tol(xd, tokens[:4], 1.0, a, None, want, torch.bfloat16))
+
+
+def test_smallest_temperature():
+    """log2(e) / T near fp32's largest: the row's maxima share the probability, everything else has none."""
+    x = torch.full((2, 1000), -0.5, device="cuda")
+    x[0, [3, 700]] = 1.0
+    x[1, 999] = 1.0
+    for dtype in (torch.float32, torch.bfloat16):
+        lp, h, lse, ids, top = _run(x.to(dtype), [700, 0], 4.3e-39, 3)
+        ln2 = float(np.log(2.0))
+        assert abs(float(lp[0]) + ln2) <= 4 * U and abs(float(h[0]) - ln2) <= 4 * U and float(h[1]) == 0
+        assert float(lp[1]) < -3e38 and bool(lse.isfinite().all())
+        assert ids[0, :2].tolist() == [3, 700] and int(ids[1, 0]) == 999 and float(top[1, 0]) == 0

@@ -135,3 +135,12 @@ def test_reference_gradient_is_the_difference_of_the_definition():
             b[r, v] -= eps
             # central differences: O(eps^2) truncation and 2^-52 |f| / eps rounding, both under 1e-8 here
             assert abs((f(a) - f(b)) / (2 * eps) - g[r, v]) < 1e-8
+
+
+@pytest.mark.parametrize("temp", [2.95e-39, 4.2e-39])
+def test_temperature_whose_exponent_scale_overflows_is_refused(L, temp):  # noqa: F811
+    """1 / T is finite, log2(e) / T is not."""
+    assert np.isfinite(np.float32(1) / np.float32(temp))
+    assert _logprobs(L, temp=temp) == -1
+    assert _backward(L, temp=temp) == -1
+    assert _logprobs(L, rows=0, temp=4.3e-39) == 0      # both are finite
