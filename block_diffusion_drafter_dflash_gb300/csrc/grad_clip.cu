@@ -177,6 +177,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_square_sum_kernel(c
   if (threadIdx.x == 0) partial[blockIdx.x] = accumulate ? partial[blockIdx.x] + total : total;
 }
 
+// 16 bytes of gradients times f.
+__device__ __forceinline__ void scale16(uint32_t* w, float f, bool bf16) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      __nv_bfloat162 b = __floats2bfloat162_rn(lo_bf16(w[i]) * f, hi_bf16(w[i]) * f);
+      w[i] = *reinterpret_cast<uint32_t*>(&b);
+    } else {
+      w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+    }
+  }
+}
+
 // Every CTA adds the partial sums of all (in the same order), then scales its
 // chunks, the list's last ones first.
 template <class Tab>
@@ -188,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
   griddep_trigger();
   __shared__ double sh[kThreads];
   __shared__ float s_factor;   // negative: no clipping
+  __shared__ bool s_tiny;
   double v = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) v += partial[i];
   v = block_sum(v, sh);
@@ -195,11 +209,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
     const double norm = sqrt(v);
     if (blockIdx.x == 0 && norm_out) *norm_out = (float)norm;
     const bool over = norm > (double)max_norm && norm <= 1.7976931348623157e308;   // false for NaN and infinity
-    s_factor = over ? (float)((double)max_norm / norm) : -1.f;
+    // a factor below fp32's normal range (gradients near its largest value) is taken in two steps
+    const double factor = (double)max_norm / norm;
+    const bool tiny = factor < 0x1p-126;
+    s_factor = over ? (float)(tiny ? factor * 0x1p126 : factor) : -1.f;
+    s_tiny = tiny;
   }
   __syncthreads();
   const float f = s_factor;
-  const bool clip = f >= 0.f;
+  const bool clip = f >= 0.f, tiny = s_tiny;
   if (!clip && in_place) return;
   for (long long c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const Entry& e = t.e[find_entry(t, c)];
@@ -219,15 +237,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const 
       if (q >= p.nvec) break;
       uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
       if (clip) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (bf16) {
-            __nv_bfloat162 b = __floats2bfloat162_rn(lo_bf16(w[i]) * f, hi_bf16(w[i]) * f);
-            w[i] = *reinterpret_cast<uint32_t*>(&b);
-          } else {
-            w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-          }
-        }
+        scale16(w, f, bf16);
+        if (tiny) scale16(w, 0x1p-126f, bf16);   // exact above fp32's normal range
       }
       const long long b = q << 4;
       if (aligned && b >= p.lo && b + 16 <= p.hi) {

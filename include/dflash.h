@@ -475,8 +475,8 @@ int32_t dflash_token_logprobs_backward(const void* logits_dev, int32_t dtype, in
  * Paper §7.1 trains the drafter with gradients clipped at norm 1.0.  Over all
  * tensors together, norm = sqrt(sum g^2); where it is finite and exceeds
  * max_norm every gradient is multiplied by max_norm / norm, else it stays as
- * it is, bit for bit (a norm of inf or NaN clips nothing: read it and drop the
- * step).
+ * it is, bit for bit (an infinite or NaN gradient makes the norm so and clips
+ * nothing: read it and drop the step).
  *   grads_host, out_host   HOST arrays of n_tensors device pointers; out_host
  *               NULL clips in place, else the (clipped) gradients are written
  *               there; out_host[i] may be grads_host[i] and overlaps no other
@@ -487,8 +487,8 @@ int32_t dflash_token_logprobs_backward(const void* logits_dev, int32_t dtype, in
  *   norm_dev    fp32 [1]: the norm before clipping; in no tensor that is written
  *   workspace   >= dflash_clip_workspace_bytes() bytes, 8-byte aligned
  * The host arrays are read before the call returns.  Sums of squares are kept
- * in double, so finite gradients of any size have a finite norm (norm_dev
- * itself is inf where it exceeds fp32), and are added in a fixed order: the
+ * in double, so finite gradients of any size have a finite norm and are clipped
+ * by it (norm_dev itself is inf where it exceeds fp32), and are added in a fixed order: the
  * same call gives the same bits on the same device. */
 size_t dflash_clip_workspace_bytes(void);
 int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_host, const int64_t* numel_host,

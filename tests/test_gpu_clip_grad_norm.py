@@ -175,3 +175,20 @@ def test_offsets_past_32_bits():
         w = b.double() / want
         assert bool(((a.double() - w).abs() <= w.abs() * (36 * U + (2.0 ** -8 * 1.01 if a.dtype == torch.bfloat16 else 0))
                      + 1e-40).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("max_norm", [1.0, 1e-3, 1e-6])
+def test_factor_outside_fp32(max_norm, dtype):
+    """Gradients near fp32's largest: norm_dev is infinite, the norm finite in double, and max_norm / norm below
+    fp32's normal range (2.5e-46 in the last case, which no fp32 holds)."""
+    grads = _grads([5000, 3, 4000], 2, dtypes=(dtype,), scale=2e37)
+    before = [g.clone() for g in grads]
+    want = _norm(before)
+    assert 3.5e38 < want < 1e40 and all(bool(g.isfinite().all()) for g in grads)
+    norm = _clip(grads, max_norm)
+    assert float(norm) == float("inf")
+    own = 36 * U + (2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 0)
+    for b, a in zip(before, grads):
+        w = b.double() * (float(torch.tensor(max_norm)) / want)
+        assert bool(((a.double() - w).abs() <= w.abs() * own + 1e-40).all())
