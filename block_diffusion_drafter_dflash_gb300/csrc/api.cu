@@ -1541,12 +1541,21 @@ int32_t dflash_token_logprobs_backward(const void* logits, int32_t dtype, int64_
     return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld of the gradient < vocab %d", (long long)d_row_stride, vocab);
   const size_t es = dtype == DFLASH_DTYPE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(d_logits) % es) return fail(DFLASH_ERR_INVALID_ARG, "d_logits is not aligned to its type");
-  // the gradient may take the logits' place, element for element; any other overlap would be read after it is written
-  const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(d_logits);
-  const uintptr_t x1 = x0 + ((size_t)(rows - 1) * (rows > 1 ? row_stride : 0) + vocab) * es;
-  const uintptr_t d1 = d0 + ((size_t)(rows - 1) * (rows > 1 ? d_row_stride : 0) + vocab) * es;
-  if (x0 < d1 && d0 < x1 && !(x0 == d0 && (rows == 1 || row_stride == d_row_stride)))
-    return fail(DFLASH_ERR_INVALID_ARG, "d_logits overlaps the logits without being the same rows");
+  // The gradient may take the logits' place, element for element, or lie between their rows (equal strides, and from
+  // the start of a row of the one to the next start of the other at least a row's length); any other overlap would be
+  // read after it is written.
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), d0 = reinterpret_cast<uintptr_t>(d_logits), len = vocab * es;
+  const uintptr_t x1 = x0 + (size_t)(rows - 1) * (rows > 1 ? row_stride : 0) * es + len;
+  const uintptr_t d1 = d0 + (size_t)(rows - 1) * (rows > 1 ? d_row_stride : 0) * es + len;
+  const bool same = x0 == d0 && (rows == 1 || row_stride == d_row_stride);
+  if (x0 < d1 && d0 < x1 && !same) {
+    bool between = rows > 1 && row_stride == d_row_stride;
+    if (between) {
+      const uintptr_t step = (size_t)row_stride * es, behind = d0 >= x0 ? (d0 - x0) % step : (step - (x0 - d0) % step) % step;
+      between = behind >= len && step - behind >= len;
+    }
+    if (!between) return fail(DFLASH_ERR_INVALID_ARG, "d_logits overlaps the logits without being the same rows");
+  }
   LogprobGradArgs a{};
   a.logits = logits;
   a.row_stride = row_stride;

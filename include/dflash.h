@@ -460,8 +460,8 @@ int32_t dflash_token_logprobs(const void* logits_dev, int32_t dtype, int64_t row
  *   d_logprob_dev with tokens_dev, and d_entropy_dev with entropy_dev, fp32
  *               [rows]; either pair may be NULL, not both
  *   d_logits_dev  [rows][vocab] in `dtype`, rows d_row_stride apart, rounded to
- *               nearest; may be the logits themselves (the same rows), and
- *               overlaps them in no other way
+ *               nearest; may be the logits themselves (the same rows) or lie
+ *               between their rows, and overlaps them in no other way
  * A token outside [0, vocab) has no gradient of its log probability; neither
  * has a row that masks everything (lse below -1e30) any gradient.  p is
  * computed from lse, so its relative error grows as |lse| * 2^-24. */

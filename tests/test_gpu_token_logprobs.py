@@ -332,3 +332,30 @@ def test_smallest_temperature():
         assert abs(float(lp[0]) + ln2) <= 4 * U and abs(float(h[0]) - ln2) <= 4 * U and float(h[1]) == 0
         assert float(lp[1]) < -3e38 and bool(lse.isfinite().all())
         assert ids[0, :2].tolist() == [3, 700] and int(ids[1, 0]) == 999 and float(top[1, 0]) == 0
+
+
+def test_gradient_between_the_logits_rows():
+    """d_logits in the gaps between the logits' rows, before and behind them, overlaps nothing: the bits of a separate
+    gradient, and the logits and what lies between stay.  A gap that is one element short is refused."""
+    df = _df()
+    R, V = 5, 1003
+    for dtype in (torch.float32, torch.bfloat16):
+        for at_x, at_d in ((0, V + 1), (V, 0), (2, V + 2)):
+            store = torch.full((R + 1, 2 * V + 3), 5.0, dtype=dtype, device="cuda")
+            x, d = store[:R, at_x:at_x + V], store[:R, at_d:at_d + V]
+            x.copy_(_logits(R, V, dtype, 3))
+            kept = store.clone()
+            tok = torch.arange(R, dtype=torch.int32, device="cuda")
+            g, lse = torch.linspace(-1, 1, R, device="cuda"), torch.empty(R, device="cuda")
+            df.dflash_token_logprobs(x, None, 0.9, None, lse=lse)
+            alone = torch.empty((R, V), dtype=dtype, device="cuda")
+            df.dflash_token_logprobs_backward(x, tok, 0.9, lse, alone, d_logprob=g)
+            df.dflash_token_logprobs_backward(x, tok, 0.9, lse, d, d_logprob=g)
+            assert torch.equal(d, alone)
+            kept[:R, at_d:at_d + V] = alone
+            assert torch.equal(store, kept)
+            for shift in (1, 2 * V + 3 - 1):
+                bad = store.view(-1)[at_x + V - 1 if shift == 1 else at_x + V + 4:]
+                bad = bad.as_strided((R, V), (2 * V + 3, 1), bad.storage_offset())
+                with pytest.raises(df.DFlashError):
+                    df.dflash_token_logprobs_backward(x, tok, 0.9, lse, bad, d_logprob=g)
