@@ -57,7 +57,11 @@
 // take each operand, P and ds included, as a hi + lo pair (22 bits) and each
 // product as three MMAs (hi hi, hi lo, lo hi).  Every sum and the softmax are fp32;
 // the tensor cores' sums truncate (by 2e-8 a step of 16 rows, measured, all to the
-// same side), so those of fp32 tensors are kept short.
+// same side), so those of fp32 tensors are kept short: a context item moves them to
+// its share's memory every 96 steps.  512 blocks of 16 in 4,096 positions, 32/8 heads:
+// 3.04 ms with heads of 128 and 1.50 with 64.  Never moved: 2.85 ms, but an error of
+// 1.6e-5 of the gradients' norm instead of 2.4e-6 (200 blocks in 3,000); a share in
+// memory for every 8 tiles instead: 3.49 ms and 2.1 GB of them.
 #include <cuda.h>
 
 #include <algorithm>
@@ -702,6 +706,10 @@ struct GradCfg {
   // the large one takes a third of the steps.
   static constexpr int kColP = 128, kColV = 256, kColK = kColV + HD, kLoKeys = PL == 2 && HD == 64 ? 2 * HD : 0;
   static constexpr int kColPRows = 2 * kN, kColQ = kN == 64 ? 256 : 384, kLoRows = PL == 2 ? HD : 0;
+  // Two planes: streamed tiles after which a context item moves its sums to memory
+  // and starts them again, 96 truncating steps of 16 rows (8 a tile with heads of 64,
+  // whose small products have sums of their own, 12 with 128).
+  static constexpr int kDrain = HD == 64 ? 12 : 8;
   static constexpr uint32_t kTmem = 512;
   static_assert(kColK + kLoKeys + HD <= 512 && kColQ + kLoRows + HD <= 512 && kColPRows + kN <= kColQ, "tensor memory");
   static_assert(kBytes <= 227 * 1024 && 2 * kRows * kPitch <= kOffStat, "shared memory");
@@ -768,6 +776,54 @@ __device__ __forceinline__ void mma_gradient(uint32_t d, uint32_t a, uint32_t st
                str + (pb * C::kSub * C::kStrTile >> 4) + k * (2048 >> 4), id, acc);
       acc = 1;
     }
+  }
+}
+
+// 32 columns of a gradient in tensor memory, with the small products' sum `lo`
+// columns further (0: none).
+__device__ __forceinline__ void read_sum(uint32_t at, int lo, float* v) {
+  uint32_t raw[32];
+  tmem_ld<32>(at, raw);
+  tmem_ld_wait();
+  tmem_values<32>(raw, v);
+  if (lo) {
+    float small[32];
+    tmem_ld<32>(at + lo, raw);
+    tmem_ld_wait();
+    tmem_values<32>(raw, small);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += small[j];
+  }
+}
+// A key's gradients of a share while its item still runs: [hd / 4][128 keys][4], so
+// that a warp's accesses are consecutive.  `d` is the thread's place of 32 columns;
+// each thread meets its own values only.
+__device__ __forceinline__ void add_so_far(const float4* d, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 b = __ldcg(d + j * kRows);
+    v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+  }
+}
+// dK and dV of this thread's key (columns `at` and `at` - HD of tensor memory) into
+// dk and dv in memory.  The warps of a lane quarter take the 32-column groups of
+// both in turn.  A call, so that its registers are not the main loop's.
+template <int HD, int LO>
+__device__ __noinline__ void drain_sums(uint32_t at, float4* dk, float4* dv, int part, float to_k, float to_k2, float to_v,
+                                        float to_v2, bool fresh) {
+  constexpr int kGroups = HD / 32;
+#pragma unroll 1
+  for (int gq = part; gq < 2 * kGroups; gq += kParts) {
+    const int m = gq / kGroups, c = gq % kGroups * 32;   // 0: dK, 1: dV
+    float v[32];
+    read_sum(at - m * HD + c, LO, v);
+    const float a = m ? to_v : to_k, b = m ? to_v2 : to_k2;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = v[j] * a * b;
+    float4* d = (m ? dv : dk) + c / 4 * kRows;
+    if (!fresh) add_so_far(d, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) __stcg(d + j * kRows, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
   }
 }
 
@@ -979,9 +1035,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
         next1();
         for (int i = 0; i < n; ++i) {
           const bool more = i + 1 < n;
+          // (sums start again where the warps have moved them to memory, which p_ready says)
+          const uint32_t go_on = (PL == 2 && kind == 0 ? i % C::kDrain : i) != 0;
           if (more ? !wait2(&bars->full0[n0], ph0, &bars->p_ready, i & 1) : !wait(&bars->p_ready, i & 1)) break;
           if (elect()) {
-            mma_gradient<HD, PL, C::kLoKeys>(tV, tS, g1 + s1 * kStep, i > 0);
+            mma_gradient<HD, PL, C::kLoKeys>(tV, tS, g1 + s1 * kStep, go_on);
             ptx::mma_commit(&bars->freed1[s1]);
             if (more) {
               mma_scores<HD, PL>(tS, ra, k0 + n0 * kStep);
@@ -991,7 +1049,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           __syncwarp();
           if (more && kAhead ? !wait2(&bars->full1[n1], ph1, &bars->ds_ready[0], i & 1) : !wait(&bars->ds_ready[0], i & 1)) break;
           if (elect()) {
-            mma_gradient<HD, PL, C::kLoKeys>(tK, tP, g0 + s0 * kStep, i > 0);
+            mma_gradient<HD, PL, C::kLoKeys>(tK, tP, g0 + s0 * kStep, go_on);
             ptx::mma_commit(&bars->freed0[s0]);
           }
           __syncwarp();
@@ -1073,21 +1131,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
       return ok;
     };
     const int own = me / pl.block;            // block of my lane's row or key within its tile
-    // 32 columns of a gradient, with the small products' sum `lo` columns further (0: none)
-    auto read_sum = [&](uint32_t at, int lo, float* v) {
-      uint32_t raw[32];
-      tmem_ld<32>(at, raw);
-      tmem_ld_wait();
-      tmem_values<32>(raw, v);
-      if (lo) {
-        float small[32];
-        tmem_ld<32>(at + lo, raw);
-        tmem_ld_wait();
-        tmem_values<32>(raw, small);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += small[j];
-      }
-    };
     // staged output rows: matrix m's row r at m * kRows * kPitch + r * kPitch
     auto stage32 = [&](int m, int c, const float* v, bool wide) {   // 32 columns from c on
       uint8_t* d = sm + (size_t)(m * kRows + me) * C::kPitch + c * (wide ? 4 : (int)sizeof(T));
@@ -1139,91 +1182,106 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < NC / 4; ++j) st[j] = x[j];
       };
-      if (wait(&bars->full0[0], 0)) load_stats(0);
-      for (int i = 0; i < n; ++i) {
-        const int r0 = row0 + in_head * C::kN + c0;   // my first column's row
-        const bool compare = kind == 2 || r0 < whole * kRows;
-        if (++in_head == per_head) in_head = 0;
-        if (!wait(&bars->s_full, i & 1)) break;
-        const int anchor = kind == 0 && compare ? __ldg(pl.row_anchor + r0 + lane % NC) : 0;   // of column `lane`
-        // P: as the fp16 pairs that enter dV and, with two planes, as fp32
-        uint32_t pairs[NC / 2];
-        float p[NC];
-        {
-          uint32_t raw[NC];
-          tmem_ld<NC>(tS, raw);
-          tmem_ld_wait();
-          tmem_values<NC>(raw, p);
-        }
+      auto so_far = [&](float* base) {   // my key's place in this share's rows
+        return reinterpret_cast<float4*>(base + (((size_t)h * pl.splits + share) * ctx + tile * kRows) * HD) + me;
+      };
+      int i = 0;
+      for (;;) {
+        const int end = PL == 2 && kind == 0 ? min(n, i + C::kDrain) : n;
+        if (wait(&bars->full0[s0], ph0)) load_stats(s0);
+        for (; i < end; ++i) {
+          const int r0 = row0 + in_head * C::kN + c0;   // my first column's row
+          const bool compare = kind == 2 || r0 < whole * kRows;
+          if (++in_head == per_head) in_head = 0;
+          if (!wait(&bars->s_full, i & 1)) break;
+          const int anchor = kind == 0 && compare ? __ldg(pl.row_anchor + r0 + lane % NC) : 0;   // of column `lane`
+          // P: as the fp16 pairs that enter dV and, with two planes, as fp32
+          uint32_t pairs[NC / 2];
+          float p[NC];
+          {
+            uint32_t raw[NC];
+            tmem_ld<NC>(tS, raw);
+            tmem_ld_wait();
+            tmem_values<NC>(raw, p);
+          }
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-          const float4 l = st[j / 4];
-          const float2 a = fma2(make_float2(p[j], p[j + 1]), make_float2(sc2, sc2), make_float2(-l.x, -l.y));
-          const float2 b = fma2(make_float2(p[j + 2], p[j + 3]), make_float2(sc2, sc2), make_float2(-l.z, -l.w));
-          p[j] = ex2(a.x);
-          p[j + 1] = ex2(a.y);
-          p[j + 2] = ex2(b.x);
-          p[j + 3] = ex2(b.y);
-        }
-        if (compare) {
-          int from = own * pl.block - (r0 - row0), to = from + pl.block;   // own keys: my block's rows
-          if (kind == 0) {   // the rows from the first one anchored behind my key on (anchors ascend)
-            from = 0;
-            to = NC;
+          for (int j = 0; j < NC; j += 4) {
+            const float4 l = st[j / 4];
+            const float2 a = fma2(make_float2(p[j], p[j + 1]), make_float2(sc2, sc2), make_float2(-l.x, -l.y));
+            const float2 b = fma2(make_float2(p[j + 2], p[j + 3]), make_float2(sc2, sc2), make_float2(-l.z, -l.w));
+            p[j] = ex2(a.x);
+            p[j + 1] = ex2(a.y);
+            p[j + 2] = ex2(b.x);
+            p[j + 3] = ex2(b.y);
+          }
+          if (compare) {
+            int from = own * pl.block - (r0 - row0), to = from + pl.block;   // own keys: my block's rows
+            if (kind == 0) {   // the rows from the first one anchored behind my key on (anchors ascend)
+              from = 0;
+              to = NC;
 #pragma unroll 1
-            for (int step = NC / 2; step; step /= 2)
-              if (__shfl_sync(0xffffffffu, anchor, from + step - 1) <= key) from += step;
-            if (__shfl_sync(0xffffffffu, anchor, from) <= key) ++from;
+              for (int step = NC / 2; step; step /= 2)
+                if (__shfl_sync(0xffffffffu, anchor, from + step - 1) <= key) from += step;
+              if (__shfl_sync(0xffffffffu, anchor, from) <= key) ++from;
+            }
+            keep_columns<NC>(p, from, to);
           }
-          keep_columns<NC>(p, from, to);
-        }
-        pairs_of<NC>(p, pairs);
-        put_pairs<PL, NC>(tS, pairs, p);
-        tmem_st_wait();
-        arrive(&bars->p_ready);
-        if (!wait(&bars->full1[s1], ph1)) break;
-        load_stats(C::kS0 + s1);
-        if (++s1 == C::kS1) s1 = 0, ph1 ^= 1;
-        if (!wait(&bars->dp_full, i & 1)) break;
-        uint32_t hi[NC / 2];
-        float d[NC];
-        {
-          uint32_t raw[NC];
-          tmem_ld<NC>(tP, raw);
-          tmem_ld_wait();
-          tmem_values<NC>(raw, d);
-        }
-        const float2 f = make_float2(f_dp, f_dp);
+          pairs_of<NC>(p, pairs);
+          put_pairs<PL, NC>(tS, pairs, p);
+          tmem_st_wait();
+          arrive(&bars->p_ready);
+          if (!wait(&bars->full1[s1], ph1)) break;
+          load_stats(C::kS0 + s1);
+          if (++s1 == C::kS1) s1 = 0, ph1 ^= 1;
+          if (!wait(&bars->dp_full, i & 1)) break;
+          uint32_t hi[NC / 2];
+          float d[NC];
+          {
+            uint32_t raw[NC];
+            tmem_ld<NC>(tP, raw);
+            tmem_ld_wait();
+            tmem_values<NC>(raw, d);
+          }
+          const float2 f = make_float2(f_dp, f_dp);
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-          const float4 x = st[j / 4];
-          const float2 a = fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y));
-          const float2 b = fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w));
-          if (PL == 1) {
-            // P 2^14 from its pairs, dp - D (at most 1) in fp32 until their product is rounded: as fp16 it would be
-            // 0 below 2^-25, and blocks of small d_out would lose what the 2^14 gives them.  (P kept in fp32 instead
-            // spills: 1,393 us for the training shape, 860 so.)
-            const float2 u = mul2(__half22float2(as_half2(pairs[j / 2])), a);
-            const float2 v = mul2(__half22float2(as_half2(pairs[j / 2 + 1])), b);
-            hi[j / 2] = as_u32(__floats2half2_rn(u.x, u.y));
-            hi[j / 2 + 1] = as_u32(__floats2half2_rn(v.x, v.y));
-          } else {
-            const float2 u = mul2(make_float2(p[j], p[j + 1]), a), v = mul2(make_float2(p[j + 2], p[j + 3]), b);
-            d[j] = u.x, d[j + 1] = u.y, d[j + 2] = v.x, d[j + 3] = v.y;
+          for (int j = 0; j < NC; j += 4) {
+            const float4 x = st[j / 4];
+            const float2 a = fma2(make_float2(d[j], d[j + 1]), f, make_float2(-x.x, -x.y));
+            const float2 b = fma2(make_float2(d[j + 2], d[j + 3]), f, make_float2(-x.z, -x.w));
+            if (PL == 1) {
+              // P 2^14 from its pairs, dp - D (at most 1) in fp32 until their product is rounded: as fp16 it would be
+              // 0 below 2^-25, and blocks of small d_out would lose what the 2^14 gives them.  (P kept in fp32 instead
+              // spills: 1,393 us for the training shape, 860 so.)
+              const float2 u = mul2(__half22float2(as_half2(pairs[j / 2])), a);
+              const float2 v = mul2(__half22float2(as_half2(pairs[j / 2 + 1])), b);
+              hi[j / 2] = as_u32(__floats2half2_rn(u.x, u.y));
+              hi[j / 2 + 1] = as_u32(__floats2half2_rn(v.x, v.y));
+            } else {
+              const float2 u = mul2(make_float2(p[j], p[j + 1]), a), v = mul2(make_float2(p[j + 2], p[j + 3]), b);
+              d[j] = u.x, d[j + 1] = u.y, d[j + 2] = v.x, d[j + 3] = v.y;
+            }
+          }
+          if (PL == 2) pairs_of<NC>(d, hi);
+          put_pairs<PL, NC>(tP, hi, d);
+          tmem_st_wait();
+          arrive(&bars->ds_ready[0]);
+          if (++s0 == C::kS0) s0 = 0, ph0 ^= 1;
+          if (i + 1 < end) {
+            if (!wait(&bars->full0[s0], ph0)) break;
+            load_stats(s0);
           }
         }
-        if (PL == 2) pairs_of<NC>(d, hi);
-        put_pairs<PL, NC>(tP, hi, d);
-        tmem_st_wait();
-        arrive(&bars->ds_ready[0]);
-        if (++s0 == C::kS0) s0 = 0, ph0 ^= 1;
-        if (i + 1 < n) {
-          if (!wait(&bars->full0[s0], ph0)) break;
-          load_stats(s0);
-        }
+        if (PL == 1 || !ok || i == n) break;
+        // dK(i - 1) is the last to add to the sums.  (Its stage's phase before that one has completed: tile i - 1,
+        // which the warps have seen, was loaded after it.)
+        if (!wait(&bars->freed0[(i - 1) % C::kS0], par0(i - 1))) break;
+        const Pow2 to_v(-kPExp - sc.o), to_k(-kPExp - sc.dp - sc.q);
+        drain_sums<HD, C::kLoKeys>(tmem + lanes + C::kColK, so_far(pl.dk_part), so_far(pl.dv_part), part, to_k.a * scale,
+                                   to_k.b, to_v.a, to_v.b, i == C::kDrain);
       }
       // ---- dV and dK of my key: the warps of a lane quarter take the 32-column groups of both in turn
       wait(&bars->done, 0);
+      const bool drained = PL == 2 && kind == 0 && n > C::kDrain;
       if (ok) {
         const Pow2 to_v(-kPExp - sc.o), to_k(-kPExp - sc.dp - sc.q);
 #pragma unroll
@@ -1233,16 +1291,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) packed_grad_kernel(const __gr
           read_sum(tmem + lanes + (m ? C::kColV : C::kColK) + c, C::kLoKeys, v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = m ? to_v(v[j]) : to_k(v[j] * scale);
+          if (drained) add_so_far(so_far(m ? pl.dv_part : pl.dk_part) + c / 4 * kRows, v);
           stage32(m, c, v, kind == 0);
         }
       }
+      if (drained) ptx::fence_proxy_async_global();   // the rows go where the sums so far were
       void* dst = nullptr;
       if (ok && tid < 2 * kRows) {
         const int r = tid % kRows;
         const bool v = tid >= kRows;
         if (kind == 0) {
           if (tile * kRows + r < pl.S)
-            dst = (v ? pl.dv_part : pl.dk_part) + (((size_t)h * pl.splits + share) * pl.S + tile * kRows + r) * HD;
+            dst = (v ? pl.dv_part : pl.dk_part) + (((size_t)h * pl.splits + share) * ctx + tile * kRows + r) * HD;
         } else {
           dst = block_row(v ? t.d_v_blk : t.d_k_blk, r, pl.nkv, kvh);
         }
@@ -1331,7 +1391,7 @@ __global__ void __launch_bounds__(256) reduce_ctx_kernel(PackedBwdPlan pl, T* dk
   const int shares = s_shares, e = blockIdx.x % kParts * 256 + threadIdx.x;
   const int s = tile * kRows + e / Q, d = e % Q * 4;
   if (s >= pl.S) return;
-  const size_t slab = (size_t)pl.S * HD, src = (size_t)h * pl.splits * slab + (size_t)s * HD + d;
+  const size_t slab = (size_t)pl.KT * kRows * HD, src = (size_t)h * pl.splits * slab + (size_t)s * HD + d;
   float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
   for (int i = 0; i < shares; ++i) {
     const float4 a = __ldcs(reinterpret_cast<const float4*>(pl.dk_part + src + i * slab));
@@ -1433,13 +1493,13 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   // 926, 128 -> 109 and 876; of 8 x 2: 3 -> 32 us, 12 -> 53.)
   const int per = kRows / (f32 && hd == 128 ? GradCfg<128, 2>::kN : kRows);
   const long long all = (long long)(nq / nkv) * p.T * per;
-  // fp32 tensors: at most 96 steps of 16 rows on a sum that the tensor cores truncate
-  // at each (12 tiles of 8 with head size 64, where the small products have sums of
-  // their own, else 8 of 12).  200 blocks of 16 in 3,000 positions, 8 / 2 heads of 64
-  // and of 128: 12 -> 2.0e-6 of the gradients' norm and 140 us, 31 -> 5.4e-6 and 133;
-  // 8 -> 2.0e-6 and 323 us, 63 -> 1.6e-5 and 262 (1.9e-6 with plain fp32 sums).
-  const long long most = !f32 ? 128 : hd == 64 ? 12 : 8;
-  p.share = (int)std::max(3LL, std::min(most, all * p.KT * nkv / sms));
+  // Each share has its own rows in memory, so no more of them than make about eight
+  // items an SM: that memory follows the SM count and the context, not the blocks
+  // (4,096 blocks of 16 in 32,768 positions, 32/8 heads of 128: 0.27 GB; shares of 128
+  // tiles would take 4.3).  It costs no time: that case takes 38.6 ms in bf16 (44.9 with
+  // shares of 128), 1,024 blocks in 8,192 2.77 (2.78).
+  const long long tiles = std::max(1LL, (long long)p.KT * nkv), most = (8LL * sms + tiles - 1) / tiles;
+  p.share = (int)std::max({3LL, std::min(128LL, all * p.KT * nkv / sms), (all + most - 1) / most});
   p.splits = (int)((all + p.share - 1) / p.share);
   const size_t rows = (size_t)p.T * kRows, ctx = (size_t)std::max(p.KT, 1) * kRows;
   char* c = static_cast<char*>(ws);
@@ -1467,7 +1527,7 @@ PackedBwdPlan packed_bwd_plan(void* ws, int N, int block, int S, int nq, int nkv
   p.vc = reinterpret_cast<__half*>(take(pe * ctx * nkv * hd));
   p.kb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
   p.vb = reinterpret_cast<__half*>(take(pe * rows * nkv * hd));
-  const size_t part = 4 * (size_t)nkv * p.splits * S * hd;
+  const size_t part = 4 * (size_t)nkv * p.splits * p.KT * kRows * hd;
   p.dk_part = reinterpret_cast<float*>(take(part));
   p.dv_part = reinterpret_cast<float*>(take(part));
   p.bytes = at;

@@ -37,7 +37,7 @@ struct PackedBwdPlan {
   __half* vc;
   __half* kb;             // [nkv][planes][T*128][hd]
   __half* vb;
-  float* dk_part;         // [nkv][splits][S][hd] each share's sum of d_k_ctx
+  float* dk_part;         // [nkv][splits][KT*128][hd] each share's sum of d_k_ctx
   float* dv_part;
   size_t bytes;
 };
