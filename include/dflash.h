@@ -402,12 +402,23 @@ int32_t dflash_packed_block_attention_lse(const void* q_dev, const void* k_ctx_d
  *               256-byte aligned; its first int32 is the call's status word
  *               (dflash_packed_attention_status)
  * Operands that some block sees have to be finite: a NaN or an infinity
- * spreads to gradients that do not depend on it.  Operands, P and ds enter their products as scaled fp16
- * (fp32 operands: as hi/lo pairs of it, 22 bits), sums are fp32: what is
- * 2^-28 of a tensor's largest value (of 1, for P) or less loses bits, and below
- * 2^-39 counts as 0.  The tensor cores truncate their sums, so that fp32
- * gradients are good to about 2e-6 of their norm with contexts of a few
- * thousand positions (d_q loses in proportion to longer ones).  Context rows that no block sees are not read.  The same
+ * spreads to gradients that do not depend on it.  Context rows that no block
+ * sees are not read.
+ * Precision.  Sums are fp32; operands, P and ds enter their products as fp16 with
+ * one power of two a tensor: bf16 tensors as one fp16 (q, k and v exactly; d_out,
+ * P and ds rounded to 2^-12 of themselves), fp32 tensors as a hi/lo pair of them
+ * (22 bits).  Against a tensor's largest value (P: 1; ds: twice the largest norm
+ * of a row of d_out times that of a row of v, but for d_q the row's own norm of
+ * d_out) one fp16 loses bits below 2^-28 and a pair some of its 22 from 2^-17 on;
+ * both count what is below 2^-39 as 0.  So the d_k of blocks, and of context that
+ * only they see, is good to bf16's rounding where their d_out is 2^-16 of the
+ * largest, but to fewer bits than the others' for fp32 tensors.  The tensor cores
+ * truncate their sums: given exact out and lse, fp32 gradients are good to about
+ * 2.5e-6 of their norm with contexts of a few thousand positions (d_q loses in
+ * proportion to longer ones).  The forward's own lse and out of fp32 tensors are
+ * off by up to 3 * 2^-18 of a score's terms, which the gradients inherit: 1 to
+ * 3e-6 of their norm in all with scores of about 1, 1e-5 with scores of about 3.
+ * The same
  * call gives the same bits on the same device.  n_blocks = 0 zeroes
  * d_k_ctx and d_v_ctx.  The forward's limits, and 2^31 rows of laid-out
  * operands.  The workspace size depends on the current device's SM count. */

@@ -133,3 +133,33 @@ def test_one_value_row_far_larger(dtype):
         ref, got, want = gradients(ops, anchors, d_out, dtype)
         e2 = squared_errors(ref, anchors, d_out.double(), want, dtype)
         check(got, want, e2, range(N // 2, N), slice(150, S), f"2^-{k}")
+
+
+@pytest.mark.parametrize("S,N,g,nq,nkv,hd,larger", [(300, 20, 6, 4, 2, 64, 1.0), (1000, 96, 7, 4, 2, 64, 1.0),
+                                                    (3000, 200, 16, 8, 2, 128, 1.0), (1000, 60, 16, 8, 2, 128, 3.0)])
+def test_fp32_forward_and_gradient_together(S, N, g, nq, nkv, hd, larger):
+    """fp32 gradients from the library's own out and lse, by norm.  The forward's operands are bf16 hi/lo pairs: each
+    product of a score is off by 2^-18 for either operand and for the lo lo part, independently, the score by e =
+    sqrt(3) * 2^-18 of the root of its terms' squares (their mean over the rows, weighted by P).  lse is off by e at
+    most, P by that factor, out by twice that and v's 2^-18, and ds by what P and D are off."""
+    df = _df()
+    anchors = torch.randint(0, S + 1, (N,), generator=torch.Generator().manual_seed(13)).tolist()
+    ops = operands(S, N, g, nq, nkv, hd, torch.float32, 14, "cuda")
+    ops = (ops[0] * larger, *ops[1:])
+    d_out = torch.randn(ops[0].shape, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    a = torch.tensor(anchors, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(ops[0], math.nan), torch.full((N, g, nq), math.nan, device="cuda")
+    df.dflash_packed_block_attention(*ops, a, out, df.dflash_packed_attention_workspace(N, g, S, nq, nkv, hd), lse=lse)
+    got = [torch.full_like(t, math.nan) for t in ops]
+    ws = df.dflash_packed_attention_backward_workspace(N, g, S, nq, nkv, hd, torch.float32)
+    df.dflash_packed_block_attention_backward(*ops, a, out, lse, d_out, *got, ws)
+    assert df.dflash_packed_attention_status(ws) == 0
+    ref = [t.double() for t in ops]
+    q2, (k2, b2) = ref[0].square(), (t.square().repeat_interleave(nq // nkv, dim=-2) for t in (ref[1], ref[3]))
+    p = forward_reference(*ref, anchors)[2]
+    terms = (p[..., :S] * torch.einsum("nihd,shd->nihs", q2, k2)).sum() + (p[..., S:] * torch.einsum("nihd,njhd->nihj", q2, b2)).sum()
+    e = math.sqrt(3.0) * 2.0 ** -18 * math.sqrt(float(terms) / (N * g * nq) / hd)
+    for name, x, w in zip(NAMES, got, backward_reference(*ref, anchors, d_out.double())):
+        err = float((x.double() - w).norm() / w.norm())
+        print(f"{name}: rel {err:.2e} (bound {3 * e + 2.0 ** -18 + 96 * 2.0 ** -24 + 2.0 ** -20:.1e})")
+        assert err <= 3 * e + 2.0 ** -18 + 96 * 2.0 ** -24 + 2.0 ** -20, name
