@@ -384,8 +384,8 @@ def dflash_packed_block_attention_backward(q: torch.Tensor, k_ctx: torch.Tensor,
         _abi.DTYPE_F32 if dt == torch.float32 else _abi.DTYPE_BF16, _vector(out, rows, torch.float32, q, "out"),
         _vector(lse, N * g * nq, torch.float32, q, "lse"), _vector(d_out, rows, torch.float32, q, "d_out"),
         vec(d_q, rows, "d_q"), vec(d_k_ctx, ctx, "d_k_ctx"), vec(d_v_ctx, ctx, "d_v_ctx"), vec(d_k_blk, blk, "d_k_blk"),
-        vec(d_v_blk, blk, "d_v_blk"), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream)), "dflash_packed_block_attention_backward")
+        vec(d_v_blk, blk, "d_v_blk"), *_workspace(workspace, q), _stream_ptr(stream)),
+        "dflash_packed_block_attention_backward")
 
 
 def dflash_packed_attention_status(workspace: torch.Tensor, stream=None) -> int:
@@ -419,6 +419,14 @@ def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.T
     if t.dtype is not dtype or t.numel() != n or t.get_device() != like.get_device() or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on {like.device}")
     return t.data_ptr()
+
+
+def _workspace(t: torch.Tensor, like: torch.Tensor):
+    """(address, bytes) of a workspace on the device of `like`."""
+    at = _ptr(t)
+    if t is not None and t.get_device() != like.get_device():
+        raise ValueError(f"the workspace must be on {like.device}")
+    return at, 0 if t is None else t.numel() * t.element_size()
 
 
 def _on_current_device(t: torch.Tensor) -> None:
@@ -519,8 +527,8 @@ def dflash_clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None,
         workspace = _scratch(int(lib().dflash_clip_workspace_bytes()), stream)
     check(lib().dflash_clip_grad_norm(
         at, None if out is None else at + 8 * n, sizes.buffer_info()[0], types.buffer_info()[0], n, float(max_norm),
-        _vector(norm, 1, torch.float32, norm, "norm"), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream)), "dflash_clip_grad_norm")
+        _vector(norm, 1, torch.float32, norm, "norm"), *_workspace(workspace, norm), _stream_ptr(stream)),
+        "dflash_clip_grad_norm")
 
 
 class BlockPolicy:

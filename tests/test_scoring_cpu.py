@@ -144,3 +144,24 @@ def test_temperature_whose_exponent_scale_overflows_is_refused(L, temp):  # noqa
     assert _logprobs(L, temp=temp) == -1
     assert _backward(L, temp=temp) == -1
     assert _logprobs(L, rows=0, temp=4.3e-39) == 0      # both are finite
+
+
+def test_workspace_on_another_device_is_refused():
+    """By the device's number alone: stand-ins for tensors of two devices."""
+    import block_diffusion_drafter_dflash_gb300 as df
+
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, device):
+            self.index, self.device = device, f"cuda:{device}"
+
+        get_device = lambda self: self.index  # noqa: E731
+        is_contiguous = lambda self: True  # noqa: E731
+        data_ptr = lambda self: P  # noqa: E731
+        numel = lambda self: 100  # noqa: E731
+        element_size = lambda self: 2  # noqa: E731
+
+    assert df._workspace(OnDevice(1), OnDevice(1)) == (P, 200)
+    with pytest.raises(ValueError):
+        df._workspace(OnDevice(1), OnDevice(0))
