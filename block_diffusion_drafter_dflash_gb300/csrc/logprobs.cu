@@ -12,7 +12,7 @@
 // reads and writes every logit once.  Measured on rows of 151,936 logits: 480 fp32
 // rows with 5 alternatives 49.2 us (5.9 TB/s), 2,048 bf16 rows 101 us (6.1 TB/s),
 // their gradient 177 us (7.0 TB/s of reads and writes); one fp32 row with 20
-// alternatives 9.1 us, which is latency: the launch, 37 KB to each of eight SMs,
+// alternatives 9.1 us, which is latency: the launch, 76 KB to each of eight SMs,
 // the bar's and the lists' sorts and the cluster's two barriers.
 //
 // Forward.  A row is one cluster of C CTAs, each taking a C-th of it (C = 1
@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_backward_kernel(Lo
       }
     }
   } else {
-    // rows whose two alignments differ: element by element, coalesced
+    // rows whose two alignments differ: element by element, coalesced (2,048 rows of
+    // 151,935: 518 us in bf16, 689 in fp32, against 179 and 349 by vectors)
     const int u_first = blockIdx.x * kBwdThreads * kBwdVec * E + threadIdx.x;
 #pragma unroll 8
     for (int j = 0; j < kBwdVec * E; ++j) {
@@ -560,8 +561,8 @@ cudaError_t launch_bwd(const LogprobGradArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t token_logprobs_launch(const LogprobArgs& a, bool bf16, int sms, cudaStream_t s) {
-  // One CTA an SM at most, two vectors a thread at least, in clusters: a row
-  // alone is spread over eight SMs (151,936 fp32 logits, 20 alternatives: 27.0 us on
+  // A row's cluster doubles while that leaves at most 1.25 CTAs an SM and at least two
+  // vectors a thread: a row alone is spread over eight SMs (151,936 fp32 logits, 20 alternatives: 27.0 us on
   // one, 11.4 on eight), 77 rows of 32,003 over two each (13.9 on one, 11.7 on two,
   // 12.9 on eight), 1,000 logits stay on one (4.4 us, 7.8 on eight).
   const int nvec = a.vocab / (bf16 ? 8 : 4);
@@ -570,7 +571,9 @@ cudaError_t token_logprobs_launch(const LogprobArgs& a, bool bf16, int sms, cuda
   // 512 threads a CTA where there are few CTAs and enough to do for them (one row
   // of 151,936: 9.0 us against 11.4 with 256 threads; 150 rows: 24.7 against 34.5;
   // 600 rows: 68.6 against 61.4).  With bf16 logits they pay only for a handful of
-  // rows (one: 9.1 against 11.2, 16: 17.7 against 14.4).
+  // rows (one: 9.1 against 11.2, 16: 17.7 against 14.4; 600 rows: 108 against 89, which
+  // is slower than fp32's 61 on twice the bytes: with alternatives bf16 takes 79
+  // registers, three CTAs an SM, and twice the candidates a load).
   const bool wide = nvec >= 1024 * cluster && (long long)a.rows * cluster <= (bf16 ? sms / 2 : 2 * sms);
   auto launch = [&](auto t, auto topk) {
     using T = decltype(t);

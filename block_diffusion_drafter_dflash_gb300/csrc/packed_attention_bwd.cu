@@ -31,12 +31,12 @@
 // that a key tile meets, or 2 GB of fp32 atomics (at the training shape below).
 //
 // Measured (512 blocks of 16 in 4,096 positions, 32 query and 8 kv heads of 128,
-// bf16): 865 us, of which the ranges take 46 (HBM, 5.5 TB/s), the layout 83 (HBM,
-// 6.9 TB/s), the gradients 685 and the shares' sum 11; 693 GFLOP of five products
-// at 0.80 PFLOP/s, the gradient kernel's seven at 1.42 PFLOP/s.  What bounds
+// bf16): 866 us, of which the ranges take 45 (HBM, 5.6 TB/s), the layout 87 (HBM,
+// 6.6 TB/s), the gradients 692 and the shares' sum 12; 693 GFLOP of five products
+// at 0.80 PFLOP/s, the gradient kernel's seven at 1.40 PFLOP/s.  What bounds
 // that kernel is the hand-over between tensor cores and softmax warps: a tile of
-// context keys takes about 3,000 cycles, 2,048 of them MMAs.  100 blocks of 10 in
-// 1,999 positions: 112 us; 12 blocks of 8 in 500: 23 us, four launches' latency.
+// context keys takes about 2,800 cycles, 2,050 of them MMAs.  100 blocks of 10 in
+// 1,999 positions: 111 us; 12 blocks of 8 in 500: 23 us, four launches' latency.
 //
 // In a CTA one thread loads tiles by TMA, one issues the MMAs, and sixteen warps
 // turn S and dP into P and dS.  The MMA thread alternates so that the tensor
@@ -674,6 +674,8 @@ __device__ __forceinline__ void put_pairs(uint32_t at, const uint32_t* h, const 
 // warp 16 loads, warp 17 issues the MMAs.
 constexpr int kSoftWarps = 16;
 constexpr int kParts = kSoftWarps / 4;             // warps of a lane quarter
+// 96 registers a thread, the most that five warps of one scheduler leave each other.
+// ptxas spills 52 bytes (bf16, heads of 128), 28 (of 64), 44 and 316 (fp32).
 constexpr int kGradThreads = 32 * (kSoftWarps + 2);
 
 // Two streams of tiles pass the two resident operands: the first feeds S and dK
