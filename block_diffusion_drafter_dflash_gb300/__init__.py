@@ -26,7 +26,10 @@ __all__ = ["DFlashError", "Model", "Cache", "lib", "dflash_model_create", "dflas
            "BlockPolicy", "dflash_packed_attention_workspace", "dflash_packed_block_attention",
            "dflash_packed_attention_status", "dflash_token_logprobs", "dflash_token_logprobs_backward",
            "dflash_clip_workspace", "dflash_clip_grad_norm", "dflash_packed_attention_backward_workspace",
-           "dflash_packed_block_attention_backward"]
+           "dflash_packed_block_attention_backward", "dflash_linear_cross_entropy_workspace",
+           "dflash_linear_cross_entropy", "dflash_linear_cross_entropy_backward_workspace",
+           "dflash_linear_cross_entropy_backward", "dflash_linear_cross_entropy_status", "dflash_embed_tokens",
+           "dflash_embed_tokens_backward_workspace", "dflash_embed_tokens_backward"]
 
 
 # The current stream's handle without a Stream object (microseconds a call).
@@ -529,6 +532,126 @@ def dflash_clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None,
         at, None if out is None else at + 8 * n, sizes.buffer_info()[0], types.buffer_info()[0], n, float(max_norm),
         _vector(norm, 1, torch.float32, norm, "norm"), *_workspace(workspace, norm), _stream_ptr(stream)),
         "dflash_clip_grad_norm")
+
+
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    code = _CLIP_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return code
+
+
+def _head_workspace(nbytes, rows: int, dim: int, vocab: int, dtype: torch.dtype) -> torch.Tensor:
+    if dtype not in _CLIP_DTYPES:
+        raise ValueError("hidden states and head are float32 or bfloat16")
+    n = int(nbytes(rows, dim, vocab, _CLIP_DTYPES[dtype]))
+    if n == 0:
+        raise ValueError("invalid cross-entropy shape")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def dflash_linear_cross_entropy_workspace(rows: int, dim: int, vocab: int, dtype: torch.dtype) -> torch.Tensor:
+    """Device scratch for dflash_linear_cross_entropy."""
+    return _head_workspace(lib().dflash_linear_cross_entropy_workspace_bytes, rows, dim, vocab, dtype)
+
+
+def dflash_linear_cross_entropy_backward_workspace(rows: int, dim: int, vocab: int, dtype: torch.dtype) -> torch.Tensor:
+    """Device scratch for dflash_linear_cross_entropy_backward (a piece of the logits' gradient, not all of it)."""
+    return _head_workspace(lib().dflash_linear_cross_entropy_backward_workspace_bytes, rows, dim, vocab, dtype)
+
+
+def _head_operands(hidden: torch.Tensor, weight: torch.Tensor):
+    """(rows, dim, vocab, elements between rows, dtype code) of hidden [..., D] against the head [V, D]."""
+    _on_current_device(hidden)
+    rows, D, stride = _rows_of(hidden, "hidden")
+    if weight.dim() != 2 or weight.shape[1] != D:
+        raise ValueError(f"the head must be [V, {D}]")
+    return rows, D, weight.shape[0], stride, _dtype_of(hidden, "hidden")
+
+
+def dflash_linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
+                                lse: torch.Tensor, workspace: torch.Tensor, temperature: float = 1.0,
+                                stream=None) -> None:
+    """Softmax cross-entropy of hidden [..., D] against the LM head weight [V, D]
+    (fp32 or bf16 both) for targets int32 [...], without storing the logits ->
+    loss and lse fp32 [...]; a target outside [0, V) gives 0 for both."""
+    rows, D, V, stride, dt = _head_operands(hidden, weight)
+    check(lib().dflash_linear_cross_entropy(
+        hidden.data_ptr(), dt, stride, _vector(weight, V * D, hidden.dtype, hidden, "weight"),
+        _vector(targets, rows, torch.int32, hidden, "targets"), rows, D, V, float(temperature),
+        _vector(loss, rows, torch.float32, hidden, "loss"), _vector(lse, rows, torch.float32, hidden, "lse"),
+        *_workspace(workspace, hidden), _stream_ptr(stream)), "dflash_linear_cross_entropy")
+
+
+def dflash_linear_cross_entropy_backward(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                                         lse: torch.Tensor, d_loss: torch.Tensor, d_hidden: Optional[torch.Tensor],
+                                         d_weight: Optional[torch.Tensor], workspace: torch.Tensor,
+                                         temperature: float = 1.0, stream=None) -> None:
+    """Gradients of sum(d_loss * loss): d_hidden [..., D] (which may be hidden
+    itself) and d_weight [V, D], in the operands' type; either may be None.  lse
+    is dflash_linear_cross_entropy's."""
+    rows, D, V, stride, dt = _head_operands(hidden, weight)
+    d_stride = D
+    if d_hidden is not None:
+        d_rows, d_D, d_stride = _rows_of(d_hidden, "d_hidden")
+        if d_rows != rows or d_D != D or d_hidden.dtype != hidden.dtype or d_hidden.device != hidden.device:
+            raise ValueError("d_hidden must have the hidden states' rows, type and device")
+    check(lib().dflash_linear_cross_entropy_backward(
+        hidden.data_ptr(), dt, stride, _vector(weight, V * D, hidden.dtype, hidden, "weight"),
+        _vector(targets, rows, torch.int32, hidden, "targets"), rows, D, V, float(temperature),
+        _vector(lse, rows, torch.float32, hidden, "lse"), _vector(d_loss, rows, torch.float32, hidden, "d_loss"),
+        None if d_hidden is None else d_hidden.data_ptr(), d_stride,
+        _vector(d_weight, V * D, hidden.dtype, hidden, "d_weight"), *_workspace(workspace, hidden),
+        _stream_ptr(stream)), "dflash_linear_cross_entropy_backward")
+
+
+def dflash_linear_cross_entropy_status(workspace: torch.Tensor, stream=None) -> int:
+    st = ctypes.c_int32(0)
+    check(lib().dflash_linear_cross_entropy_status(_ptr(workspace), _stream_ptr(stream), ctypes.byref(st)),
+          "dflash_linear_cross_entropy_status")
+    return st.value
+
+
+def _table(t: torch.Tensor, like: torch.Tensor, D: int, name: str):
+    """(address, rows) of a contiguous table [V, D] on the device of `like`."""
+    if t.dim() != 2 or t.shape[1] != D:
+        raise ValueError(f"{name} must be [V, {D}]")
+    return _vector(t, t.numel(), t.dtype, like, name), t.shape[0]
+
+
+def dflash_embed_tokens(table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+                        stream=None) -> None:
+    """out [..., D] = scale * table[tokens], table [V, D] and out fp32 or bf16 each,
+    tokens int32 [...]; a token outside [0, V) gives zeros."""
+    _on_current_device(out)
+    rows, D, stride = _rows_of(out, "out")
+    at, V = _table(table, out, D, "table")
+    check(lib().dflash_embed_tokens(at, _dtype_of(table, "table"), V, D, _vector(tokens, rows, torch.int32, out, "tokens"),
+                                    rows, float(scale), out.data_ptr(), _dtype_of(out, "out"), stride,
+                                    _stream_ptr(stream)), "dflash_embed_tokens")
+
+
+def dflash_embed_tokens_backward_workspace(n_tokens: int, dim: int, vocab: int) -> torch.Tensor:
+    """Device scratch for dflash_embed_tokens_backward."""
+    n = int(lib().dflash_embed_tokens_backward_workspace_bytes(n_tokens, dim, vocab))
+    if n == 0:
+        raise ValueError("invalid embedding shape")
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def dflash_embed_tokens_backward(d_out: torch.Tensor, tokens: torch.Tensor, d_table: torch.Tensor,
+                                 workspace: torch.Tensor, scale: float = 1.0, accumulate: bool = False,
+                                 stream=None) -> None:
+    """d_table [V, D] = scale * the sum of d_out's rows [..., D] over the tokens
+    int32 [...] that are each v (fp32 or bf16 each), or, with accumulate, added
+    to what d_table holds."""
+    _on_current_device(d_out)
+    rows, D, stride = _rows_of(d_out, "d_out")
+    at, V = _table(d_table, d_out, D, "d_table")
+    check(lib().dflash_embed_tokens_backward(
+        d_out.data_ptr(), _dtype_of(d_out, "d_out"), stride, _vector(tokens, rows, torch.int32, d_out, "tokens"), rows, V,
+        D, float(scale), at, _dtype_of(d_table, "d_table"), 1 if accumulate else 0, *_workspace(workspace, d_out),
+        _stream_ptr(stream)), "dflash_embed_tokens_backward")
 
 
 class BlockPolicy:

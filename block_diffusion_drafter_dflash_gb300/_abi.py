@@ -99,6 +99,19 @@ SIGNATURES = {
                                                c_ptr, c_ptr, c_ptr, c_ptr, ctypes.c_int64, c_ptr]),
     "dflash_clip_workspace_bytes": (c_size, []),
     "dflash_clip_grad_norm": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_i32, ctypes.c_float, c_ptr, c_ptr, c_size, c_ptr]),
+    "dflash_linear_cross_entropy_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32]),
+    "dflash_linear_cross_entropy_backward_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32]),
+    "dflash_linear_cross_entropy": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_ptr, c_i32, c_i32, c_i32,
+                                            ctypes.c_float, c_ptr, c_ptr, c_ptr, c_size, c_ptr]),
+    "dflash_linear_cross_entropy_backward": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_ptr, c_i32, c_i32, c_i32,
+                                                     ctypes.c_float, c_ptr, c_ptr, c_ptr, ctypes.c_int64, c_ptr, c_ptr,
+                                                     c_size, c_ptr]),
+    "dflash_linear_cross_entropy_status": (c_i32, [c_ptr, c_ptr, c_i32p]),
+    "dflash_embed_tokens": (c_i32, [c_ptr, c_i32, c_i32, c_i32, c_ptr, c_i32, ctypes.c_float, c_ptr, c_i32,
+                                    ctypes.c_int64, c_ptr]),
+    "dflash_embed_tokens_backward_workspace_bytes": (c_size, [c_i32, c_i32, c_i32]),
+    "dflash_embed_tokens_backward": (c_i32, [c_ptr, c_i32, ctypes.c_int64, c_ptr, c_i32, c_i32, c_i32, ctypes.c_float,
+                                             c_ptr, c_i32, c_i32, c_ptr, c_size, c_ptr]),
     "dflash_launch_count": (ctypes.c_uint64, []),
     "dflash_synthetic_target": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_i32, c_ptr, c_ptr, c_ptr, c_i32, c_i32, c_i32,
                                         c_ptr, c_ptr]),

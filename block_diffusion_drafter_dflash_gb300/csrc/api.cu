@@ -21,6 +21,8 @@
 #include "sampling.cuh"
 #include "logprobs.cuh"
 #include "grad_clip.cuh"
+#include "cross_entropy.cuh"
+#include "embed.cuh"
 #include "packed_attention.cuh"
 #include "packed_attention_bwd.cuh"
 
@@ -1633,6 +1635,242 @@ int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_ho
   } catch (const std::bad_alloc&) {
     return fail(DFLASH_ERR_INVALID_ARG, "out of host memory for %d tensors", n_tensors);
   }
+  return DFLASH_OK;
+}
+
+namespace {
+// Bytes that rows of `len` bytes, `stride` bytes apart, span from their start.
+struct Span {
+  uintptr_t at, end, stride, len;
+  Span(const void* p, long long rows, long long stride_, long long len_)
+      : at(reinterpret_cast<uintptr_t>(p)), end(at + (rows ? (rows - 1) * stride_ + len_ : 0)), stride(stride_), len(len_) {}
+};
+bool overlap(const Span& a, const Span& b) {
+  if (a.at >= b.end || b.at >= a.end) return false;
+  if (a.stride != b.stride || a.stride < a.len + b.len) return true;
+  // rows of one step: each may lie between the other's
+  const uintptr_t behind = b.at >= a.at ? (b.at - a.at) % a.stride : (a.stride - (a.at - b.at) % a.stride) % a.stride;
+  return behind < a.len || a.stride - behind < b.len;
+}
+
+// A once-per-device set-up: `what` returns its error; bit `bit` of `done[device]` says that it has run.
+int32_t once_per_device(std::atomic<unsigned>* done, unsigned bit, const char* name, cudaError_t (*what)()) {
+  int dev = 0;
+  DF_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev < 0 || dev >= 64 || !(done[dev].load() & bit)) {
+    DF_CUDA(what(), name);
+    if (dev >= 0 && dev < 64) done[dev].fetch_or(bit);
+  }
+  return DFLASH_OK;
+}
+
+int32_t ce_shape(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype) {
+  if (rows < 0) return fail(DFLASH_ERR_INVALID_ARG, "rows %d < 0", rows);
+  if (rows > (1 << 20)) return fail(DFLASH_ERR_SHAPE, "%d rows > 2^20", rows);
+  if (dim <= 0 || dim % 8 || dim > 65536) return fail(DFLASH_ERR_SHAPE, "dim %d must be a positive multiple of 8, at most 65536", dim);
+  if (vocab <= 0 || vocab > (1 << 24)) return fail(DFLASH_ERR_SHAPE, "vocab %d outside [1, 2^24]", vocab);
+  if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  return DFLASH_OK;
+}
+// What the loss and its gradient check alike.
+int32_t ce_check(const void* hidden, int64_t row_stride, const void* weight, const int32_t* targets, int32_t rows, int32_t dim,
+                 int32_t vocab, int32_t dtype, float temperature, const void* workspace) {
+  int32_t rc = ce_shape(rows, dim, vocab, dtype);
+  if (rc) return rc;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(logprob_scale2(temperature)))
+    return fail(DFLASH_ERR_INVALID_ARG, "temperature must be positive and finite, and so log2(e) / temperature");
+  if (!weight || (rows > 0 && (!hidden || !targets))) return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (rows > 1 && row_stride < dim) return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld < dim %d", (long long)row_stride, dim);
+  if (reinterpret_cast<uintptr_t>(hidden) % (dtype == DFLASH_DTYPE_F32 ? 4 : 2))
+    return fail(DFLASH_ERR_INVALID_ARG, "hidden states are not aligned to their type");
+  if (reinterpret_cast<uintptr_t>(weight) % 16) return fail(DFLASH_ERR_INVALID_ARG, "the head must be 16-byte aligned");
+  if (!workspace) return fail(DFLASH_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(DFLASH_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return DFLASH_OK;
+}
+std::atomic<unsigned> g_ce_prepared[64], g_embed_prepared[64];
+}  // namespace
+
+size_t dflash_linear_cross_entropy_workspace_bytes(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype) {
+  if (ce_shape(rows, dim, vocab, dtype) != DFLASH_OK) return 0;
+  const int sms = current_sms();
+  return sms > 0 ? ce_plan(nullptr, std::max(rows, 1), dim, vocab, dtype == DFLASH_DTYPE_F32, false, false, sms).bytes : 0;
+}
+
+size_t dflash_linear_cross_entropy_backward_workspace_bytes(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype) {
+  if (ce_shape(rows, dim, vocab, dtype) != DFLASH_OK) return 0;
+  const int sms = current_sms();
+  return sms > 0 ? ce_plan(nullptr, std::max(rows, 1), dim, vocab, dtype == DFLASH_DTYPE_F32, true, true, sms).bytes : 0;
+}
+
+int32_t dflash_linear_cross_entropy(const void* hidden, int32_t dtype, int64_t row_stride, const void* weight,
+                                    const int32_t* targets, int32_t rows, int32_t dim, int32_t vocab, float temperature,
+                                    float* loss, float* lse, void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  int32_t rc = ce_check(hidden, row_stride, weight, targets, rows, dim, vocab, dtype, temperature, workspace);
+  if (rc) return rc;
+  if (rows > 0 && (!loss || !lse)) return fail(DFLASH_ERR_INVALID_ARG, "loss or lse is NULL");
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  const bool f32 = dtype == DFLASH_DTYPE_F32;
+  const CePlan pl = ce_plan(workspace, std::max(rows, 1), dim, vocab, f32, false, false, sms);
+  if (ws_bytes < pl.bytes) return fail(DFLASH_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, pl.bytes);
+  if (rows == 0) {
+    DF_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream), "status reset");
+    return DFLASH_OK;
+  }
+  if ((rc = once_per_device(g_ce_prepared, f32 ? 2u : 1u, "cross-entropy set-up", f32 ? ce_prepare_f32 : ce_prepare_bf16))) return rc;
+  CeTensors t{};
+  t.hidden = hidden;
+  t.row_stride = row_stride;
+  t.weight = weight;
+  t.targets = targets;
+  t.temperature = temperature;
+  t.loss = loss;
+  t.lse = lse;
+  int launches = 0;
+  DF_CUDA(ce_forward(pl, t, sms, &launches, (cudaStream_t)stream), "cross-entropy");
+  g_launch_count += launches;
+  return DFLASH_OK;
+}
+
+int32_t dflash_linear_cross_entropy_backward(const void* hidden, int32_t dtype, int64_t row_stride, const void* weight,
+                                             const int32_t* targets, int32_t rows, int32_t dim, int32_t vocab,
+                                             float temperature, const float* lse, const float* d_loss, void* d_hidden,
+                                             int64_t d_row_stride, void* d_weight, void* workspace, size_t ws_bytes,
+                                             dflash_stream_t stream) {
+  int32_t rc = ce_check(hidden, row_stride, weight, targets, rows, dim, vocab, dtype, temperature, workspace);
+  if (rc) return rc;
+  if (!d_hidden && !d_weight) return fail(DFLASH_ERR_INVALID_ARG, "d_hidden or d_weight is needed");
+  if (rows > 0 && (!lse || !d_loss)) return fail(DFLASH_ERR_INVALID_ARG, "lse or d_loss is NULL");
+  const bool f32 = dtype == DFLASH_DTYPE_F32;
+  const long long es = f32 ? 4 : 2;
+  if (d_hidden && rows > 1 && d_row_stride < dim)
+    return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld of the gradient < dim %d", (long long)d_row_stride, dim);
+  if (reinterpret_cast<uintptr_t>(d_hidden) % es) return fail(DFLASH_ERR_INVALID_ARG, "d_hidden is not aligned to its type");
+  if (reinterpret_cast<uintptr_t>(d_weight) % 16) return fail(DFLASH_ERR_INVALID_ARG, "d_weight must be 16-byte aligned");
+  // d_hidden may take the hidden states' place (they are packed before it is written); nothing else may overlap
+  const Span h(hidden, rows, row_stride * es, dim * es), w(weight, vocab, dim * es, dim * es);
+  const Span dh(d_hidden, d_hidden ? rows : 0, d_row_stride * es, dim * es), dw(d_weight, d_weight ? vocab : 0, dim * es, dim * es);
+  const bool same = d_hidden == hidden && (rows <= 1 || row_stride == d_row_stride);
+  if ((!same && overlap(dh, h)) || overlap(dh, w) || overlap(dw, h) || overlap(dw, w) || overlap(dh, dw))
+    return fail(DFLASH_ERR_INVALID_ARG, "a gradient overlaps an operand or the other gradient");
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  const CePlan pl = ce_plan(workspace, std::max(rows, 1), dim, vocab, f32, true, true, sms);
+  if (ws_bytes < pl.bytes) return fail(DFLASH_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, pl.bytes);
+  if (rows == 0) {
+    DF_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int32_t), (cudaStream_t)stream), "status reset");
+    if (d_weight) DF_CUDA(cudaMemsetAsync(d_weight, 0, (size_t)vocab * dim * es, (cudaStream_t)stream), "zero gradient");
+    return DFLASH_OK;
+  }
+  if ((rc = once_per_device(g_ce_prepared, f32 ? 2u : 1u, "cross-entropy set-up", f32 ? ce_prepare_f32 : ce_prepare_bf16))) return rc;
+  CeTensors t{};
+  t.hidden = hidden;
+  t.row_stride = row_stride;
+  t.weight = weight;
+  t.targets = targets;
+  t.temperature = temperature;
+  t.lse_in = lse;
+  t.d_loss = d_loss;
+  t.d_hidden = d_hidden;
+  t.d_row_stride = d_row_stride;
+  t.d_weight = d_weight;
+  int launches = 0;
+  DF_CUDA(ce_backward(pl, t, sms, &launches, (cudaStream_t)stream), "cross-entropy gradient");
+  g_launch_count += launches;
+  return DFLASH_OK;
+}
+
+int32_t dflash_linear_cross_entropy_status(const void* workspace, dflash_stream_t stream, int32_t* status_host) {
+  return dflash_packed_attention_status(workspace, stream, status_host);
+}
+
+namespace {
+int32_t embed_check(int32_t n, int32_t dim, int32_t vocab, int32_t table_dtype, int32_t row_dtype, float scale) {
+  if (n < 0) return fail(DFLASH_ERR_INVALID_ARG, "%d tokens < 0", n);
+  if (n > (1 << 24)) return fail(DFLASH_ERR_SHAPE, "%d tokens > 2^24", n);
+  if (dim <= 0 || dim > 65536) return fail(DFLASH_ERR_SHAPE, "dim %d outside [1, 65536]", dim);
+  if (vocab <= 0 || vocab > (1 << 24)) return fail(DFLASH_ERR_SHAPE, "vocab %d outside [1, 2^24]", vocab);
+  for (int32_t d : {table_dtype, row_dtype})
+    if (d != DFLASH_DTYPE_F32 && d != DFLASH_DTYPE_BF16) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", d);
+  if (!std::isfinite(scale)) return fail(DFLASH_ERR_INVALID_ARG, "scale must be finite");
+  return DFLASH_OK;
+}
+// Rows of tokens against the table: strides, alignment, overlap.
+int32_t embed_rows(const void* rows, int32_t row_dtype, int64_t stride, int32_t n, const void* table, int32_t table_dtype,
+                   int32_t dim, int32_t vocab, const int32_t* tokens) {
+  const long long re = row_dtype == DFLASH_DTYPE_F32 ? 4 : 2, te = table_dtype == DFLASH_DTYPE_F32 ? 4 : 2;
+  if (n > 1 && stride < dim) return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld < dim %d", (long long)stride, dim);
+  if (reinterpret_cast<uintptr_t>(rows) % re || reinterpret_cast<uintptr_t>(table) % te)
+    return fail(DFLASH_ERR_INVALID_ARG, "a tensor is not aligned to its type");
+  const Span r(rows, n, stride * re, dim * re), t(table, vocab, dim * te, dim * te), k(tokens, n, 4, 4);
+  if (overlap(r, t) || overlap(r, k) || overlap(t, k)) return fail(DFLASH_ERR_INVALID_ARG, "the tensors overlap");
+  return DFLASH_OK;
+}
+}  // namespace
+
+int32_t dflash_embed_tokens(const void* table, int32_t table_dtype, int32_t vocab, int32_t dim, const int32_t* tokens,
+                            int32_t n_tokens, float scale, void* out, int32_t out_dtype, int64_t out_stride,
+                            dflash_stream_t stream) {
+  int32_t rc = embed_check(n_tokens, dim, vocab, table_dtype, out_dtype, scale);
+  if (rc) return rc;
+  if (n_tokens == 0) return DFLASH_OK;
+  if (!table || !tokens || !out) return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  if ((rc = embed_rows(out, out_dtype, out_stride, n_tokens, table, table_dtype, dim, vocab, tokens))) return rc;
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  EmbedArgs a{};
+  a.table = table;
+  a.tokens = tokens;
+  a.n = n_tokens;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.scale = scale;
+  a.out = out;
+  a.out_stride = n_tokens > 1 ? out_stride : dim;
+  DF_CUDA(embed_launch(a, table_dtype == DFLASH_DTYPE_F32, out_dtype == DFLASH_DTYPE_F32, sms, (cudaStream_t)stream), "embedding");
+  g_launch_count += 1;
+  return DFLASH_OK;
+}
+
+size_t dflash_embed_tokens_backward_workspace_bytes(int32_t n_tokens, int32_t dim, int32_t vocab) {
+  if (embed_check(n_tokens, dim, vocab, DFLASH_DTYPE_F32, DFLASH_DTYPE_F32, 1.f) != DFLASH_OK) return 0;
+  return embed_bwd_plan(nullptr, n_tokens, dim, vocab).bytes;
+}
+
+int32_t dflash_embed_tokens_backward(const void* d_out, int32_t d_out_dtype, int64_t d_out_stride, const int32_t* tokens,
+                                     int32_t n_tokens, int32_t vocab, int32_t dim, float scale, void* d_table,
+                                     int32_t table_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                     dflash_stream_t stream) {
+  int32_t rc = embed_check(n_tokens, dim, vocab, table_dtype, d_out_dtype, scale);
+  if (rc) return rc;
+  if (accumulate != 0 && accumulate != 1) return fail(DFLASH_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
+  if (!d_table || !workspace || (n_tokens > 0 && (!d_out || !tokens))) return fail(DFLASH_ERR_INVALID_ARG, "a device pointer is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(DFLASH_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if ((rc = embed_rows(d_out, d_out_dtype, d_out_stride, n_tokens, d_table, table_dtype, dim, vocab, tokens))) return rc;
+  const EmbedBwdPlan pl = embed_bwd_plan(workspace, n_tokens, dim, vocab);
+  if (ws_bytes < pl.bytes) return fail(DFLASH_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, pl.bytes);
+  const int sms = current_sms();
+  if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
+  if (n_tokens == 0) {
+    if (!accumulate)
+      DF_CUDA(cudaMemsetAsync(d_table, 0, (size_t)vocab * dim * (table_dtype == DFLASH_DTYPE_F32 ? 4 : 2), (cudaStream_t)stream),
+              "zero gradient");
+    return DFLASH_OK;
+  }
+  if ((rc = once_per_device(g_embed_prepared, 1u, "embedding gradient set-up", embed_backward_prepare))) return rc;
+  EmbedBwdArgs a{};
+  a.d_out = d_out;
+  a.stride = n_tokens > 1 ? d_out_stride : dim;
+  a.tokens = tokens;
+  a.scale = scale;
+  a.d_table = d_table;
+  a.accumulate = accumulate;
+  int launches = 0;
+  DF_CUDA(embed_backward_launch(pl, a, d_out_dtype == DFLASH_DTYPE_F32, table_dtype == DFLASH_DTYPE_F32, sms, &launches,
+                                (cudaStream_t)stream),
+          "embedding gradient");
+  g_launch_count += launches;
   return DFLASH_OK;
 }
 

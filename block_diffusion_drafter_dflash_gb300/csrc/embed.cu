@@ -1,0 +1,433 @@
+// Token embedding with a factor, and its gradient (the drafter's input: an anchor
+// token and block_size - 1 mask tokens a block, paper section 4.2):
+//
+//   out_i = scale E[t_i]            dE[v] (+)= scale sum_{i: t_i = v} d_out_i
+//
+// The lookup is bound by HBM: rows out, and each distinct row of the table once.
+//
+// The gradient.  In a block drafter's training one token, the mask, collects nearly
+// all rows, so rows of the table are no unit of work.  One cluster sorts the
+// (token, position) pairs by token, positions ascending (a stable radix sort, two
+// passes for vocabularies up to 2^18), and marks the tokens that occur.  Then every
+// chunk of kEmbedChunk sorted tokens is summed by CTAs of its own: tokens that lie
+// inside the chunk go straight to the table's gradient; the sums of a first or last
+// token that goes on in another chunk go to memory, and a last kernel adds them in
+// order.  Rows without a token are zeroed beside the sums.  No float atomics: the
+// same call gives the same bits.  Sums are fp32, at most kEmbedChunk terms, and the
+// chunks' sums are added with their rounding errors carried along.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "embed.cuh"
+
+namespace dflash {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kChunk = kEmbedChunk;
+
+// ---------------------------------------------------------------- rows in vectors of W values
+template <typename T, int W>
+struct alignas(sizeof(T) * W) Vec {
+  T v[W];
+};
+// Accesses of at most 16 bytes.
+template <int W, typename T>
+__device__ __forceinline__ void load_row(const T* p, float* v) {
+  constexpr int P = W * sizeof(T) > 16 ? 16 / sizeof(T) : W;
+#pragma unroll
+  for (int k = 0; k < W; k += P) {
+    const Vec<T, P> x = *reinterpret_cast<const Vec<T, P>*>(p + k);
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[k + j] = to_f32<T>(x.v[j]);
+  }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_row(T* p, const float* v) {
+  constexpr int P = W * sizeof(T) > 16 ? 16 / sizeof(T) : W;
+#pragma unroll
+  for (int k = 0; k < W; k += P) {
+    Vec<T, P> x;
+#pragma unroll
+    for (int j = 0; j < P; ++j) x.v[j] = from_f32<T>(v[k + j]);
+    *reinterpret_cast<Vec<T, P>*>(p + k) = x;
+  }
+}
+// The widest vector (8, 4, 2 or 1 values) that both sides' rows allow: rows start at
+// multiples of it, and accesses of up to 16 bytes are aligned.
+int width_of(const void* a, int64_t a_stride, int a_size, const void* b, int64_t b_stride, int b_size, int dim) {
+  for (int w = 8; w > 1; w /= 2) {
+    auto fits = [&](const void* p, int64_t stride, int size) {
+      const uintptr_t bytes = std::min(16, w * size);
+      return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (uintptr_t)(stride * size) % bytes == 0;
+    };
+    if (dim % w == 0 && fits(a, a_stride, a_size) && fits(b, b_stride, b_size)) return w;
+  }
+  return 1;
+}
+
+// ---------------------------------------------------------------- lookup
+template <typename TT, typename TO, int W>
+__global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
+  griddep_wait();
+  griddep_trigger();
+  const unsigned groups = a.dim / W;
+  const long long n = (long long)a.n * groups, step = (long long)gridDim.x * 256;
+  const TT* table = static_cast<const TT*>(a.table);
+  TO* out = static_cast<TO*>(a.out);
+  constexpr int U = 4;
+  for (long long i0 = blockIdx.x * 256LL + threadIdx.x; i0 < n; i0 += step * U) {
+    float v[U][W];
+    TO* to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long i = i0 + u * step;
+      to[u] = nullptr;
+      if (i < n) {
+        const int r = n < (1LL << 32) ? (unsigned)i / groups : (int)(i / groups);
+        const int c = (int)(i - (long long)r * groups) * W;
+        const unsigned t = a.tokens[r];
+        to[u] = out + r * a.out_stride + c;
+        if (t < (unsigned)a.vocab) {
+          load_row<W>(table + (size_t)t * a.dim + c, v[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < W; ++j) v[u][j] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (to[u]) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[u][j] *= a.scale;
+        store_row<W>(to[u], v[u]);
+      }
+  }
+}
+
+// ---------------------------------------------------------------- sort
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
+constexpr int kMaxCluster = 8;
+constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + 2);
+
+// One cluster.  Each warp owns a contiguous share of the pairs.  A pass counts its
+// digits, turns the counts into places (digits first, then CTAs, then warps, so equal
+// digits keep their order) and moves the pairs.  Tokens outside the vocabulary sort
+// behind all others.
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPlan pl, const int32_t* tokens, int passes) {
+  griddep_wait();
+  griddep_trigger();
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ uint32_t sh[];
+  uint32_t* count = sh;                          // [warps][bins]
+  uint32_t* total = sh + kBins * kSortWarps;     // [bins] of this CTA
+  uint32_t* place = total + kBins;               // [bins] first place of the CTA's pairs
+  __shared__ uint32_t s_scan[kBins / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+  const long long all_warps = (long long)ctas * kSortWarps, me = (long long)cta * kSortWarps + warp;
+  const int share = (int)(((pl.n + all_warps - 1) / all_warps + 31) / 32 * 32);
+  const int beg = (int)min((long long)pl.n, me * share), end = (int)min((long long)pl.n, (me + 1) * share);
+  const int words = (pl.vocab + 31) / 32;
+  for (int i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) pl.seen[i] = 0;
+  if (cta == 0 && tid == 0) *pl.kept = 0;
+  for (int pass = 0; pass < passes; ++pass) {
+    const bool last_odd = (passes - pass) & 1;   // the last pass writes `order`
+    const uint2* src = last_odd ? pl.spare : pl.order;
+    uint2* dst = last_odd ? pl.order : pl.spare;
+    const int shift = pass * kDigitBits;
+    auto pair_at = [&](int i) {
+      if (pass) return src[i];
+      const unsigned t = tokens[i];
+      return make_uint2(min(t, (unsigned)pl.vocab), i);
+    };
+    for (int i = tid; i < kBins * kSortWarps; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    uint32_t* mine = count + warp * kBins;
+    for (int i = beg; i < end; i += 32) {
+      const bool in = i + lane < end;
+      const unsigned d = in ? pair_at(i + lane).x >> shift & (kBins - 1) : kBins;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (tid < kBins) {
+      uint32_t sum = 0;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = count[w * kBins + tid];
+        count[w * kBins + tid] = sum;
+        sum += c;
+      }
+      total[tid] = sum;
+    }
+    cluster.sync();
+    uint32_t before = 0, all = 0, run = 0;
+    if (tid < kBins) {
+      for (int c = 0; c < ctas; ++c) {
+        const uint32_t x = cluster.map_shared_rank(total, c)[tid];
+        before += c < cta ? x : 0;
+        all += x;
+      }
+      run = all;   // inclusive scan over the digits
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += x;
+      }
+      if (lane == 31) s_scan[warp] = run;
+    }
+    __syncthreads();
+    if (tid < kBins) {
+      for (int w = 0; w < warp; ++w) run += s_scan[w];
+      place[tid] = run - all + before;
+    }
+    __syncthreads();
+    for (int i = beg; i < end; i += 32) {
+      const bool in = i + lane < end;
+      const uint2 p = in ? pair_at(i + lane) : make_uint2(0, 0);
+      const unsigned d = in ? p.x >> shift & (kBins - 1) : kBins;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      if (in) dst[place[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p;
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    cluster.sync();   // the pairs are where the next pass reads them, and `total` may change
+  }
+  const uint2* got = pl.order;
+  for (int i = beg + lane; i < end; i += 32) {
+    const unsigned t = got[i].x;
+    if (t < (unsigned)pl.vocab) {
+      if (i == 0 || got[i - 1].x != t) atomicOr(&pl.seen[t >> 5], 1u << (t & 31));
+      if (i == pl.n - 1 || got[i + 1].x >= (unsigned)pl.vocab) *pl.kept = i + 1;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sums
+// A chunk's (or a whole token's) sum into the table's gradient.
+template <typename TT, int W>
+__device__ __forceinline__ void put_sum(TT* p, const float* sum, float scale, int accumulate) {
+  float v[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) v[j] = sum[j] * scale;
+  if (accumulate) {
+    float o[W];
+    load_row<W>(p, o);
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = fmaf(sum[j], scale, o[j]);
+  }
+  store_row<W>(p, v);
+}
+
+// First `chunks` blocks of the grid's x: a chunk's sums over blockDim.x * W columns.
+// The others, unless the gradient is added to what is there: rows without a token.
+template <typename TO, typename TT, int W>
+__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
+  griddep_wait();
+  griddep_trigger();
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
+  TT* table = static_cast<TT*>(a.d_table);
+  if ((int)blockIdx.x >= pl.chunks) {
+    if (c >= pl.dim) return;
+    const float zero[W] = {};
+    for (int v = blockIdx.x - pl.chunks; v < pl.vocab; v += gridDim.x - pl.chunks)
+      if (!(pl.seen[v >> 5] >> (v & 31) & 1)) store_row<W>(table + (size_t)v * pl.dim + c, zero);
+    return;
+  }
+  __shared__ uint2 s_pair[kChunk];
+  const uint2* order = pl.order;
+  const int kept = *pl.kept, i0 = blockIdx.x * kChunk, n = min(kChunk, kept - i0);
+  if (n <= 0) return;
+  if (threadIdx.x < n) s_pair[threadIdx.x] = order[i0 + threadIdx.x];
+  __syncthreads();
+  if (c >= pl.dim) return;
+  const bool from_before = i0 > 0 && order[i0 - 1].x == s_pair[0].x;
+  const bool goes_on = i0 + n < kept && order[i0 + n].x == s_pair[n - 1].x;
+  const TO* d_out = static_cast<const TO*>(a.d_out);
+  float sum[W] = {};
+  bool first = true;
+  constexpr int U = 8;
+  for (int i = 0; i < n; i += U) {
+    float v[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u < n) load_row<W>(d_out + (int64_t)s_pair[i + u].y * a.stride + c, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = i + u;
+      if (k < n) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum[j] += v[u][j];
+        const bool last = k == n - 1;
+        if (last || s_pair[k + 1].x != s_pair[k].x) {
+          const bool head = first && from_before, tail = last && goes_on;
+          if (head || tail)   // (a chunk of one token alone has one sum, as its first)
+            store_row<W>(pl.part + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * pl.dim + c, sum);
+          else
+            put_sum<TT, W>(table + (size_t)s_pair[k].x * pl.dim + c, sum, a.scale, a.accumulate);
+          first = false;
+#pragma unroll
+          for (int j = 0; j < W; ++j) sum[j] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// A token that begins in this chunk and goes on: its chunks' sums in order, with
+// what each addition rounds off summed beside them.
+template <typename TT, int W>
+__global__ void __launch_bounds__(256) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
+  griddep_wait();
+  griddep_trigger();
+  const uint2* order = pl.order;
+  const int kept = *pl.kept, b = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
+  const int next = (b + 1) * kChunk;   // the chunk's end; a token that goes on fills it
+  if (next >= kept || c >= pl.dim) return;
+  const unsigned t = order[next - 1].x;
+  if (order[next].x != t) return;
+  if (b > 0 && order[b * kChunk - 1].x == t) return;   // begins in an earlier chunk
+  // the last chunk that has the token: the one of the last pair up to it
+  int lo = next, hi = kept;   // order[lo].x == t; order[hi].x > t or the end
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (order[mid].x == t) lo = mid; else hi = mid;
+  }
+  const int last = lo / kChunk;
+  float sum[W], err[W] = {};
+  // (a token that fills its first chunk from the start has its sum in the chunk's last place all the same)
+  load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, sum);
+  constexpr int U = 8;
+  for (int k = b + 1; k <= last; k += U) {
+    float v[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u <= last) load_row<W>(pl.part + (size_t)(k + u) * 2 * pl.dim + c, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u <= last) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const float s = sum[j] + v[u][j], x = s - sum[j];
+          err[j] += (sum[j] - (s - x)) + (v[u][j] - x);
+          sum[j] = s;
+        }
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) sum[j] += isfinite(err[j]) ? err[j] : 0.f;
+  put_sum<TT, W>(static_cast<TT*>(a.d_table) + (size_t)t * pl.dim + c, sum, a.scale, a.accumulate);
+}
+
+// ---------------------------------------------------------------- host side
+template <typename TT, typename TO, int W>
+cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
+  const long long groups = (long long)a.n * (a.dim / W);
+  const unsigned grid = (unsigned)std::min<long long>((groups + 255) / 256, (long long)sms * 16);
+  return launch_pdl(embed_kernel<TT, TO, W>, dim3(grid), dim3(256), 0, s, a);
+}
+template <typename TT, typename TO>
+cudaError_t lookup_w(const EmbedArgs& a, int sms, cudaStream_t s) {
+  switch (width_of(a.table, a.dim, sizeof(TT), a.out, a.out_stride, sizeof(TO), a.dim)) {
+    case 8: return lookup<TT, TO, 8>(a, sms, s);
+    case 4: return lookup<TT, TO, 4>(a, sms, s);
+    case 2: return lookup<TT, TO, 2>(a, sms, s);
+    default: return lookup<TT, TO, 1>(a, sms, s);
+  }
+}
+
+int passes_of(int vocab) {
+  int bits = 0;
+  while ((long long)vocab >> bits) ++bits;   // tokens and the one place behind them
+  return (bits + kDigitBits - 1) / kDigitBits;
+}
+
+template <typename TO, typename TT, int W>
+cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
+  const int groups = pl.dim / W, threads = std::min(256, (groups + 31) / 32 * 32), tiles = (groups + threads - 1) / threads;
+  // rows to zero: enough CTAs beside the chunks' to fill the SMs a few times
+  const int zero = a.accumulate ? 0 : (int)std::min<long long>(pl.vocab, std::max(1, sms * 16 * (256 / threads) / tiles));
+  cudaError_t e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks + zero, tiles), dim3(threads), 0, s, pl, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (pl.chunks < 2) return cudaSuccess;   // no token goes on in another chunk
+  ++*launches;
+  return launch_pdl(embed_join_kernel<TT, W>, dim3(pl.chunks - 1, tiles), dim3(threads), 0, s, pl, a);
+}
+template <typename TO, typename TT>
+cudaError_t sums_w(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
+  switch (width_of(a.d_out, a.stride, sizeof(TO), a.d_table, pl.dim, sizeof(TT), pl.dim)) {
+    case 8: return sums<TO, TT, 8>(pl, a, sms, launches, s);
+    case 4: return sums<TO, TT, 4>(pl, a, sms, launches, s);
+    case 2: return sums<TO, TT, 2>(pl, a, sms, launches, s);
+    default: return sums<TO, TT, 1>(pl, a, sms, launches, s);
+  }
+}
+
+}  // namespace
+
+EmbedBwdPlan embed_bwd_plan(void* ws, int n, int dim, int vocab) {
+  EmbedBwdPlan pl{};
+  pl.n = n;
+  pl.vocab = vocab;
+  pl.dim = dim;
+  pl.chunks = (n + kChunk - 1) / kChunk;
+  char* p = static_cast<char*>(ws);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* r = p ? p + off : nullptr;
+    off += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  pl.kept = reinterpret_cast<int32_t*>(take(256));
+  pl.order = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
+  pl.spare = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
+  pl.seen = reinterpret_cast<uint32_t*>(take(4 * (((size_t)vocab + 31) / 32)));
+  pl.part = reinterpret_cast<float*>(take(sizeof(float) * 2 * (size_t)pl.chunks * dim));
+  pl.bytes = off;
+  return pl;
+}
+
+cudaError_t embed_backward_prepare() {
+  return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortBytes);
+}
+
+cudaError_t embed_launch(const EmbedArgs& a, bool table_f32, bool out_f32, int sms, cudaStream_t s) {
+  if (table_f32) return out_f32 ? lookup_w<float, float>(a, sms, s) : lookup_w<float, __nv_bfloat16>(a, sms, s);
+  return out_f32 ? lookup_w<__nv_bfloat16, float>(a, sms, s) : lookup_w<__nv_bfloat16, __nv_bfloat16>(a, sms, s);
+}
+
+cudaError_t embed_backward_launch(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, bool out_f32, bool table_f32, int sms,
+                                  int* launches, cudaStream_t s) {
+  *launches = 0;
+  int ctas = 1;
+  while (ctas < kMaxCluster && ctas * 4096 < pl.n) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, a.tokens, passes_of(pl.vocab));
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  if (out_f32) return table_f32 ? sums_w<float, float>(pl, a, sms, launches, s) : sums_w<float, __nv_bfloat16>(pl, a, sms, launches, s);
+  return table_f32 ? sums_w<__nv_bfloat16, float>(pl, a, sms, launches, s)
+                   : sums_w<__nv_bfloat16, __nv_bfloat16>(pl, a, sms, launches, s);
+}
+
+}  // namespace dflash

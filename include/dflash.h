@@ -506,6 +506,95 @@ int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_ho
                               const int32_t* dtype_host, int32_t n_tensors, float max_norm, float* norm_dev,
                               void* workspace, size_t workspace_bytes, dflash_stream_t stream);
 
+/* --- softmax cross-entropy at the LM head, without the logits ------------------
+ * The loss of a drafter's training (paper §4.2, eq. 1) from the final hidden
+ * states on: the logits of 8,192 rows and 151,936 tokens would be 5 GB, their
+ * gradient as much again.  The vocabulary is taken in pieces; what is stored is
+ * a pair of numbers per row and 128 columns.  For every row r with a target t
+ * inside [0, vocab), z = hidden weight^T / T:
+ *   lse[r] = ln sum_v e^(z_v)      loss[r] = lse[r] - z_t
+ * A row whose target lies outside (padding, an anchor: -1) is ignored: loss
+ * and lse 0, no work, and what its hidden state holds reaches nothing.
+ *   hidden_dev  [rows][dim] in `dtype`, rows row_stride (>= dim) elements
+ *               apart, any alignment of the type
+ *   weight_dev  [vocab][dim] in `dtype`, contiguous, 16-byte aligned
+ *   targets_dev int32 [rows];  loss_dev, lse_dev fp32 [rows]
+ *   workspace   >= dflash_linear_cross_entropy_workspace_bytes(...) bytes,
+ *               256-byte aligned; its first int32 is the call's status word (0
+ *               or DFLASH_ERR_TIMEOUT), read with
+ *               dflash_linear_cross_entropy_status
+ * Precision.  bf16 tensors: exact products, fp32 sums.  fp32 tensors: products
+ * of all 24 bits (three bf16 planes each, six products), fp32 sums.  Sums of the
+ * tensor cores, which truncate, span at most 512 of the dim.
+ * A NaN or an infinity in a row's hidden state makes that row's results NaN, in
+ * the head all rows'.  rows <= 2^20; dim a multiple of 8, <= 65536; vocab in
+ * [1, 2^24]; 0 < T < inf and log2(e) / T < inf; rows = 0 launches nothing. */
+size_t dflash_linear_cross_entropy_workspace_bytes(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype);
+int32_t dflash_linear_cross_entropy(const void* hidden_dev, int32_t dtype, int64_t row_stride, const void* weight_dev,
+                                    const int32_t* targets_dev, int32_t rows, int32_t dim, int32_t vocab,
+                                    float temperature, float* loss_dev, float* lse_dev, void* workspace,
+                                    size_t workspace_bytes, dflash_stream_t stream);
+
+/* Gradients of sum_r d_loss[r] loss[r], from lse as the forward gave it for the
+ * same operands and T.  With G = d_loss / T (e^(z - lse) - 1[v = t]), zero in
+ * ignored rows:
+ *   d_hidden = G weight        d_weight = G^T hidden
+ * The logits are computed again, a piece of the vocabulary at a time.
+ *   d_loss_dev    fp32 [rows] (the position weights of eq. 1 over their sum)
+ *   d_hidden_dev  [rows][dim] in `dtype`, rows d_row_stride apart, every element
+ *                 written; may be the hidden states themselves (the same rows);
+ *                 NULL: not wanted
+ *   d_weight_dev  [vocab][dim] in `dtype`, contiguous, 16-byte aligned, every
+ *                 element written; NULL where the head is frozen.  Not both NULL
+ *   workspace     >= dflash_linear_cross_entropy_backward_workspace_bytes(...)
+ * The gradients overlap neither each other nor an operand in any other way.
+ * Precision: as the forward; G of bf16 tensors is rounded to one bf16 before its
+ * products, G of fp32 tensors enters with all 24 bits.  Sums are added in a
+ * fixed order: the same call gives the same bits on the same device.  rows = 0
+ * zeroes d_weight. */
+size_t dflash_linear_cross_entropy_backward_workspace_bytes(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype);
+int32_t dflash_linear_cross_entropy_backward(const void* hidden_dev, int32_t dtype, int64_t row_stride,
+                                             const void* weight_dev, const int32_t* targets_dev, int32_t rows,
+                                             int32_t dim, int32_t vocab, float temperature, const float* lse_dev,
+                                             const float* d_loss_dev, void* d_hidden_dev, int64_t d_row_stride,
+                                             void* d_weight_dev, void* workspace, size_t workspace_bytes,
+                                             dflash_stream_t stream);
+
+/* Synchronises `stream` and copies the call's status word to *status_host. */
+int32_t dflash_linear_cross_entropy_status(const void* workspace, dflash_stream_t stream, int32_t* status_host);
+
+/* --- token embedding and its gradient --------------------------------------------
+ * The drafter's input (paper §4.2: the embedding is shared with the target):
+ *   out[i] = scale * table[tokens[i]]
+ * A token outside [0, vocab) (padding) gives a row of zeros.
+ *   table_dev   [vocab][dim] in table_dtype, contiguous
+ *   tokens_dev  int32 [n_tokens]
+ *   out_dev     rows of dim in out_dtype, out_stride (>= dim) elements apart
+ * Types are independent (a bf16 table to the fp32 residual stream), alignment
+ * any of the types; tensors do not overlap.  n_tokens <= 2^24, dim <= 65536,
+ * vocab <= 2^24, scale finite; n_tokens = 0 launches nothing. */
+int32_t dflash_embed_tokens(const void* table_dev, int32_t table_dtype, int32_t vocab, int32_t dim,
+                            const int32_t* tokens_dev, int32_t n_tokens, float scale, void* out_dev, int32_t out_dtype,
+                            int64_t out_stride, dflash_stream_t stream);
+
+/* d_table[v] = scale * sum over the tokens i equal to v of d_out[i]; 0 for rows
+ * without a token (every element is written), or, with accumulate = 1, added to
+ * what d_table holds (rows without a token are not touched): the gradient of a
+ * table that is the LM head too goes onto dflash_linear_cross_entropy_backward's
+ * d_weight.  Tokens outside [0, vocab) have no gradient and their rows of d_out
+ * are not read.
+ *   d_out_dev   rows of dim in d_out_dtype, d_out_stride elements apart
+ *   d_table_dev [vocab][dim] in table_dtype, contiguous
+ *   workspace   >= dflash_embed_tokens_backward_workspace_bytes(...) bytes,
+ *               256-byte aligned
+ * Sums are fp32 over the sorted tokens in a fixed order (the same call gives the
+ * same bits), rounded once.  The limits of dflash_embed_tokens. */
+size_t dflash_embed_tokens_backward_workspace_bytes(int32_t n_tokens, int32_t dim, int32_t vocab);
+int32_t dflash_embed_tokens_backward(const void* d_out_dev, int32_t d_out_dtype, int64_t d_out_stride,
+                                     const int32_t* tokens_dev, int32_t n_tokens, int32_t vocab, int32_t dim, float scale,
+                                     void* d_table_dev, int32_t table_dtype, int32_t accumulate, void* workspace,
+                                     size_t workspace_bytes, dflash_stream_t stream);
+
 /* --- block-size scheduling (host policy) ---------------------------------------
  * Paper §5.5.4: a drafter trained at a large block size serves smaller
  * inference-time block sizes nearly as well, and large blocks raise the
