@@ -20,15 +20,18 @@
 //   weight   dW = G' H of a piece's rows of the head (both along the rows)
 // A piece is as many columns as keep G within kPieceBytes.
 //
-// A thread loads tiles by TMA into a ring, one warp issues the MMAs, eight warps
-// read the sums.  The tensor cores' fp32 sums truncate (by 2e-8 of the sum a step
-// of 16, to one side), which over a dim of 4,096 would put the loss off by 3e-6 of
-// itself; so a sum ends after kSumBlocks blocks of 64 and the eight warps add it to
-// fp32 registers, two accumulators taking turns.
+// bf16: the two CTAs of a cluster share a tile of 256 x 256 (tcgen05 cta_group::2, each
+// holding half of either operand); a thread of each loads tiles by TMA into a ring, a
+// warp of the first issues the MMAs, eight warps of each read the sums.  The tensor
+// cores' fp32 sums truncate (by 2e-8 of the sum a step of 16, to one side), which over a
+// dim of 4,096 would put the loss off by 3e-6 of itself; so a sum ends after kSumBlocks
+// blocks of 64 and the eight warps add it to fp32 registers, two accumulators taking
+// turns.
 //
 // fp32 tensors enter as three bf16 planes each (x = h + m + l, 24 bits), every
 // product as six (h h, h m, m h, m m, h l, l h; what is left out is below 2^-24),
-// the five small ones with a sum of their own.
+// the five small ones with a sum of their own that spans more blocks.  One CTA a tile
+// of 128 x 128.
 #include <cuda.h>
 
 #include <algorithm>
@@ -42,26 +45,31 @@
 namespace dflash {
 namespace {
 
-constexpr int kBM = 128;                 // rows of an output tile
-constexpr int kSumBlocks = 8;            // K blocks of 64 that one sum of the tensor cores spans
+constexpr int kBM = 128;                 // rows of a CTA's part of a tile: the lanes of tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
 constexpr long long kBudget = 400000000LL;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxParts = 32, kTailWaves = 3;   // parts of a tile of the hidden states' gradient, waves of them
 constexpr size_t kPieceBytes = size_t(192) << 20;
 
 enum Use { kStats, kGrad, kHidden, kWeight };
 
 template <int PL>
 struct GemmCfg {
-  static constexpr int kBN = PL == 1 ? 256 : 128;
-  static constexpr int kA = kBM * 128, kB = kBN * 128;     // bytes of a K block of 64
+  static constexpr int kCtas = PL == 1 ? 2 : 1;            // CTAs that share a tile
+  static constexpr int kTM = kBM * kCtas, kBN = PL == 1 ? 256 : 128;   // the tile
+  static constexpr int kOwnN = kBN / kCtas;                // rows of the second operand that a CTA holds
+  static constexpr int kA = kBM * 128, kB = kOwnN * 128;   // bytes of a K block of 64
   static constexpr int kStage = PL * (kA + kB);
-  static constexpr int kStages = PL == 1 ? 4 : 2;
-  static constexpr int kAccCols = PL == 1 ? kBN : 2 * kBN; // tensor-memory columns of one accumulator (three planes: the small products' sum behind the large one's)
+  static constexpr int kStages = PL == 1 ? 6 : 2;
+  static constexpr int kOut = PL == 1 ? kEpiWarps * 4096 : 0;   // rows staged on their way out, 32 x 64 a warp
+  static constexpr int kAccCols = kBN;                     // tensor-memory columns of an accumulator
   static constexpr int kNC = kBN / 2;                      // columns of an epilogue thread
-  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + 256;
-  static_assert(2 * kAccCols == 512, "two accumulators fill tensor memory");
+  static constexpr int kSumBlocks = PL == 1 ? 8 : 1;       // K blocks that one sum of the tensor cores spans
+  static constexpr int kSmallSums = 8;                     // three planes: sums of the large product to one of the small ones
+  static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + kOut + 256;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct GemmArgs {
@@ -233,7 +241,8 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
     __syncthreads();
   }
   // the last tile's rows behind the kept ones
-  const int end = min((total + kBM - 1) / kBM * kBM, pl.rows_pad);
+  constexpr int kTM = GemmCfg<PL>::kTM;
+  const int end = min((total + kTM - 1) / kTM * kTM, pl.rows_pad);
   for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += gridDim.x * (kGatherThreads / 32)) {
     __nv_bfloat16* dst = pl.h + (size_t)p * pl.dim_pad;
     for (int c = lane * 8; c < pl.dim_pad; c += 256) put8<PL>(dst + c, plane, zero);
@@ -273,87 +282,207 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
+// ---- forms for a CTA alone (G = 1) and for a pair (G = 2)
+template <int G>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%1, %3};\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (G == 2) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
-__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-                   ptx::smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y)
+// One arrival at `bar` (of both CTAs of a pair) when what this thread issued completes.
+template <int G>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (G == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     ptx::smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+  else
+    ptx::mma_commit(bar);
+}
+// The same for this CTA's barrier alone.
+template <int G>
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  if constexpr (G == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+  else
+    ptx::mma_commit(bar);
+}
+template <int G>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+  if constexpr (G == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ptx::smem_u32(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    ptx::tmem_alloc(slot, 512);
+    ptx::tmem_relinquish();
+  }
+}
+template <int G>
+__device__ __forceinline__ void tmem_free(uint32_t taddr) {
+  if constexpr (G == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+  else ptx::tmem_dealloc(taddr, 512);
+}
+// The same place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(ptx::smem_u32(p)), "r"(rank));
+  return r;
+}
+// Box (x = column, y = row) of a tensor map into this CTA's shared memory; the bytes
+// count at `bar`, an address in the cluster (the pair's first CTA).
+template <int G>
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  if constexpr (G == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                     ptx::smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(ptx::smem_u32(src)), "r"(x), "r"(y)
                : "memory");
 }
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// As ptx::mbar_try_wait, for what a thread of the other CTA did before it arrived.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(ptx::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+template <int G>
+__device__ __forceinline__ void sync_tile_ctas() {
+  if constexpr (G == 2) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+__device__ __forceinline__ void red_add4(float* p, float a, float b, float c, float d) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 
-// Items of a launch: output tiles (with a share of K for the hidden states' gradient).
+// Items of a launch, for a group of CTAs that shares a tile: output tiles with their K
+// blocks of 64.
+//
+// The hidden states' gradient has few tiles and a long K: the tiles that would not
+// fill the last wave of CTAs are cut along K into as many parts as make that wave
+// shortest; each part has its sums in memory of its own, and they are added in order
+// at the end.
 template <int PL, int USE>
 struct Items {
-  int m_tiles, n_tiles, splits, blocks;   // blocks: K blocks of 64
-  __device__ __forceinline__ Items(const GemmArgs& a, int kept) {
-    using C = GemmCfg<PL>;
-    const CePlan& pl = a.pl;
-    splits = 1;
+  using C = GemmCfg<PL>;
+  int m_tiles, n_tiles, blocks;
+  int whole, parts;   // tiles that are not cut; parts of each of the others
+  __device__ __forceinline__ Items(const CePlan& pl, int cols, int kept, int groups) {
     if (USE == kWeight) {
-      m_tiles = (a.cols + kBM - 1) / kBM;
+      m_tiles = (cols + C::kTM - 1) / C::kTM;
       n_tiles = (pl.dim + C::kBN - 1) / C::kBN;
       blocks = (kept + 63) / 64;
     } else {
-      m_tiles = (kept + kBM - 1) / kBM;
-      if (USE == kHidden) {
-        n_tiles = (pl.dim + C::kBN - 1) / C::kBN;
-        blocks = (a.cols + 63) / 64;
-        splits = pl.splits;
-      } else {
-        n_tiles = (a.cols + C::kBN - 1) / C::kBN;
-        blocks = pl.dim_pad / 64;
+      m_tiles = (kept + C::kTM - 1) / C::kTM;
+      n_tiles = ((USE == kHidden ? pl.dim : cols) + C::kBN - 1) / C::kBN;
+      blocks = USE == kHidden ? (cols + 63) / 64 : pl.dim_pad / 64;
+    }
+    whole = m_tiles * n_tiles;
+    parts = 1;
+    if (USE == kHidden) {
+      const int rest = whole % groups, all = pl.piece / 64;   // (the same cut for every piece)
+      float best = 1.f;
+      for (int p = 2; p <= kMaxParts && rest * p <= kTailWaves * groups && p * 4 <= all; ++p) {
+        const float waves = (float)((rest * p + groups - 1) / groups) / p + 0.02f * p;
+        if (rest && waves < best) best = waves, parts = p;
       }
+      if (parts > 1) whole -= rest;
     }
   }
-  __device__ __forceinline__ int count() const { return m_tiles * n_tiles * splits; }
+  __device__ __forceinline__ int count() const { return whole + (m_tiles * n_tiles - whole) * parts; }
   // first row and column of the item's tile, and its K blocks
   __device__ __forceinline__ void get(int item, int& m0, int& n0, int& b0, int& b1) const {
-    int mt, nt, sp = 0;
-    if (USE == kWeight) {   // along a row of tiles: G's columns stay in L2
-      nt = item % n_tiles;
-      mt = item / n_tiles;
-    } else {
-      mt = item % m_tiles;
-      nt = item / m_tiles;
-      if (USE == kHidden) {
-        sp = nt / n_tiles;
-        nt -= sp * n_tiles;
-      }
+    int tile = item;
+    b0 = 0;
+    b1 = blocks;
+    if (USE == kHidden && item >= whole) {   // the same part of all tiles side by side
+      const int rest = m_tiles * n_tiles - whole, part = (item - whole) / rest;
+      tile = whole + (item - whole) - part * rest;
+      b0 = (int)((long long)blocks * part / parts);
+      b1 = (int)((long long)blocks * (part + 1) / parts);
     }
-    m0 = mt * kBM;
-    n0 = nt * GemmCfg<PL>::kBN;
-    b0 = (int)((long long)blocks * sp / splits);
-    b1 = (int)((long long)blocks * (sp + 1) / splits);
+    if (USE == kWeight) {   // along a row of tiles: G's columns stay in L2
+      n0 = tile % n_tiles * C::kBN;
+      m0 = tile / n_tiles * C::kTM;
+    } else {
+      m0 = tile % m_tiles * C::kTM;
+      n0 = tile / m_tiles * C::kBN;
+    }
   }
-  __device__ __forceinline__ int split_of(int item) const { return item / (m_tiles * n_tiles); }
 };
 
 struct GemmBars {
-  uint64_t full[4], empty[4], acc_full[2], acc_free[2], done;
+  uint64_t full[6], empty[6], acc_full[2], acc_free[2], done;
   uint32_t tmem;
 };
+
+// A warp's 32 rows of 64 bf16 to `map` at (x, y), through 4 KB of its own in the maps'
+// 128-byte swizzle; v: this lane's row.
+__device__ __forceinline__ void store_rows(const CUtensorMap* map, uint8_t* stage, int lane, int x, int y, const float* v) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the last rows have left
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    put8<1>(reinterpret_cast<__nv_bfloat16*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)), 0, v + 8 * j);
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) tma_store(map, stage, x, y);
+}
 
 template <int PL, int USE>
 __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                   const __grid_constant__ CUtensorMap map_b,
+                                                                  const __grid_constant__ CUtensorMap map_out,
                                                                   const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<PL>;
-  constexpr int S = C::kStages;
+  constexpr int S = C::kStages, G = C::kCtas;
   constexpr bool kAMN = USE == kWeight, kBMN = USE == kWeight || USE == kHidden;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
-  GemmBars* bars = reinterpret_cast<GemmBars*>(sm + (size_t)S * C::kStage);
+  GemmBars* bars = reinterpret_cast<GemmBars*>(sm + (size_t)S * C::kStage + C::kOut);
   const CePlan& pl = a.pl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = G == 2 ? blockIdx.x & 1 : 0, group = blockIdx.x / G, groups = gridDim.x / G;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(bars->full + s, 1);
@@ -361,25 +490,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bars->acc_full + b, 1);
-      ptx::mbar_init(bars->acc_free + b, kEpiWarps);
+      ptx::mbar_init(bars->acc_free + b, kEpiWarps * G);
     }
     ptx::mbar_init(&bars->done, 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&map_a);
     ptx::prefetch_tmap(&map_b);
   }
-  if (warp == 2) {
-    ptx::tmem_alloc(&bars->tmem, 512);
-    ptx::tmem_relinquish();
-  }
+  if (warp == 2) tmem_alloc<G>(&bars->tmem);
   ptx::tc_fence_before();
   __syncthreads();
+  sync_tile_ctas<G>();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem;
   griddep_wait();
   griddep_trigger();
   const int kept = *pl.kept;
-  const Items<PL, USE> items(a, kept);
+  const Items<PL, USE> items(pl, a.cols, kept, groups);
   const int n_items = items.count();
 
   if (warp == 0) {
@@ -388,11 +515,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       bool ok = true;
       // rows between the planes of each operand
       const int a_plane = pl.rows_pad, b_plane = USE == kWeight ? pl.rows_pad : pl.piece;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      // a bf16 head is read where the caller has it
+      const int v0 = PL == 1 ? a.v0 : 0;
+      for (int item = group; item < n_items && ok; item += groups) {
         int m0, n0, b0, b1;
         items.get(item, m0, n0, b0, b1);
-        // a bf16 head is read where the caller has it
-        const int v0 = PL == 1 ? a.v0 : 0;
+        m0 += rank * kBM;
+        n0 += rank * C::kOwnN;
         for (int kb = b0; kb < b1; ++kb, ++it) {
           const int s = it % S;
           if (it >= S && !ptx::mbar_wait(bars->empty + s, ((it / S) & 1) ^ 1, kBudget, pl.status)) {
@@ -400,40 +529,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
             break;
           }
           uint8_t* st = sm + (size_t)s * C::kStage;
-          ptx::mbar_arrive_expect_tx(bars->full + s, C::kStage);
+          // the bytes of both CTAs count at the first one's barrier
+          const uint32_t bar = G == 2 ? at_rank(bars->full + s, 0) : ptx::smem_u32(bars->full + s);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(bars->full + s, G * C::kStage);
 #pragma unroll
           for (int p = 0; p < PL; ++p) {
             uint8_t* ta = st + p * C::kA;
             if (kAMN) {
 #pragma unroll
-              for (int i = 0; i < kBM / 64; ++i)
-                tma_tile(ta + i * 8192, &map_a, bars->full + s, m0 + 64 * i, p * a_plane + kb * 64);
+              for (int i = 0; i < kBM / 64; ++i) tma_tile<G>(ta + i * 8192, &map_a, bar, m0 + 64 * i, p * a_plane + kb * 64);
             } else {
-              tma_tile(ta, &map_a, bars->full + s, kb * 64, p * a_plane + m0);
+              tma_tile<G>(ta, &map_a, bar, kb * 64, p * a_plane + m0);
             }
             uint8_t* tb = st + PL * C::kA + p * C::kB;
             if (kBMN) {
               const int row = p * b_plane + (USE == kHidden ? v0 : 0) + kb * 64;
 #pragma unroll
-              for (int i = 0; i < C::kBN / 64; ++i) tma_tile(tb + i * 8192, &map_b, bars->full + s, n0 + 64 * i, row);
+              for (int i = 0; i < C::kOwnN / 64; ++i) tma_tile<G>(tb + i * 8192, &map_b, bar, n0 + 64 * i, row);
             } else {
-              tma_tile(tb, &map_b, bars->full + s, kb * 64, p * b_plane + v0 + n0);
+              tma_tile<G>(tb, &map_b, bar, kb * 64, p * b_plane + v0 + n0);
             }
           }
         }
       }
-      // every load issued lands before the CTA can exit
-      for (int j = max(0, it - S); j < it; ++j) ptx::mbar_wait(bars->full + j % S, (j / S) & 1, kBudget, nullptr);
+      // every load issued lands before the CTA can exit (the other CTA's wait for the
+      // first one at the end)
+      if (rank == 0)
+        for (int j = max(0, it - S); j < it; ++j) ptx::mbar_wait(bars->full + j % S, (j / S) & 1, kBudget, nullptr);
     }
-  } else if (warp == 1) {   // ---------------------------------------------- MMAs
+  } else if (warp == 1 && rank == 0) {   // --------------------------------- MMAs
     // The whole warp runs this, so that what it computes is uniform; one elected
     // lane issues each group of MMAs with the commits behind it.
-    constexpr uint32_t id = ptx::idesc_bf16_f32(kBM, C::kBN) | (kAMN ? 1u << 15 : 0u) | (kBMN ? 1u << 16 : 0u);
+    constexpr uint32_t id = ptx::idesc_bf16_f32(C::kTM, C::kBN) | (kAMN ? 1u << 15 : 0u) | (kBMN ? 1u << 16 : 0u);
     constexpr uint32_t ka = k_step<kAMN>(), kb_ = k_step<kBMN>();
     bool ok = true;
     auto wait = [&](uint64_t* b, uint32_t p) {
-      if (!__all_sync(0xffffffffu, ptx::mbar_try_wait(b, p))) {
-        ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status);
+      if (!__all_sync(0xffffffffu, try_wait_cluster(b, p))) {
+        ok = ok && ptx::mbar_wait(b, p, kBudget, pl.status) && try_wait_cluster(b, p);
         ok = __all_sync(0xffffffffu, ok);
       }
       ptx::tc_fence_after();
@@ -441,15 +573,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     };
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t base = ptx::smem_u32(sm);
-    int it = 0, seq = 0;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+    int it = 0, seq = 0, small_seq = 0;
+    for (int item = group; item < n_items && ok; item += groups) {
       int m0, n0, b0, b1;
       items.get(item, m0, n0, b0, b1);
+      int sums = 0;
       for (int kb = b0; kb < b1 && ok; ++seq) {
         const int buf = seq & 1, use = seq >> 1;
         if (use >= 1 && !wait(bars->acc_free + buf, (use - 1) & 1)) break;
         const uint32_t d = tm + buf * C::kAccCols;
-        const int end = min(kb + kSumBlocks, b1);
+        // the small products' sum spans kSmallSums of the large one's; its two
+        // accumulators lie behind the large one's two, and one is free again before
+        // the last but one of the large one's is
+        const uint32_t ds = tm + (2 + (small_seq & 1)) * C::kAccCols;
+        const int end = min(kb + C::kSumBlocks, b1);
         uint32_t acc = 0;
         for (; kb < end; ++kb, ++it) {
           const int s = it % S;
@@ -458,7 +595,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           if (elect()) {
             if constexpr (PL == 1) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma(d, da + k * ka, db + k * kb_, id, acc | (k != 0));
+              for (int k = 0; k < 4; ++k) mma<G>(d, da + k * ka, db + k * kb_, id, acc | (k != 0));
             } else {
               // small products first: l h, h l, m m, m h, h m, then h h
               constexpr int qa[6] = {2, 0, 1, 1, 0, 0}, qb[6] = {0, 2, 1, 0, 1, 0};
@@ -466,34 +603,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
               for (int q = 0; q < 6; ++q)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  mma(d + (q < 5 ? C::kBN : 0), da + (qa[q] * C::kA >> 4) + k * ka, db + (qb[q] * C::kB >> 4) + k * kb_,
-                      id, acc | (k != 0) | (q > 0 && q < 5));
+                  mma<G>(q < 5 ? ds : d, da + (qa[q] * C::kA >> 4) + k * ka, db + (qb[q] * C::kB >> 4) + k * kb_, id,
+                         q < 5 ? (acc | (sums != 0)) | (k != 0) | (q > 0) : acc | (k != 0));
             }
-            ptx::mma_commit(bars->empty + s);
-            if (kb + 1 == end) ptx::mma_commit(bars->acc_full + buf);
+            commit<G>(bars->empty + s);
+            if (kb + 1 == end) commit<G>(bars->acc_full + buf);
           }
           __syncwarp();
           acc = 1;
         }
+        if (++sums == C::kSmallSums || kb == b1) sums = 0, ++small_seq;
       }
     }
-    if (elect()) ptx::mma_commit(&bars->done);
+    if (elect()) commit_own<G>(&bars->done);
     __syncwarp();
-    ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTA does
+    ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTAs do
   } else if (warp >= 4) {   // ---------------------------------------------- sums
     constexpr int NC = C::kNC;
     const int half = (warp - 4) >> 2, lane_row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int c_half = half * NC;
-    int seq = 0;
+    uint8_t* stage = sm + (size_t)S * C::kStage + (warp - 4) * 4096;
+    const uint32_t free0 = G == 2 ? at_rank(bars->acc_free, 0) : ptx::smem_u32(bars->acc_free);
+    int seq = 0, small_seq = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+    for (int item = group; item < n_items && ok; item += groups) {
       int m0, n0, b0, b1;
       items.get(item, m0, n0, b0, b1);
+      m0 += rank * kBM;
+      const int row = m0 + lane_row;   // (a vocabulary row of the piece for kWeight)
+      // what the row needs at the end
+      const bool in = USE != kStats && USE != kGrad ? false : row < kept;
+      const int target = in ? pl.target[row] : -1;
+      const float2 l2 = USE == kGrad && in ? pl.lse2[row] : make_float2(0.f, 0.f);
+      const float gain = USE == kGrad && in ? pl.gain[row] : 0.f;
       float acc[NC];
 #pragma unroll
       for (int j = 0; j < NC; ++j) acc[j] = 0.f;
-      for (int kb = b0; kb < b1; kb += kSumBlocks, ++seq) {
+      int sums = 0;
+      for (int kb = b0; kb < b1; kb += C::kSumBlocks, ++seq) {
         const int buf = seq & 1;
         if (!ptx::mbar_wait(bars->acc_full + buf, (seq >> 1) & 1, kBudget, pl.status)) ok = false;
         if (!__all_sync(0xffffffffu, ok)) {
@@ -501,30 +649,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t at = tmem + lanes + buf * C::kAccCols + c_half;
+        auto drain = [&](uint32_t at) {
 #pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 16) {
-          float v[16];
-          if constexpr (PL == 3) {
-            ptx::tmem_ld16(at + C::kBN + j0, v);
+          for (int j0 = 0; j0 < NC; j0 += 16) {
+            float v[16];
+            ptx::tmem_ld16(at + j0, v);
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[j0 + j] += v[j];
           }
-          ptx::tmem_ld16(at + j0, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j0 + j] += v[j];
+        };
+        if (PL == 3 && (++sums == C::kSmallSums || kb + C::kSumBlocks >= b1)) {
+          drain(tmem + lanes + (2 + (small_seq & 1)) * C::kAccCols + c_half);
+          sums = 0;
+          ++small_seq;
         }
+        drain(tmem + lanes + buf * C::kAccCols + c_half);
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bars->acc_free + buf);
+        if (lane == 0) arrive_at(free0 + buf * 8);
       }
       if (!ok) break;
-      const int row = m0 + lane_row;   // (a vocabulary row of the piece for kWeight)
+      const int col = n0 + c_half;     // within the piece, or the dim
       if constexpr (USE == kStats) {
-        if (row < kept) {
-          const int col = n0 + c_half;                       // within the piece
+        if (in) {
           const int left = a.cols - col;                     // columns that there are
-          const int tgt = pl.target[row] - a.v0 - col;
+          const int tgt = target - a.v0 - col;
           float m = -INFINITY, s = 0.f;
 #pragma unroll
           for (int j0 = 0; j0 < NC; j0 += 32) {
@@ -548,56 +697,63 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           pl.part[(size_t)(a.part0 + 2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
         }
       } else if constexpr (USE == kGrad) {
-        const bool in = row < kept;
-        const float2 l2 = in ? pl.lse2[row] : make_float2(0.f, 0.f);
-        const float gain = in ? pl.gain[row] : 0.f;
-        const int col = n0 + c_half, left = in ? a.cols - col : 0, tgt = in ? pl.target[row] - a.v0 - col : -1;
-        __nv_bfloat16* out = pl.g + (size_t)row * pl.piece + col;
+        const int left = in ? a.cols - col : 0, tgt = target - a.v0 - col;
 #pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 8) {
-          float g[8];
+        for (int j = 0; j < NC; ++j) {
+          float e = fmaf(acc[j], a.scale2, -l2.x);
+          if (PL == 3) e = fmaf(acc[j], a.scale2_lo, e - l2.y);
+          e = ex2(e);
+          if (j == tgt) e -= 1.f;
+          acc[j] = j < left ? gain * e : 0.f;
+        }
+        if constexpr (PL == 1) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = j0 + j;
-            float e = fmaf(acc[c], a.scale2, -l2.x);
-            if (PL == 3) e = fmaf(acc[c], a.scale2_lo, e - l2.y);
-            g[j] = c < left ? gain * (ex2(e) - (c == tgt ? 1.f : 0.f)) : 0.f;
-          }
-          put8<PL>(out + j0, (size_t)pl.rows_pad * pl.piece, g);
+          for (int j0 = 0; j0 < NC; j0 += 64) store_rows(&map_out, stage, lane, col + j0, m0 + 32 * (warp & 3), acc + j0);
+        } else {
+          __nv_bfloat16* out = pl.g + (size_t)row * pl.piece + col;
+#pragma unroll
+          for (int j0 = 0; j0 < NC; j0 += 8) put8<PL>(out + j0, (size_t)pl.rows_pad * pl.piece, acc + j0);
         }
       } else if constexpr (USE == kHidden) {
-        float* out = pl.acc + ((size_t)items.split_of(item) * pl.rows_pad + row) * pl.dim_pad + n0 + c_half;
-        const int left = pl.dim_pad - n0 - c_half;
+        // whole tiles to their place, parts of a tile to a tile of their own; a piece
+        // adds to what the pieces before it left (each value once a launch: the order
+        // of the additions is fixed)
+        const bool part = item >= items.whole;
+        float* out = part ? pl.tail + ((size_t)(item - items.whole) * C::kTM + rank * kBM + lane_row) * C::kBN + c_half
+                          : pl.acc + (size_t)row * pl.dim_pad + col;
+        const int left = part ? NC : pl.dim_pad - col;
+        if (a.first) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-          if (j >= left) break;
-          float4 v = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-          float4* p = reinterpret_cast<float4*>(out + j);
-          if (!a.first) {
-            const float4 o = *p;
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-          }
-          *p = v;
-        }
-      } else {
-        if (row < a.cols) {
-          const size_t at = (size_t)(a.v0 + row) * pl.dim + n0 + c_half;
-          const int left = pl.dim - n0 - c_half;   // a multiple of 8
+          for (int j = 0; j < NC; j += 4)
+            if (j < left) *reinterpret_cast<float4*>(out + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        } else {
 #pragma unroll
-          for (int j = 0; j < NC; j += 8) {
-            if (j >= left) break;
-            if (PL == 3) set8(static_cast<float*>(a.d_weight) + at + j, true, acc + j);
-            else set8(static_cast<__nv_bfloat16*>(a.d_weight) + at + j, true, acc + j);
-          }
+          for (int j = 0; j < NC; j += 4)
+            if (j < left) red_add4(out + j, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
+      } else if constexpr (PL == 1) {
+        // (rows behind the head's last and columns behind the dim are cut off by the map)
+#pragma unroll
+        for (int j0 = 0; j0 < NC; j0 += 64)
+          if (m0 + 32 * (warp & 3) < a.cols && col + j0 < pl.dim)
+            store_rows(&map_out, stage, lane, col + j0, a.v0 + m0 + 32 * (warp & 3), acc + j0);
+      } else if (row < a.cols) {
+        float* out = static_cast<float*>(a.d_weight) + (size_t)(a.v0 + row) * pl.dim + col;
+        const int left = pl.dim - col;   // a multiple of 8
+#pragma unroll
+        for (int j = 0; j < NC; j += 8)
+          if (j < left) set8(out + j, true, acc + j);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
+  sync_tile_ctas<G>();   // neither CTA leaves while the other's MMAs or arrivals may reach it
   if (warp == 2) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    tmem_free<G>(tmem);
   }
 }
 
@@ -645,24 +801,33 @@ __global__ void __launch_bounds__(32 * kMergeWarps) ce_merge_kernel(CePlan pl, i
   }
 }
 
-// The shares of the hidden states' gradient added in order, to the caller's rows.
-template <typename T>
-__global__ void __launch_bounds__(256) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride) {
+// The hidden states' gradient to the caller's rows, the parts of a cut tile added in
+// order.
+template <typename T, int PL>
+__global__ void __launch_bounds__(256) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
   griddep_wait();
   griddep_trigger();
+  using C = GemmCfg<PL>;
   const int kept = *pl.kept, groups = pl.dim / 8;
+  const Items<PL, kHidden> items(pl, pl.piece, kept, groups_of_ctas);
+  const int rest = items.m_tiles * items.n_tiles - items.whole;
   const bool vec = rows_vec(d_hidden, stride);
-  const size_t share = (size_t)pl.rows_pad * pl.dim_pad;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)kept * groups; i += gridDim.x * 256LL) {
     const int r = (int)(i / groups), c = (int)(i - (long long)r * groups) * 8;
-    const float* src = pl.acc + (size_t)r * pl.dim_pad + c;
+    const int tile = c / C::kBN * items.m_tiles + r / C::kTM;
     float sum[8];
-    get8(src, true, sum);
-    for (int s = 1; s < pl.splits; ++s) {
-      float v[8];
-      get8(src + s * share, true, v);
+    if (tile < items.whole) {
+      get8(pl.acc + (size_t)r * pl.dim_pad + c, true, sum);
+    } else {
+      const float* src = pl.tail + ((size_t)(tile - items.whole) * C::kTM + r % C::kTM) * C::kBN + c % C::kBN;
+      get8(src, true, sum);
+#pragma unroll 4
+      for (int p = 1; p < items.parts; ++p) {
+        float v[8];
+        get8(src + (size_t)p * rest * C::kTM * C::kBN, true, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
     }
     set8(d_hidden + pl.row_of[r] * stride + c, vec, sum);
   }
@@ -678,10 +843,33 @@ cudaError_t prepare() {
   return cudaSuccess;
 }
 
+int gemm_grid(int planes, int sms) { return planes == 1 ? std::max(2, sms / 2 * 2) : sms; }
+
 template <int PL, int USE>
-cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, int sms, int* launches, cudaStream_t s) {
+cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, int sms, int* launches,
+                 cudaStream_t s) {
   ++*launches;
-  return launch_pdl(ce_gemm_kernel<PL, USE>, dim3(sms), dim3(kGemmThreads), GemmCfg<PL>::kBytes, s, ma, mb, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gemm_grid(PL, sms));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = GemmCfg<PL>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (GemmCfg<PL>::kCtas > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = GemmCfg<PL>::kCtas;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<PL, USE>, ma, mb, mo, a);
 }
 
 struct Scale {
@@ -707,8 +895,8 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
   if (e != cudaSuccess) return e;
   CUtensorMap mh, mw;
   bool ok = encode_activation_map(&mh, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM);
-  ok = ok && (PL == 1 ? encode_activation_map(&mw, t.weight, pl.dim, pl.vocab, pl.dim, C::kBN)
-                      : encode_activation_map(&mw, pl.w, pl.dim_pad, PL * pl.piece, pl.dim_pad, C::kBN));
+  ok = ok && (PL == 1 ? encode_activation_map(&mw, t.weight, pl.dim, pl.vocab, pl.dim, C::kOwnN)
+                      : encode_activation_map(&mw, pl.w, pl.dim_pad, PL * pl.piece, pl.dim_pad, C::kOwnN));
   if (!ok) return cudaErrorInvalidValue;
   GemmArgs a{};
   a.pl = pl;
@@ -723,7 +911,7 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    e = gemm<PL, kStats>(a, mh, mw, sms, launches, s);
+    e = gemm<PL, kStats>(a, mh, mw, mw, sms, launches, s);
     if (e != cudaSuccess) return e;
     a.part0 += 2 * ((a.cols + C::kBN - 1) / C::kBN);
   }
@@ -739,15 +927,17 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
   ++*launches;
   if (e != cudaSuccess) return e;
   // operands with the product's K along their rows (boxes of 64 x rows of the tile) or across them (64 x 64)
-  CUtensorMap h_k, h_mn, w_k, w_mn, g_k, g_mn;
+  CUtensorMap h_k, h_mn, w_k, w_mn, g_k, g_mn, g_out, dw_out;
   const void* w = PL == 1 ? t.weight : pl.w;
   const int w_dim = PL == 1 ? pl.dim : pl.dim_pad, w_rows = PL == 1 ? pl.vocab : PL * pl.piece;
   if (!encode_activation_map(&h_k, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM) ||
       !encode_activation_map(&h_mn, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, 64) ||
-      !encode_activation_map(&w_k, w, w_dim, w_rows, w_dim, C::kBN) ||
+      !encode_activation_map(&w_k, w, w_dim, w_rows, w_dim, C::kOwnN) ||
       !encode_activation_map(&w_mn, w, w_dim, w_rows, w_dim, 64) ||
       !encode_activation_map(&g_k, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, kBM) ||
-      !encode_activation_map(&g_mn, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 64))
+      !encode_activation_map(&g_mn, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 64) ||
+      !encode_activation_map(&g_out, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 32) ||
+      !(PL == 1 && t.d_weight ? encode_activation_map(&dw_out, t.d_weight, pl.dim, pl.vocab, pl.dim, 32) : (dw_out = g_out, true)))
     return cudaErrorInvalidValue;
   GemmArgs a{};
   a.pl = pl;
@@ -764,15 +954,15 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    if ((e = gemm<PL, kGrad>(a, h_k, w_k, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_hidden && (e = gemm<PL, kHidden>(a, g_k, w_mn, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_weight && (e = gemm<PL, kWeight>(a, g_mn, h_mn, sms, launches, s)) != cudaSuccess) return e;
+    if ((e = gemm<PL, kGrad>(a, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (t.d_hidden && (e = gemm<PL, kHidden>(a, g_k, w_mn, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (t.d_weight && (e = gemm<PL, kWeight>(a, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
   }
   if (!t.d_hidden) return cudaSuccess;
   ++*launches;
   const long long groups = (long long)pl.rows * (pl.dim / 8);
-  return launch_pdl(ce_finish_hidden_kernel<T>, dim3((unsigned)std::min<long long>((groups + 255) / 256, sms * 8)), dim3(256), 0,
-                    s, pl, static_cast<T*>(t.d_hidden), t.d_row_stride);
+  return launch_pdl(ce_finish_hidden_kernel<T, PL>, dim3((unsigned)std::min<long long>((groups + 255) / 256, sms * 8)), dim3(256), 0,
+                    s, pl, static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_grid(PL, sms) / C::kCtas);
 }
 
 }  // namespace
@@ -783,7 +973,8 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.dim = dim;
   pl.vocab = vocab;
   pl.planes = f32 ? 3 : 1;
-  pl.rows_pad = (rows + kBM - 1) / kBM * kBM;
+  const int tm = f32 ? GemmCfg<3>::kTM : GemmCfg<1>::kTM;
+  pl.rows_pad = (rows + tm - 1) / tm * tm;
   pl.dim_pad = (dim + 63) / 64 * 64;
   const int bn = f32 ? GemmCfg<3>::kBN : GemmCfg<1>::kBN;
   // pieces of equal size, as few as the limit allows
@@ -811,7 +1002,6 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.target = reinterpret_cast<int32_t*>(take(4 * R));
   pl.h = reinterpret_cast<__nv_bfloat16*>(take(2 * pl.planes * R * pl.dim_pad));
   if (f32) pl.w = reinterpret_cast<__nv_bfloat16*>(take(6 * (size_t)pl.piece * pl.dim_pad));
-  pl.splits = 1;
   if (!backward) {
     const size_t pieces = (size_t)((vocab + pl.piece - 1) / pl.piece);
     pl.part = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * pieces * ((pl.piece + bn - 1) / bn) * R));
@@ -821,18 +1011,8 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
     pl.gain = reinterpret_cast<float*>(take(4 * R));
     pl.g = reinterpret_cast<__nv_bfloat16*>(take(2 * pl.planes * R * pl.piece));
     if (want_hidden) {
-      // shares of a piece's columns: as many as fill the SMs evenly, against the fp32 sums' traffic
-      const double tiles = (double)(R / kBM) * ((dim + bn - 1) / bn), blocks = pl.piece / 64;
-      double best = 1e300;
-      for (int n = 1; n <= 64 && n <= blocks; ++n) {
-        const double items = std::ceil(tiles * n / sms) * (std::ceil(blocks / n) * (f32 ? 1600 : 550) + 4000);
-        const double sums = n * tiles * kBM * bn * 8.0 / 3500.0;   // bytes over bytes a cycle
-        if (items + sums < best * 0.98) {
-          best = items + sums;
-          pl.splits = n;
-        }
-      }
-      pl.acc = reinterpret_cast<float*>(take(4 * (size_t)pl.splits * R * pl.dim_pad));
+      pl.acc = reinterpret_cast<float*>(take(4 * R * pl.dim_pad));
+      pl.tail = reinterpret_cast<float*>(take(4 * (size_t)kTailWaves * sms * kBM * bn));
     }
   }
   pl.bytes = off;

@@ -15,9 +15,8 @@ namespace dflash {
 struct CePlan {
   int rows, dim, vocab;
   int planes;            // bf16 planes of an operand: 1 (bf16 tensors) or 3 (fp32 tensors)
-  int rows_pad, dim_pad; // multiples of 128 and 64
+  int rows_pad, dim_pad; // multiples of a tile's rows (256 or, for fp32 tensors, 128) and of 64
   int piece;             // vocabulary columns of a piece (a multiple of 256)
-  int splits;            // shares of a piece's columns in the hidden states' gradient
   int32_t* status;
   int32_t* kept;         // rows kept
   int32_t* row_of;       // [rows_pad] the caller's row
@@ -29,7 +28,8 @@ struct CePlan {
   float2* lse2;          // gradient: [rows_pad] lse log2(e) as a rounded value and its residual
   float* gain;           // gradient: [rows_pad] d_loss / T
   __nv_bfloat16* g;      // gradient: [planes][rows_pad][piece] gradient of a piece of the logits
-  float* acc;            // gradient: [splits][rows_pad][dim_pad] sums of the hidden states' gradient
+  float* acc;            // gradient: [rows_pad][dim_pad] sums of the hidden states' gradient
+  float* tail;           // gradient: sums of the parts of its tiles that are cut
   size_t bytes;
 };
 

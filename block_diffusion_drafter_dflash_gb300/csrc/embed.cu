@@ -56,12 +56,12 @@ __device__ __forceinline__ void store_row(T* p, const float* v) {
     *reinterpret_cast<Vec<T, P>*>(p + k) = x;
   }
 }
-// The widest vector (8, 4, 2 or 1 values) that both sides' rows allow: rows start at
-// multiples of it, and accesses of up to 16 bytes are aligned.
+// The widest vector (8, 4, 2 or 1 values, at most 16 bytes of the wider type, so that a
+// warp's accesses have no gaps) that both sides' rows allow: rows start at multiples of it.
 int width_of(const void* a, int64_t a_stride, int a_size, const void* b, int64_t b_stride, int b_size, int dim) {
-  for (int w = 8; w > 1; w /= 2) {
+  for (int w = 16 / std::max(a_size, b_size); w > 1; w /= 2) {
     auto fits = [&](const void* p, int64_t stride, int size) {
-      const uintptr_t bytes = std::min(16, w * size);
+      const uintptr_t bytes = w * size;
       return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (uintptr_t)(stride * size) % bytes == 0;
     };
     if (dim % w == 0 && fits(a, a_stride, a_size) && fits(b, b_stride, b_size)) return w;
@@ -70,21 +70,22 @@ int width_of(const void* a, int64_t a_stride, int a_size, const void* b, int64_t
 }
 
 // ---------------------------------------------------------------- lookup
+constexpr int kLookups = 4;   // vectors of a thread, all loaded before the first is stored
+
 template <typename TT, typename TO, int W>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_wait();
   griddep_trigger();
   const unsigned groups = a.dim / W;
-  const long long n = (long long)a.n * groups, step = (long long)gridDim.x * 256;
+  const long long n = (long long)a.n * groups, step = (long long)gridDim.x * (256 * kLookups);
   const TT* table = static_cast<const TT*>(a.table);
   TO* out = static_cast<TO*>(a.out);
-  constexpr int U = 4;
-  for (long long i0 = blockIdx.x * 256LL + threadIdx.x; i0 < n; i0 += step * U) {
-    float v[U][W];
-    TO* to[U];
+  for (long long i0 = blockIdx.x * (256LL * kLookups) + threadIdx.x; i0 < n; i0 += step) {
+    float v[kLookups][W];
+    TO* to[kLookups];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long i = i0 + u * step;
+    for (int u = 0; u < kLookups; ++u) {
+      const long long i = i0 + u * 256;
       to[u] = nullptr;
       if (i < n) {
         const int r = n < (1LL << 32) ? (unsigned)i / groups : (int)(i / groups);
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < kLookups; ++u)
       if (to[u]) {
 #pragma unroll
         for (int j = 0; j < W; ++j) v[u][j] *= a.scale;
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMaxCluster = 8;
+constexpr int kBatch = 8;   // steps of 32 pairs that a warp loads together
 constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + 2);
 
 // One cluster.  Each warp owns a contiguous share of the pairs.  A pass counts its
@@ -149,12 +151,23 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
     for (int i = tid; i < kBins * kSortWarps; i += kSortThreads) count[i] = 0;
     __syncthreads();
     uint32_t* mine = count + warp * kBins;
-    for (int i = beg; i < end; i += 32) {
-      const bool in = i + lane < end;
-      const unsigned d = in ? pair_at(i + lane).x >> shift & (kBins - 1) : kBins;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
-      __syncwarp();
+    uint2 p[kBatch];
+    auto load_batch = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * 32 + lane < end) p[u] = pair_at(i + u * 32 + lane);
+    };
+    for (int i = beg; i < end; i += 32 * kBatch) {
+      load_batch(i);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * 32 < end) {
+          const bool in = i + u * 32 + lane < end;
+          const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
+          const unsigned same = __match_any_sync(0xffffffffu, d);
+          if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+          __syncwarp();
+        }
     }
     __syncthreads();
     if (tid < kBins) {
@@ -188,15 +201,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
       place[tid] = run - all + before;
     }
     __syncthreads();
-    for (int i = beg; i < end; i += 32) {
-      const bool in = i + lane < end;
-      const uint2 p = in ? pair_at(i + lane) : make_uint2(0, 0);
-      const unsigned d = in ? p.x >> shift & (kBins - 1) : kBins;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (in) dst[place[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p;
-      __syncwarp();
-      if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
-      __syncwarp();
+    for (int i = beg; i < end; i += 32 * kBatch) {
+      if (share > 32 * kBatch) load_batch(i);   // (otherwise they are still here)
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + u * 32 < end) {
+          const bool in = i + u * 32 + lane < end;
+          const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
+          const unsigned same = __match_any_sync(0xffffffffu, d);
+          if (in) dst[place[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p[u];
+          __syncwarp();
+          if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+          __syncwarp();
+        }
     }
     cluster.sync();   // the pairs are where the next pass reads them, and `total` may change
   }
@@ -227,7 +244,8 @@ __device__ __forceinline__ void put_sum(TT* p, const float* sum, float scale, in
 }
 
 // First `chunks` blocks of the grid's x: a chunk's sums over blockDim.x * W columns.
-// The others, unless the gradient is added to what is there: rows without a token.
+// The others, unless the gradient is added to what is there: rows without a token, 32
+// at a time (one word of `seen`), all their stores independent.
 template <typename TO, typename TT, int W>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
@@ -237,8 +255,19 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
   if ((int)blockIdx.x >= pl.chunks) {
     if (c >= pl.dim) return;
     const float zero[W] = {};
-    for (int v = blockIdx.x - pl.chunks; v < pl.vocab; v += gridDim.x - pl.chunks)
-      if (!(pl.seen[v >> 5] >> (v & 31) & 1)) store_row<W>(table + (size_t)v * pl.dim + c, zero);
+    const int words = (pl.vocab + 31) / 32;
+    for (int w = blockIdx.x - pl.chunks; w < words; w += gridDim.x - pl.chunks) {
+      const uint32_t seen = pl.seen[w];
+      const int n = min(32, pl.vocab - w * 32);
+      TT* row = table + (size_t)w * 32 * pl.dim + c;
+      if (seen == 0 && n == 32) {
+#pragma unroll 8
+        for (int v = 0; v < 32; ++v) store_row<W>(row + (size_t)v * pl.dim, zero);
+      } else {
+        for (int v = 0; v < n; ++v)
+          if (!(seen >> v & 1)) store_row<W>(row + (size_t)v * pl.dim, zero);
+      }
+    }
     return;
   }
   __shared__ uint2 s_pair[kChunk];
@@ -253,7 +282,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
   const TO* d_out = static_cast<const TO*>(a.d_out);
   float sum[W] = {};
   bool first = true;
-  constexpr int U = 8;
+  constexpr int U = W == 8 ? 4 : 8;
   for (int i = 0; i < n; i += U) {
     float v[U][W];
 #pragma unroll
@@ -281,56 +310,222 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
   }
 }
 
-// A token that begins in this chunk and goes on: its chunks' sums in order, with
-// what each addition rounds off summed beside them.
+// Tokens that go on from a chunk into others: their chunks' sums in order, with what
+// each addition rounds off summed beside them.  A CTA looks at the ends of kJoinChunks
+// chunks, over 32 * W columns.  A token of few chunks is one warp's; those of more are
+// taken by all warps together, a run of chunks each.
+constexpr int kJoinWarps = 8, kJoinChunks = 32, kJoinAlone = 12;
+
+template <int W>
+struct Sum {
+  float s[W], e[W];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < W; ++j) s[j] = e[j] = 0.f;
+  }
+  __device__ __forceinline__ void add(const float* v) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float t = s[j] + v[j], x = t - s[j];
+      e[j] += (s[j] - (t - x)) + (v[j] - x);
+      s[j] = t;
+    }
+  }
+  // the sum with its error (which is NaN where the sum is infinite)
+  __device__ __forceinline__ void done(float* v) const {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = isfinite(e[j]) ? s[j] + e[j] : s[j];
+  }
+};
+
 template <typename TT, int W>
-__global__ void __launch_bounds__(256) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
+  __shared__ int s_last[kJoinChunks];              // a chunk's token's last chunk; 0: none begins here and goes on
+  __shared__ Sum<W> s_sum[kJoinWarps][32];
   const uint2* order = pl.order;
-  const int kept = *pl.kept, b = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
-  const int next = (b + 1) * kChunk;   // the chunk's end; a token that goes on fills it
-  if (next >= kept || c >= pl.dim) return;
-  const unsigned t = order[next - 1].x;
-  if (order[next].x != t) return;
-  if (b > 0 && order[b * kChunk - 1].x == t) return;   // begins in an earlier chunk
-  // the last chunk that has the token: the one of the last pair up to it
-  int lo = next, hi = kept;   // order[lo].x == t; order[hi].x > t or the end
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (order[mid].x == t) lo = mid; else hi = mid;
-  }
-  const int last = lo / kChunk;
-  float sum[W], err[W] = {};
-  // (a token that fills its first chunk from the start has its sum in the chunk's last place all the same)
-  load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, sum);
-  constexpr int U = 8;
-  for (int k = b + 1; k <= last; k += U) {
-    float v[U][W];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u <= last) load_row<W>(pl.part + (size_t)(k + u) * 2 * pl.dim + c, v[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (k + u <= last) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const float s = sum[j] + v[u][j], x = s - sum[j];
-          err[j] += (sum[j] - (s - x)) + (v[u][j] - x);
-          sum[j] = s;
+  const int kept = *pl.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b0 = blockIdx.x * kJoinChunks, c = (blockIdx.y * 32 + lane) * W;
+  if (threadIdx.x < kJoinChunks) {
+    const int b = b0 + threadIdx.x, next = (b + 1) * kChunk;   // a token that goes on reaches the chunk's end
+    int last = 0;
+    if (next < kept) {
+      const unsigned t = order[next - 1].x;
+      if (order[next].x == t && (b == 0 || order[b * kChunk - 1].x != t)) {
+        int lo = next, hi = kept;   // order[lo].x == t; order[hi].x > t or the end
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (order[mid].x == t) lo = mid; else hi = mid;
         }
+        last = lo / kChunk;
       }
+    }
+    s_last[threadIdx.x] = last;
   }
+  __syncthreads();
+  const bool in = c < pl.dim;
+  TT* table = static_cast<TT*>(a.d_table) + c;
+  // chunks [from, to) of those after b, whose sums are a chunk's first
+  auto add_chunks = [&](Sum<W>& sum, int from, int to) {
+    constexpr int U = W == 8 ? 4 : 8;
+    for (int k = from; k < to; k += U) {
+      float v[U][W];
 #pragma unroll
-  for (int j = 0; j < W; ++j) sum[j] += isfinite(err[j]) ? err[j] : 0.f;
-  put_sum<TT, W>(static_cast<TT*>(a.d_table) + (size_t)t * pl.dim + c, sum, a.scale, a.accumulate);
+      for (int u = 0; u < U; ++u)
+        if (k + u < to) load_row<W>(pl.part + (size_t)(k + u) * 2 * pl.dim + c, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k + u < to) sum.add(v[u]);
+    }
+  };
+  auto put = [&](const Sum<W>& sum, int b) {
+    float v[W];
+    sum.done(v);
+    put_sum<TT, W>(table + (size_t)order[(b + 1) * kChunk - 1].x * pl.dim, v, a.scale, a.accumulate);
+  };
+  int mine = 0;
+  for (int i = 0; i < kJoinChunks; ++i) {
+    const int b = b0 + i, last = s_last[i];
+    if (!last || last - b > kJoinAlone) continue;
+    if (mine++ % kJoinWarps != warp || !in) continue;
+    Sum<W> sum;
+    sum.zero();
+    float v[W];
+    load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, v);   // b's own: its last token's
+    sum.add(v);
+    add_chunks(sum, b + 1, last + 1);
+    put(sum, b);
+  }
+  for (int i = 0; i < kJoinChunks; ++i) {
+    const int b = b0 + i, last = s_last[i];
+    if (!last || last - b <= kJoinAlone) continue;
+    const int n = last - b, share = (n + kJoinWarps - 1) / kJoinWarps;
+    Sum<W> sum;
+    sum.zero();
+    if (in) {
+      if (warp == 0) {
+        float v[W];
+        load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, v);
+        sum.add(v);
+      }
+      add_chunks(sum, b + 1 + warp * share, min(last + 1, b + 1 + (warp + 1) * share));
+    }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && in) {
+      for (int w = 1; w < kJoinWarps; ++w) {
+        sum.add(s_sum[w][lane].s);
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum.e[j] += s_sum[w][lane].e[j];
+      }
+      put(sum, b);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- few tokens
+// One launch: each CTA puts the tokens in order itself (by counting those before each)
+// and takes words of 32 table rows x 32 * W columns: a warp sums a token's rows in
+// order, eight warps together those of more than kSmallAlone.
+constexpr int kSmall = 512, kSmallWarps = 8, kSmallAlone = 16;
+
+template <typename TO, typename TT, int W>
+__global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
+  griddep_wait();
+  griddep_trigger();
+  __shared__ uint32_t s_raw[kSmall], s_token[kSmall + 1];
+  __shared__ uint16_t s_pos[kSmall];
+  __shared__ Sum<W> s_sum[kSmallWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = pl.n;
+  for (int i = tid; i < n; i += 32 * kSmallWarps) s_raw[i] = min((unsigned)a.tokens[i], (unsigned)pl.vocab);
+  __syncthreads();
+  for (int i = tid; i < n; i += 32 * kSmallWarps) {
+    const uint32_t t = s_raw[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += s_raw[j] < t || (s_raw[j] == t && j < i);
+    s_token[rank] = t;
+    s_pos[rank] = (uint16_t)i;
+  }
+  if (tid == 0) s_token[n] = ~0u;
+  __syncthreads();
+  const int words = (pl.vocab + 31) / 32, tiles = (pl.dim + 32 * W - 1) / (32 * W);
+  const TO* d_out = static_cast<const TO*>(a.d_out);
+  for (long long item = blockIdx.x; item < (long long)words * tiles; item += gridDim.x) {
+    const int w = (int)(item / tiles), c = ((int)(item - (long long)w * tiles) * 32 + lane) * W;
+    const bool in = c < pl.dim;
+    TT* table = static_cast<TT*>(a.d_table) + c;
+    auto add_rows = [&](Sum<W>& sum, int from, int to) {
+      constexpr int U = W == 8 ? 4 : 8;
+      for (int k = from; k < to; k += U) {
+        float v[U][W];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k + u < to) load_row<W>(d_out + (int64_t)s_pos[k + u] * a.stride + c, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k + u < to) sum.add(v[u]);
+      }
+    };
+    // the first token that is at least v
+    auto find = [&](uint32_t v) {
+      int lo = 0, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_token[mid] >= v) hi = mid; else lo = mid + 1;
+      }
+      return lo;
+    };
+    int at = find(w * 32), end_word = find(min(w * 32 + 32, pl.vocab));
+    const int rows = min(32, pl.vocab - w * 32);
+    if (!a.accumulate) {   // rows without a token
+      uint32_t seen = 0;
+      for (int k = at; k < end_word; ++k) seen |= 1u << (s_token[k] & 31);
+      const float zero[W] = {};
+      if (in)
+        for (int v = warp; v < rows; v += kSmallWarps)
+          if (!(seen >> v & 1)) store_row<W>(table + (size_t)(w * 32 + v) * pl.dim, zero);
+    }
+    for (int turn = 0; at < end_word; ++turn) {
+      const uint32_t t = s_token[at];
+      const int end = find(t + 1);
+      float v[W];
+      Sum<W> sum;
+      sum.zero();
+      if (end - at <= kSmallAlone) {
+        if (turn % kSmallWarps == warp && in) {
+          add_rows(sum, at, end);
+          sum.done(v);
+          put_sum<TT, W>(table + (size_t)t * pl.dim, v, a.scale, a.accumulate);
+        }
+      } else {
+        const int share = (end - at + kSmallWarps - 1) / kSmallWarps;
+        if (in) add_rows(sum, at + warp * share, min(end, at + (warp + 1) * share));
+        s_sum[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && in) {
+          for (int x = 1; x < kSmallWarps; ++x) {
+            sum.add(s_sum[x][lane].s);
+#pragma unroll
+            for (int j = 0; j < W; ++j) sum.e[j] += s_sum[x][lane].e[j];
+          }
+          sum.done(v);
+          put_sum<TT, W>(table + (size_t)t * pl.dim, v, a.scale, a.accumulate);
+        }
+        __syncthreads();
+      }
+      at = end;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host side
 template <typename TT, typename TO, int W>
 cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
   const long long groups = (long long)a.n * (a.dim / W);
-  const unsigned grid = (unsigned)std::min<long long>((groups + 255) / 256, (long long)sms * 16);
+  const unsigned grid = (unsigned)std::min<long long>((groups + 256 * kLookups - 1) / (256 * kLookups), (long long)sms * 512);
   return launch_pdl(embed_kernel<TT, TO, W>, dim3(grid), dim3(256), 0, s, a);
 }
 template <typename TT, typename TO>
@@ -349,17 +544,43 @@ int passes_of(int vocab) {
   return (bits + kDigitBits - 1) / kDigitBits;
 }
 
+cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, cudaStream_t s) {
+  int ctas = 1;
+  while (ctas < kMaxCluster && ctas * 4096 < pl.n) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab));
+}
+
 template <typename TO, typename TT, int W>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
-  const int groups = pl.dim / W, threads = std::min(256, (groups + 31) / 32 * 32), tiles = (groups + threads - 1) / threads;
-  // rows to zero: enough CTAs beside the chunks' to fill the SMs a few times
-  const int zero = a.accumulate ? 0 : (int)std::min<long long>(pl.vocab, std::max(1, sms * 16 * (256 / threads) / tiles));
-  cudaError_t e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks + zero, tiles), dim3(threads), 0, s, pl, a);
+  const int groups = pl.dim / W, tiles32 = (groups + 31) / 32, words = (pl.vocab + 31) / 32;
+  if (pl.n <= kSmall) {
+    ++*launches;
+    return launch_pdl(embed_small_kernel<TO, TT, W>, dim3((unsigned)std::min<long long>((long long)words * tiles32, sms * 8)),
+                      dim3(32 * kSmallWarps), 0, s, pl, a);
+  }
+  cudaError_t e = sort(pl, a.tokens, s);
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (pl.chunks < 2) return cudaSuccess;   // no token goes on in another chunk
-  ++*launches;
-  return launch_pdl(embed_join_kernel<TT, W>, dim3(pl.chunks - 1, tiles), dim3(threads), 0, s, pl, a);
+  const int threads = std::min(256, tiles32 * 32), tiles = (groups + threads - 1) / threads;
+  // rows to zero: enough CTAs beside the chunks' to fill the SMs a few times
+  const int zero = a.accumulate ? 0 : std::min(words, std::max(1, sms * 16 * (256 / threads) / tiles));
+  e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks + zero, tiles), dim3(threads), 0, s, pl, a);
+  if (e != cudaSuccess) return e;
+  *launches += 2;
+  return launch_pdl(embed_join_kernel<TT, W>, dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, tiles32), dim3(32 * kJoinWarps), 0, s, pl, a);
 }
 template <typename TO, typename TT>
 cudaError_t sums_w(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
@@ -407,24 +628,6 @@ cudaError_t embed_launch(const EmbedArgs& a, bool table_f32, bool out_f32, int s
 cudaError_t embed_backward_launch(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, bool out_f32, bool table_f32, int sms,
                                   int* launches, cudaStream_t s) {
   *launches = 0;
-  int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 4096 < pl.n) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = kSortBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, a.tokens, passes_of(pl.vocab));
-  if (e != cudaSuccess) return e;
-  ++*launches;
   if (out_f32) return table_f32 ? sums_w<float, float>(pl, a, sms, launches, s) : sums_w<float, __nv_bfloat16>(pl, a, sms, launches, s);
   return table_f32 ? sums_w<__nv_bfloat16, float>(pl, a, sms, launches, s)
                    : sums_w<__nv_bfloat16, __nv_bfloat16>(pl, a, sms, launches, s);
