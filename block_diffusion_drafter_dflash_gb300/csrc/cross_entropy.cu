@@ -63,11 +63,11 @@ struct GemmCfg {
   static constexpr int kA = kBM * 128, kB = kOwnN * 128;   // bytes of a K block of 64
   static constexpr int kStage = PL * (kA + kB);
   static constexpr int kStages = PL == 1 ? 6 : 2;
-  static constexpr int kOut = PL == 1 ? kEpiWarps * 4096 : 0;   // rows staged on their way out, 32 x 64 a warp
+  static constexpr int kOut = kEpiWarps * 4096;            // rows staged on their way out, 32 x 64 a warp
   static constexpr int kAccCols = kBN;                     // tensor-memory columns of an accumulator
   static constexpr int kNC = kBN / 2;                      // columns of an epilogue thread
-  static constexpr int kSumBlocks = PL == 1 ? 8 : 1;       // K blocks that one sum of the tensor cores spans
-  static constexpr int kSmallSums = 8;                     // three planes: sums of the large product to one of the small ones
+  static constexpr int kSumBlocks = PL == 1 ? 8 : 2;       // K blocks that one sum of the tensor cores spans
+  static constexpr int kSmallSums = 4;                     // three planes: sums of the large product to one of the small ones
   static constexpr size_t kBytes = 1024 + (size_t)kStages * kStage + kOut + 256;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -157,6 +157,28 @@ __device__ __forceinline__ bool rows_vec(const T* p, int64_t stride) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * (int64_t)sizeof(T))) & 15) == 0;
 }
 
+// A piece of an fp32 head as three planes, zero behind its last row and column: the
+// share of CTA `cta` of `ctas` of 256 threads.
+__device__ __forceinline__ void split_weight(const CePlan& pl, const float* w, int v0, int cta, int ctas) {
+  const unsigned groups = pl.dim_pad / 8;
+  const size_t plane = (size_t)pl.piece * pl.dim_pad;
+  const unsigned n = (unsigned)pl.piece * groups;   // at most kPieceBytes / 48, or 256 * 8192
+  constexpr int U = 4;
+  for (unsigned i0 = cta * 256u + threadIdx.x; i0 < n; i0 += U * 256u * ctas) {
+    float v[U][8] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned i = i0 + u * 256u * ctas, r = i / groups, c = (i - r * groups) * 8;
+      if (i < n && v0 + (int)r < pl.vocab && (int)c < pl.dim) get8(w + (size_t)(v0 + r) * pl.dim + c, true, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned i = i0 + u * 256u * ctas;
+      if (i < n) put8<3>(pl.w + (size_t)i * 8, plane, v[u]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- rows that count
 // Kept rows in their order: where each came from, its target and statistics, and
 // its hidden state as planes.  Every CTA counts the kept rows before its own.
@@ -164,9 +186,13 @@ __device__ __forceinline__ bool rows_vec(const T* p, int64_t stride) {
 constexpr int kGatherThreads = 256;
 
 template <typename T, int PL, bool BWD>
-__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per) {
+__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per, int ctas) {
   griddep_wait();
   griddep_trigger();
+  if (PL == 3 && (int)blockIdx.x >= ctas) {   // the head's first piece
+    split_weight(pl, static_cast<const float*>(t.weight), 0, blockIdx.x - ctas, gridDim.x - ctas);
+    return;
+  }
   __shared__ int s_before, s_total, s_warp[kGatherThreads / 32], s_list[kGatherThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_before = s_total = 0;
@@ -227,10 +253,15 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
       if (to >= 0) {
         const T* src = hidden + (int64_t)(base + i) * t.row_stride;
         __nv_bfloat16* dst = pl.h + (size_t)to * pl.dim_pad;
-        for (int c = lane * 8; c < pl.dim_pad; c += 256) {
-          float v[8] = {};
-          if (c < pl.dim) get8(src + c, vec, v);
-          put8<PL>(dst + c, plane, v);
+        constexpr int U = PL == 1 ? 8 : 4;
+        for (int c0 = lane * 8; c0 < pl.dim_pad; c0 += 256 * U) {
+          float v[U][8] = {};
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c0 + u * 256 < pl.dim) get8(src + c0 + u * 256, vec, v[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c0 + u * 256 < pl.dim_pad) put8<PL>(dst + c0 + u * 256, plane, v[u]);
         }
       } else if (BWD && d_hidden) {
         T* dst = d_hidden + (int64_t)(base + i) * t.d_row_stride;
@@ -243,26 +274,16 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
   // the last tile's rows behind the kept ones
   constexpr int kTM = GemmCfg<PL>::kTM;
   const int end = min((total + kTM - 1) / kTM * kTM, pl.rows_pad);
-  for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += gridDim.x * (kGatherThreads / 32)) {
+  for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += ctas * (kGatherThreads / 32)) {
     __nv_bfloat16* dst = pl.h + (size_t)p * pl.dim_pad;
     for (int c = lane * 8; c < pl.dim_pad; c += 256) put8<PL>(dst + c, plane, zero);
   }
 }
 
-// A piece of an fp32 head as three planes, zero behind its last row and column.
 __global__ void __launch_bounds__(256) ce_split_weight_kernel(CePlan pl, const float* w, int v0) {
   griddep_wait();
   griddep_trigger();
-  const int groups = pl.dim_pad / 8;
-  const bool vec = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
-  const size_t plane = (size_t)pl.piece * pl.dim_pad;
-  const long long n = (long long)pl.piece * groups;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-    const int r = (int)(i / groups), c = (int)(i - (long long)r * groups) * 8;
-    float v[8] = {};
-    if (v0 + r < pl.vocab && c < pl.dim) get8(w + (size_t)(v0 + r) * pl.dim + c, vec, v);
-    put8<3>(pl.w + (size_t)r * pl.dim_pad + c, plane, v);
-  }
+  split_weight(pl, w, v0, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- tensor-core pieces
@@ -421,10 +442,11 @@ struct Items {
     parts = 1;
     if (USE == kHidden) {
       const int rest = whole % groups, all = pl.piece / 64;   // (the same cut for every piece)
-      float best = 1.f;
+      // in K blocks: the parts' waves, each with a start and an end worth 8, and their sums' way through memory
+      float best = all + 8.f;
       for (int p = 2; p <= kMaxParts && rest * p <= kTailWaves * groups && p * 4 <= all; ++p) {
-        const float waves = (float)((rest * p + groups - 1) / groups) / p + 0.02f * p;
-        if (rest && waves < best) best = waves, parts = p;
+        const float cost = ((rest * p + groups - 1) / groups) * ((float)all / p + 8.f) + 8.f * rest * p / groups;
+        if (rest && cost < best) best = cost, parts = p;
       }
       if (parts > 1) whole -= rest;
     }
@@ -706,13 +728,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           if (j == tgt) e -= 1.f;
           acc[j] = j < left ? gain * e : 0.f;
         }
-        if constexpr (PL == 1) {
 #pragma unroll
-          for (int j0 = 0; j0 < NC; j0 += 64) store_rows(&map_out, stage, lane, col + j0, m0 + 32 * (warp & 3), acc + j0);
-        } else {
-          __nv_bfloat16* out = pl.g + (size_t)row * pl.piece + col;
+        for (int p = 0; p < PL; ++p) {   // a plane, then what it leaves
 #pragma unroll
-          for (int j0 = 0; j0 < NC; j0 += 8) put8<PL>(out + j0, (size_t)pl.rows_pad * pl.piece, acc + j0);
+          for (int j0 = 0; j0 < NC; j0 += 64)
+            store_rows(&map_out, stage, lane, col + j0, p * pl.rows_pad + m0 + 32 * (warp & 3), acc + j0);
+          if (p + 1 < PL) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) acc[j] -= __bfloat162float(__float2bfloat16_rn(acc[j]));
+          }
         }
       } else if constexpr (USE == kHidden) {
         // whole tiles to their place, parts of a tile to a tile of their own; a piece
@@ -803,33 +827,43 @@ __global__ void __launch_bounds__(32 * kMergeWarps) ce_merge_kernel(CePlan pl, i
 
 // The hidden states' gradient to the caller's rows, the parts of a cut tile added in
 // order.
+constexpr int kFinishThreads = 256;
+
 template <typename T, int PL>
-__global__ void __launch_bounds__(256) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
+__global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
   griddep_wait();
   griddep_trigger();
   using C = GemmCfg<PL>;
-  const int kept = *pl.kept, groups = pl.dim / 8;
+  const int kept = *pl.kept;
   const Items<PL, kHidden> items(pl, pl.piece, kept, groups_of_ctas);
   const int rest = items.m_tiles * items.n_tiles - items.whole;
   const bool vec = rows_vec(d_hidden, stride);
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (long long)kept * groups; i += gridDim.x * 256LL) {
-    const int r = (int)(i / groups), c = (int)(i - (long long)r * groups) * 8;
-    const int tile = c / C::kBN * items.m_tiles + r / C::kTM;
-    float sum[8];
-    if (tile < items.whole) {
-      get8(pl.acc + (size_t)r * pl.dim_pad + c, true, sum);
-    } else {
-      const float* src = pl.tail + ((size_t)(tile - items.whole) * C::kTM + r % C::kTM) * C::kBN + c % C::kBN;
-      get8(src, true, sum);
-#pragma unroll 4
-      for (int p = 1; p < items.parts; ++p) {
-        float v[8];
-        get8(src + (size_t)p * rest * C::kTM * C::kBN, true, v);
+  const size_t step = (size_t)rest * C::kTM * C::kBN;
+  for (int r = blockIdx.x; r < kept; r += gridDim.x) {
+    T* out = d_hidden + pl.row_of[r] * stride;
+    for (int c = threadIdx.x * 8; c < pl.dim; c += kFinishThreads * 8) {
+      const int tile = c / C::kBN * items.m_tiles + r / C::kTM;
+      float sum[8];
+      if (tile < items.whole) {
+        get8(pl.acc + (size_t)r * pl.dim_pad + c, true, sum);
+      } else {
+        const float* src = pl.tail + ((size_t)(tile - items.whole) * C::kTM + r % C::kTM) * C::kBN + c % C::kBN;
+        get8(src, true, sum);
+        for (int p = 1; p < items.parts; p += 4) {
+          float v[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+          for (int u = 0; u < 4; ++u)
+            if (p + u < items.parts) get8(src + (p + u) * step, true, v[u]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (p + u < items.parts) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) sum[j] += v[u][j];
+            }
+        }
       }
+      set8(out + c, vec, sum);
     }
-    set8(d_hidden + pl.row_of[r] * stride + c, vec, sum);
   }
 }
 
@@ -885,12 +919,16 @@ Scale scale_of(float temperature) {
 
 // Rows a CTA of the first kernel takes: each counts all targets, so no more than 1,024 CTAs.
 int gather_rows(int rows) { return std::max(8, (rows + 1023) / 1024); }
+int split_ctas(const CePlan& pl, int sms) {
+  return (int)std::min<long long>(sms * 6, ((long long)pl.piece * (pl.dim_pad / 8) + 1023) / 1024);
+}
 
 template <typename T, int PL>
 cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   using C = GemmCfg<PL>;
-  const int per = gather_rows(pl.rows);
-  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3((pl.rows + per - 1) / per), dim3(kGatherThreads), 0, s, pl, t, per);
+  const int per = gather_rows(pl.rows), ctas = (pl.rows + per - 1) / per;
+  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
+                             pl, t, per, ctas);
   ++*launches;
   if (e != cudaSuccess) return e;
   CUtensorMap mh, mw;
@@ -906,8 +944,8 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
   for (int v0 = 0; v0 < pl.vocab; v0 += pl.piece) {
     a.v0 = v0;
     a.cols = std::min(pl.piece, pl.vocab - v0);
-    if (PL == 3) {
-      e = launch_pdl(ce_split_weight_kernel, dim3(sms * 8), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
+    if (PL == 3 && v0 > 0) {
+      e = launch_pdl(ce_split_weight_kernel, dim3(split_ctas(pl, sms)), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
       ++*launches;
       if (e != cudaSuccess) return e;
     }
@@ -922,8 +960,9 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
 template <typename T, int PL>
 cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   using C = GemmCfg<PL>;
-  const int per = gather_rows(pl.rows);
-  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3((pl.rows + per - 1) / per), dim3(kGatherThreads), 0, s, pl, t, per);
+  const int per = gather_rows(pl.rows), ctas = (pl.rows + per - 1) / per;
+  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
+                             pl, t, per, ctas);
   ++*launches;
   if (e != cudaSuccess) return e;
   // operands with the product's K along their rows (boxes of 64 x rows of the tile) or across them (64 x 64)
@@ -949,8 +988,8 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
     a.v0 = v0;
     a.cols = std::min(pl.piece, pl.vocab - v0);
     a.first = v0 == 0;
-    if (PL == 3) {
-      e = launch_pdl(ce_split_weight_kernel, dim3(sms * 8), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
+    if (PL == 3 && v0 > 0) {
+      e = launch_pdl(ce_split_weight_kernel, dim3(split_ctas(pl, sms)), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
       ++*launches;
       if (e != cudaSuccess) return e;
     }
@@ -960,9 +999,8 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
   }
   if (!t.d_hidden) return cudaSuccess;
   ++*launches;
-  const long long groups = (long long)pl.rows * (pl.dim / 8);
-  return launch_pdl(ce_finish_hidden_kernel<T, PL>, dim3((unsigned)std::min<long long>((groups + 255) / 256, sms * 8)), dim3(256), 0,
-                    s, pl, static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_grid(PL, sms) / C::kCtas);
+  return launch_pdl(ce_finish_hidden_kernel<T, PL>, dim3(std::min(pl.rows, sms * 8)), dim3(kFinishThreads), 0, s, pl,
+                    static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_grid(PL, sms) / C::kCtas);
 }
 
 }  // namespace

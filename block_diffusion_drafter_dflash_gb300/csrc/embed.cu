@@ -70,9 +70,8 @@ int width_of(const void* a, int64_t a_stride, int a_size, const void* b, int64_t
 }
 
 // ---------------------------------------------------------------- lookup
-constexpr int kLookups = 4;   // vectors of a thread, all loaded before the first is stored
-
-template <typename TT, typename TO, int W>
+// kLookups: vectors of a thread, all loaded before the first is stored.
+template <typename TT, typename TO, int W, int kLookups>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_wait();
   griddep_trigger();
@@ -116,6 +115,18 @@ constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMaxCluster = 8;
 constexpr int kBatch = 8;   // steps of 32 pairs that a warp loads together
 constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + 2);
+
+// The lanes that have this lane's digit (kBins: none), by a vote on each bit.
+__device__ __forceinline__ unsigned same_digit(unsigned d) {
+  unsigned same = 0xffffffffu;
+#pragma unroll
+  for (int b = 0; b <= kDigitBits; ++b) {
+    const bool on = d >> b & 1;
+    const unsigned votes = __ballot_sync(0xffffffffu, on);
+    same &= on ? votes : ~votes;
+  }
+  return same;
+}
 
 // One cluster.  Each warp owns a contiguous share of the pairs.  A pass counts its
 // digits, turns the counts into places (digits first, then CTAs, then warps, so equal
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
         if (i + u * 32 < end) {
           const bool in = i + u * 32 + lane < end;
           const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
-          const unsigned same = __match_any_sync(0xffffffffu, d);
+          const unsigned same = same_digit(d);
           if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
           __syncwarp();
         }
@@ -183,10 +194,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
     cluster.sync();
     uint32_t before = 0, all = 0, run = 0;
     if (tid < kBins) {
-      for (int c = 0; c < ctas; ++c) {
-        const uint32_t x = cluster.map_shared_rank(total, c)[tid];
-        before += c < cta ? x : 0;
-        all += x;
+      uint32_t x[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) x[c] = c < ctas ? cluster.map_shared_rank(total, c)[tid] : 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        before += c < cta ? x[c] : 0;
+        all += x[c];
       }
       run = all;   // inclusive scan over the digits
       for (int o = 1; o < 32; o <<= 1) {
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
         if (i + u * 32 < end) {
           const bool in = i + u * 32 + lane < end;
           const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
-          const unsigned same = __match_any_sync(0xffffffffu, d);
+          const unsigned same = same_digit(d);
           if (in) dst[place[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p[u];
           __syncwarp();
           if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
@@ -347,21 +361,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
   const uint2* order = pl.order;
   const int kept = *pl.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b0 = blockIdx.x * kJoinChunks, c = (blockIdx.y * 32 + lane) * W;
-  if (threadIdx.x < kJoinChunks) {
-    const int b = b0 + threadIdx.x, next = (b + 1) * kChunk;   // a token that goes on reaches the chunk's end
-    int last = 0;
+  {
+    // lane i: whether the last token of chunk b0 + i begins there and goes on
+    const int b = b0 + lane, next = (b + 1) * kChunk;   // a token that goes on reaches the chunk's end
+    unsigned t = 0;
+    bool goes_on = false;
     if (next < kept) {
-      const unsigned t = order[next - 1].x;
-      if (order[next].x == t && (b == 0 || order[b * kChunk - 1].x != t)) {
-        int lo = next, hi = kept;   // order[lo].x == t; order[hi].x > t or the end
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (order[mid].x == t) lo = mid; else hi = mid;
-        }
-        last = lo / kChunk;
-      }
+      t = order[next - 1].x;
+      const unsigned after = order[next].x, before = b > 0 ? order[b * kChunk - 1].x : ~0u;
+      goes_on = after == t && before != t;
     }
-    s_last[threadIdx.x] = last;
+    if (warp == 0) s_last[lane] = 0;
+    __syncthreads();
+    unsigned todo = __ballot_sync(0xffffffffu, goes_on);
+    const int chunks = (kept + kChunk - 1) / kChunk;
+    for (int k = 0; todo; ++k, todo &= todo - 1) {
+      if (k % kJoinWarps != warp) continue;
+      const int i = __ffs(todo) - 1;
+      const unsigned token = __shfl_sync(0xffffffffu, t, i);
+      // chunk lo begins with the token, chunk hi does not: 32 chunks between them at a time
+      int lo = b0 + i + 1, hi = chunks;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 32) / 33, at = lo + step * (lane + 1);
+        const bool same = at < hi && order[(size_t)at * kChunk].x == token;
+        const int n = __popc(__ballot_sync(0xffffffffu, same));
+        hi = min(hi, lo + step * (n + 1));
+        lo += step * n;
+      }
+      if (lane == 0) s_last[i] = lo;
+    }
   }
   __syncthreads();
   const bool in = c < pl.dim;
@@ -525,8 +553,13 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
 template <typename TT, typename TO, int W>
 cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
   const long long groups = (long long)a.n * (a.dim / W);
-  const unsigned grid = (unsigned)std::min<long long>((groups + 256 * kLookups - 1) / (256 * kLookups), (long long)sms * 512);
-  return launch_pdl(embed_kernel<TT, TO, W>, dim3(grid), dim3(256), 0, s, a);
+  // few rows: a thread a vector, so that the latency is one chain of loads; many: more
+  // loads in flight than CTAs could start
+  const bool few = groups <= (long long)sms * 2048;
+  const long long per = 256 * (few ? 1 : 8);
+  const unsigned grid = (unsigned)std::min<long long>((groups + per - 1) / per, (long long)sms * 512);
+  return few ? launch_pdl(embed_kernel<TT, TO, W, 1>, dim3(grid), dim3(256), 0, s, a)
+             : launch_pdl(embed_kernel<TT, TO, W, 8>, dim3(grid), dim3(256), 0, s, a);
 }
 template <typename TT, typename TO>
 cudaError_t lookup_w(const EmbedArgs& a, int sms, cudaStream_t s) {
