@@ -55,14 +55,15 @@ constexpr size_t kPieceBytes = size_t(192) << 20;
 
 enum Use { kStats, kGrad, kHidden, kWeight };
 
-template <int PL>
+// PL planes; G CTAs share a tile.
+template <int PL, int G>
 struct GemmCfg {
-  static constexpr int kCtas = PL == 1 ? 2 : 1;            // CTAs that share a tile
+  static constexpr int kCtas = G;
   static constexpr int kTM = kBM * kCtas, kBN = PL == 1 ? 256 : 128;   // the tile
   static constexpr int kOwnN = kBN / kCtas;                // rows of the second operand that a CTA holds
   static constexpr int kA = kBM * 128, kB = kOwnN * 128;   // bytes of a K block of 64
   static constexpr int kStage = PL * (kA + kB);
-  static constexpr int kStages = PL == 1 ? 6 : 2;
+  static constexpr int kStages = PL == 3 ? 2 : G == 2 ? 6 : 4;
   static constexpr int kOut = kEpiWarps * 4096;            // rows staged on their way out, 32 x 64 a warp
   static constexpr int kAccCols = kBN;                     // tensor-memory columns of an accumulator
   static constexpr int kNC = kBN / 2;                      // columns of an epilogue thread
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_before = s_total = 0;
   __syncthreads();
-  const int r0 = blockIdx.x * per, r1 = min(r0 + per, pl.rows);
+  const int r0 = min((int)blockIdx.x * per, pl.rows), r1 = min(r0 + per, pl.rows);
   auto inside = [&](int r) { return (unsigned)t.targets[r] < (unsigned)pl.vocab; };
   int before = 0, total = 0;
   for (int r = tid; r < pl.rows; r += kGatherThreads) {
@@ -272,8 +273,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
     __syncthreads();
   }
   // the last tile's rows behind the kept ones
-  constexpr int kTM = GemmCfg<PL>::kTM;
-  const int end = min((total + kTM - 1) / kTM * kTM, pl.rows_pad);
+  const int end = min((total + pl.tile - 1) / pl.tile * pl.tile, pl.rows_pad);
   for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += ctas * (kGatherThreads / 32)) {
     __nv_bfloat16* dst = pl.h + (size_t)p * pl.dim_pad;
     for (int c = lane * 8; c < pl.dim_pad; c += 256) put8<PL>(dst + c, plane, zero);
@@ -423,9 +423,9 @@ __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, fl
 // fill the last wave of CTAs are cut along K into as many parts as make that wave
 // shortest; each part has its sums in memory of its own, and they are added in order
 // at the end.
-template <int PL, int USE>
+template <int PL, int G, int USE>
 struct Items {
-  using C = GemmCfg<PL>;
+  using C = GemmCfg<PL, G>;
   int m_tiles, n_tiles, blocks;
   int whole, parts;   // tiles that are not cut; parts of each of the others
   __device__ __forceinline__ Items(const CePlan& pl, int cols, int kept, int groups) {
@@ -491,13 +491,13 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* map, uint8_t* stag
   if (lane == 0) tma_store(map, stage, x, y);
 }
 
-template <int PL, int USE>
+template <int PL, int G, int USE>
 __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                   const __grid_constant__ CUtensorMap map_b,
                                                                   const __grid_constant__ CUtensorMap map_out,
                                                                   const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<PL>;
-  constexpr int S = C::kStages, G = C::kCtas;
+  using C = GemmCfg<PL, G>;
+  constexpr int S = C::kStages;
   constexpr bool kAMN = USE == kWeight, kBMN = USE == kWeight || USE == kHidden;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   griddep_wait();
   griddep_trigger();
   const int kept = *pl.kept;
-  const Items<PL, USE> items(pl, a.cols, kept, groups);
+  const Items<PL, G, USE> items(pl, a.cols, kept, groups);
   const int n_items = items.count();
 
   if (warp == 0) {
@@ -784,44 +784,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
 // ---------------------------------------------------------------- ends
 // A row's pairs merged: lse = ln2 (M + log2 S), and the loss from the difference of
 // the exponents, which is exact where the target has the largest.
-constexpr int kMergeWarps = 16;
+// A CTA takes ROWS rows, its threads a share of the pairs each: 32 rows' pairs lie in
+// 256 bytes, but few rows need more CTAs.
+constexpr int kMergeThreads = 512;
 
-__global__ void __launch_bounds__(32 * kMergeWarps) ce_merge_kernel(CePlan pl, int parts, float* loss, float* lse) {
+template <int ROWS>
+__global__ void __launch_bounds__(kMergeThreads) ce_merge_kernel(CePlan pl, int parts, float* loss, float* lse) {
   griddep_wait();
   griddep_trigger();
-  __shared__ float2 sh[kMergeWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kept = *pl.kept;
-  for (int r0 = blockIdx.x * 32; r0 < kept; r0 += gridDim.x * 32) {
-    const int r = r0 + lane;
-    float m = -INFINITY, s = 0.f;
-    auto add = [&](float2 v) {
-      const float nm = fmaxf(m, v.x), ref = nm == -INFINITY ? 0.f : nm;
-      s = s * ex2(m - ref) + v.y * ex2(v.x - ref);
-      m = nm;
-    };
-    if (r < kept) {
-      int p = warp;
-      for (; p + 3 * kMergeWarps < parts; p += 4 * kMergeWarps) {
-        float2 v[4];
+  constexpr int kWarps = kMergeThreads / 32, kStep = kMergeThreads / ROWS, U = 4;
+  __shared__ float2 sh[kWarps][ROWS];
+  const int tid = threadIdx.x, warp = tid >> 5, r0 = blockIdx.x * ROWS, r = r0 + tid % ROWS, kept = *pl.kept;
+  if (r0 >= kept) return;
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](float2 v) {
+    const float nm = fmaxf(m, v.x), ref = nm == -INFINITY ? 0.f : nm;
+    s = s * ex2(m - ref) + v.y * ex2(v.x - ref);
+    m = nm;
+  };
+  if (r < kept)
+    for (int p = tid / ROWS; p < parts; p += U * kStep) {
+      float2 v[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = pl.part[(size_t)(p + u * kMergeWarps) * pl.rows_pad + r];
+      for (int u = 0; u < U; ++u) v[u] = p + u * kStep < parts ? pl.part[(size_t)(p + u * kStep) * pl.rows_pad + r] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add(v[u]);
-      }
-      for (; p < parts; p += kMergeWarps) add(pl.part[(size_t)p * pl.rows_pad + r]);
+      for (int u = 0; u < U; ++u) add(v[u]);
     }
-    __syncthreads();
-    sh[warp][lane] = make_float2(m, s);
-    __syncthreads();
-    if (warp == 0 && r < kept) {
-      m = -INFINITY;
-      s = 0.f;
-      for (int w = 0; w < kMergeWarps; ++w) add(sh[w][lane]);
-      const float l2 = log2f(s);
-      const int to = pl.row_of[r];
-      lse[to] = kLn2 * (m + l2);
-      loss[to] = kLn2 * ((m - pl.picked[r]) + l2);
-    }
+#pragma unroll
+  for (int o = ROWS; o < 32; o *= 2) {   // the warp's shares of a row
+    const float2 v = make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    add(v);
+  }
+  if ((tid & 31) < ROWS) sh[warp][tid & 31] = make_float2(m, s);
+  __syncthreads();
+  if (tid < ROWS && r < kept) {
+    for (int w = 1; w < kWarps; ++w) add(sh[w][tid]);
+    const float l2 = log2f(s);
+    const int to = pl.row_of[r];
+    lse[to] = kLn2 * (m + l2);
+    loss[to] = kLn2 * ((m - pl.picked[r]) + l2);
   }
 }
 
@@ -829,13 +830,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) ce_merge_kernel(CePlan pl, i
 // order.
 constexpr int kFinishThreads = 256;
 
-template <typename T, int PL>
+template <typename T, int PL, int G>
 __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
   griddep_wait();
   griddep_trigger();
-  using C = GemmCfg<PL>;
+  using C = GemmCfg<PL, G>;
   const int kept = *pl.kept;
-  const Items<PL, kHidden> items(pl, pl.piece, kept, groups_of_ctas);
+  const Items<PL, G, kHidden> items(pl, pl.piece, kept, groups_of_ctas);
   const int rest = items.m_tiles * items.n_tiles - items.whole;
   const bool vec = rows_vec(d_hidden, stride);
   const size_t step = (size_t)rest * C::kTM * C::kBN;
@@ -868,31 +869,32 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan
 }
 
 // ---------------------------------------------------------------- host side
-template <int PL>
+template <int PL, int G>
 cudaError_t prepare() {
-  for (auto kernel : {ce_gemm_kernel<PL, kStats>, ce_gemm_kernel<PL, kGrad>, ce_gemm_kernel<PL, kHidden>, ce_gemm_kernel<PL, kWeight>}) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmCfg<PL>::kBytes);
+  for (auto kernel : {ce_gemm_kernel<PL, G, kStats>, ce_gemm_kernel<PL, G, kGrad>, ce_gemm_kernel<PL, G, kHidden>,
+                      ce_gemm_kernel<PL, G, kWeight>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmCfg<PL, G>::kBytes);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-int gemm_grid(int planes, int sms) { return planes == 1 ? std::max(2, sms / 2 * 2) : sms; }
+int gemm_groups(int ctas, int sms) { return std::max(1, sms / ctas); }
 
-template <int PL, int USE>
+template <int PL, int G, int USE>
 cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, int sms, int* launches,
                  cudaStream_t s) {
   ++*launches;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(gemm_grid(PL, sms));
+  cfg.gridDim = dim3(G * gemm_groups(G, sms));
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = GemmCfg<PL>::kBytes;
+  cfg.dynamicSmemBytes = GemmCfg<PL, G>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (GemmCfg<PL>::kCtas > 1) {
+  if (G > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = GemmCfg<PL>::kCtas;
+    attr[n].val.clusterDim.x = G;
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
@@ -903,7 +905,7 @@ cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<PL, USE>, ma, mb, mo, a);
+  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<PL, G, USE>, ma, mb, mo, a);
 }
 
 struct Scale {
@@ -919,14 +921,16 @@ Scale scale_of(float temperature) {
 
 // Rows a CTA of the first kernel takes: each counts all targets, so no more than 1,024 CTAs.
 int gather_rows(int rows) { return std::max(8, (rows + 1023) / 1024); }
+// (and at least as many as fill a tile's padding a row a warp)
+constexpr int kTilePad = 2 * kBM / (kGatherThreads / 32);
 int split_ctas(const CePlan& pl, int sms) {
   return (int)std::min<long long>(sms * 6, ((long long)pl.piece * (pl.dim_pad / 8) + 1023) / 1024);
 }
 
-template <typename T, int PL>
+template <typename T, int PL, int G>
 cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
-  using C = GemmCfg<PL>;
-  const int per = gather_rows(pl.rows), ctas = (pl.rows + per - 1) / per;
+  using C = GemmCfg<PL, G>;
+  const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
                              pl, t, per, ctas);
   ++*launches;
@@ -949,18 +953,20 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    e = gemm<PL, kStats>(a, mh, mw, mw, sms, launches, s);
+    e = gemm<PL, G, kStats>(a, mh, mw, mw, sms, launches, s);
     if (e != cudaSuccess) return e;
     a.part0 += 2 * ((a.cols + C::kBN - 1) / C::kBN);
   }
   ++*launches;
-  return launch_pdl(ce_merge_kernel, dim3((pl.rows + 31) / 32), dim3(32 * kMergeWarps), 0, s, pl, a.part0, t.loss, t.lse);
+  const bool few = pl.rows <= 4 * sms;
+  return launch_pdl(few ? ce_merge_kernel<4> : ce_merge_kernel<32>, dim3(few ? (pl.rows + 3) / 4 : (pl.rows + 31) / 32),
+                    dim3(kMergeThreads), 0, s, pl, a.part0, t.loss, t.lse);
 }
 
-template <typename T, int PL>
+template <typename T, int PL, int G>
 cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
-  using C = GemmCfg<PL>;
-  const int per = gather_rows(pl.rows), ctas = (pl.rows + per - 1) / per;
+  using C = GemmCfg<PL, G>;
+  const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
                              pl, t, per, ctas);
   ++*launches;
@@ -993,14 +999,14 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    if ((e = gemm<PL, kGrad>(a, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_hidden && (e = gemm<PL, kHidden>(a, g_k, w_mn, g_out, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_weight && (e = gemm<PL, kWeight>(a, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
+    if ((e = gemm<PL, G, kGrad>(a, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (t.d_hidden && (e = gemm<PL, G, kHidden>(a, g_k, w_mn, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (t.d_weight && (e = gemm<PL, G, kWeight>(a, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
   }
   if (!t.d_hidden) return cudaSuccess;
   ++*launches;
-  return launch_pdl(ce_finish_hidden_kernel<T, PL>, dim3(std::min(pl.rows, sms * 8)), dim3(kFinishThreads), 0, s, pl,
-                    static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_grid(PL, sms) / C::kCtas);
+  return launch_pdl(ce_finish_hidden_kernel<T, PL, G>, dim3(std::min(pl.rows, sms * 64)), dim3(kFinishThreads), 0, s, pl,
+                    static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_groups(G, sms));
 }
 
 }  // namespace
@@ -1011,10 +1017,14 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.dim = dim;
   pl.vocab = vocab;
   pl.planes = f32 ? 3 : 1;
-  const int tm = f32 ? GemmCfg<3>::kTM : GemmCfg<1>::kTM;
-  pl.rows_pad = (rows + tm - 1) / tm * tm;
+  // a pair of CTAs shares 256 rows, unless there is one CTA's worth of them (then the
+  // second would only hold up half the loads: 15 rows of 4,096 against 151,936 in 238 us,
+  // alone 2xx)
+  pl.ctas = f32 || rows <= kBM || sms < 2 ? 1 : 2;
+  pl.tile = kBM * pl.ctas;
+  pl.rows_pad = (rows + pl.tile - 1) / pl.tile * pl.tile;
   pl.dim_pad = (dim + 63) / 64 * 64;
-  const int bn = f32 ? GemmCfg<3>::kBN : GemmCfg<1>::kBN;
+  const int bn = f32 ? GemmCfg<3, 1>::kBN : GemmCfg<1, 1>::kBN;
   // pieces of equal size, as few as the limit allows
   const size_t column = 2 * (size_t)pl.planes * (backward ? std::max(pl.rows_pad, f32 ? pl.dim_pad : 0) : pl.dim_pad);
   const long long limit = std::max<long long>(256, (long long)(kPieceBytes / column) / 256 * 256);
@@ -1057,17 +1067,22 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   return pl;
 }
 
-cudaError_t ce_prepare_f32() { return prepare<3>(); }
-cudaError_t ce_prepare_bf16() { return prepare<1>(); }
+cudaError_t ce_prepare_f32() { return prepare<3, 1>(); }
+cudaError_t ce_prepare_bf16() {
+  const cudaError_t e = prepare<1, 1>();
+  return e == cudaSuccess ? prepare<1, 2>() : e;
+}
 
 cudaError_t ce_forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   *launches = 0;
-  return pl.planes == 3 ? forward<float, 3>(pl, t, sms, launches, s) : forward<__nv_bfloat16, 1>(pl, t, sms, launches, s);
+  if (pl.planes == 3) return forward<float, 3, 1>(pl, t, sms, launches, s);
+  return pl.ctas == 2 ? forward<__nv_bfloat16, 1, 2>(pl, t, sms, launches, s) : forward<__nv_bfloat16, 1, 1>(pl, t, sms, launches, s);
 }
 
 cudaError_t ce_backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   *launches = 0;
-  return pl.planes == 3 ? backward<float, 3>(pl, t, sms, launches, s) : backward<__nv_bfloat16, 1>(pl, t, sms, launches, s);
+  if (pl.planes == 3) return backward<float, 3, 1>(pl, t, sms, launches, s);
+  return pl.ctas == 2 ? backward<__nv_bfloat16, 1, 2>(pl, t, sms, launches, s) : backward<__nv_bfloat16, 1, 1>(pl, t, sms, launches, s);
 }
 
 }  // namespace dflash

@@ -8,13 +8,14 @@
 // The gradient.  In a block drafter's training one token, the mask, collects nearly
 // all rows, so rows of the table are no unit of work.  One cluster sorts the
 // (token, position) pairs by token, positions ascending (a stable radix sort, two
-// passes for vocabularies up to 2^18), and marks the tokens that occur.  Then every
+// passes for vocabularies up to 2^18), while the other CTAs zero the gradient (rows with
+// a token are written again, which costs less than the sort would by itself).  Then every
 // chunk of kEmbedChunk sorted tokens is summed by CTAs of its own: tokens that lie
 // inside the chunk go straight to the table's gradient; the sums of a first or last
 // token that goes on in another chunk go to memory, and a last kernel adds them in
-// order.  Rows without a token are zeroed beside the sums.  No float atomics: the
-// same call gives the same bits.  Sums are fp32, at most kEmbedChunk terms, and the
-// chunks' sums are added with their rounding errors carried along.
+// order.  No float atomics: the same call gives the same bits.  Sums are fp32, at most
+// kEmbedChunk terms, and the chunks' sums are added with their rounding errors carried
+// along.  Few tokens take one launch.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -45,7 +46,8 @@ __device__ __forceinline__ void load_row(const T* p, float* v) {
     for (int j = 0; j < P; ++j) v[k + j] = to_f32<T>(x.v[j]);
   }
 }
-template <int W, typename T>
+// STREAM: what is written is not read again soon.
+template <int W, bool STREAM = false, typename T>
 __device__ __forceinline__ void store_row(T* p, const float* v) {
   constexpr int P = W * sizeof(T) > 16 ? 16 / sizeof(T) : W;
 #pragma unroll
@@ -53,7 +55,8 @@ __device__ __forceinline__ void store_row(T* p, const float* v) {
     Vec<T, P> x;
 #pragma unroll
     for (int j = 0; j < P; ++j) x.v[j] = from_f32<T>(v[k + j]);
-    *reinterpret_cast<Vec<T, P>*>(p + k) = x;
+    if constexpr (STREAM && P * sizeof(T) == 16) __stcs(reinterpret_cast<uint4*>(p + k), *reinterpret_cast<const uint4*>(&x));
+    else *reinterpret_cast<Vec<T, P>*>(p + k) = x;
   }
 }
 // The widest vector (8, 4, 2 or 1 values, at most 16 bytes of the wider type, so that a
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
       if (to[u]) {
 #pragma unroll
         for (int j = 0; j < W; ++j) v[u][j] *= a.scale;
-        store_row<W>(to[u], v[u]);
+        store_row<W, (kLookups > 1)>(to[u], v[u]);   // (without: 134 MB of output at 27 us instead of 22.5)
       }
   }
 }
@@ -114,7 +117,7 @@ constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMaxCluster = 8;
 constexpr int kBatch = 8;   // steps of 32 pairs that a warp loads together
-constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + 2);
+constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + kMaxCluster + 1);
 
 // The lanes that have this lane's digit (kBins: none), by a vote on each bit.
 __device__ __forceinline__ unsigned same_digit(unsigned d) {
@@ -128,26 +131,44 @@ __device__ __forceinline__ unsigned same_digit(unsigned d) {
   return same;
 }
 
-// One cluster.  Each warp owns a contiguous share of the pairs.  A pass counts its
+// The share of CTA `cta` of `ctas` in zeroing a table's gradient.
+__device__ void zero_fill(void* table, size_t bytes, int cta, int ctas) {
+  char* p = static_cast<char*>(table);
+  const size_t head = min(bytes, (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), vecs = (bytes - head) / 16;
+  uint4* v = reinterpret_cast<uint4*>(p + head);
+  const size_t step = (size_t)ctas * kSortThreads;
+  for (size_t i = (size_t)cta * kSortThreads + threadIdx.x; i < vecs; i += step) __stcs(v + i, make_uint4(0, 0, 0, 0));
+  if (cta == 0) {   // the ends, in the two bytes of the smaller type
+    if (threadIdx.x < head / 2) reinterpret_cast<uint16_t*>(p)[threadIdx.x] = 0;
+    const size_t tail = head + vecs * 16;
+    if (threadIdx.x < (bytes - tail) / 2) reinterpret_cast<uint16_t*>(p + tail)[threadIdx.x] = 0;
+  }
+}
+
+// The first cluster sorts, the others zero the gradient.  Each warp owns a contiguous share of the pairs.  A pass counts its
 // digits, turns the counts into places (digits first, then CTAs, then warps, so equal
 // digits keep their order) and moves the pairs.  Tokens outside the vocabulary sort
 // behind all others.
-__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPlan pl, const int32_t* tokens, int passes) {
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPlan pl, const int32_t* tokens, int passes, void* table,
+                                                                         size_t zero_bytes) {
   griddep_wait();
   griddep_trigger();
   cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+  if ((int)blockIdx.x >= ctas) {
+    zero_fill(table, zero_bytes, blockIdx.x - ctas, gridDim.x - ctas);
+    return;
+  }
   extern __shared__ uint32_t sh[];
   uint32_t* count = sh;                          // [warps][bins]
-  uint32_t* total = sh + kBins * kSortWarps;     // [bins] of this CTA
-  uint32_t* place = total + kBins;               // [bins] first place of the CTA's pairs
+  uint32_t* total = sh + kBins * kSortWarps;     // [CTAs][bins] of every CTA
+  uint32_t* place = total + kBins * kMaxCluster; // [bins] first place of the CTA's pairs
   __shared__ uint32_t s_scan[kBins / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ctas = cluster.num_blocks(), cta = cluster.block_rank();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // all CTAs run before any is written to
   const long long all_warps = (long long)ctas * kSortWarps, me = (long long)cta * kSortWarps + warp;
   const int share = (int)(((pl.n + all_warps - 1) / all_warps + 31) / 32 * 32);
   const int beg = (int)min((long long)pl.n, me * share), end = (int)min((long long)pl.n, (me + 1) * share);
-  const int words = (pl.vocab + 31) / 32;
-  for (int i = cta * kSortThreads + tid; i < words; i += ctas * kSortThreads) pl.seen[i] = 0;
   if (cta == 0 && tid == 0) *pl.kept = 0;
   for (int pass = 0; pass < passes; ++pass) {
     const bool last_odd = (passes - pass) & 1;   // the last pass writes `order`
@@ -181,6 +202,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
         }
     }
     __syncthreads();
+    if (pass == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (tid < kBins) {
       uint32_t sum = 0;
 #pragma unroll 8
@@ -189,18 +211,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
         count[w * kBins + tid] = sum;
         sum += c;
       }
-      total[tid] = sum;
+      for (int c = 0; c < ctas; ++c) cluster.map_shared_rank(total, c)[cta * kBins + tid] = sum;
     }
     cluster.sync();
     uint32_t before = 0, all = 0, run = 0;
     if (tid < kBins) {
-      uint32_t x[kMaxCluster];
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) x[c] = c < ctas ? cluster.map_shared_rank(total, c)[tid] : 0;
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) {
-        before += c < cta ? x[c] : 0;
-        all += x[c];
+      for (int c = 0; c < ctas; ++c) {
+        const uint32_t x = total[c * kBins + tid];
+        before += c < cta ? x : 0;
+        all += x;
       }
       run = all;   // inclusive scan over the digits
       for (int o = 1; o < 32; o <<= 1) {
@@ -232,13 +251,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
     cluster.sync();   // the pairs are where the next pass reads them, and `total` may change
   }
   const uint2* got = pl.order;
-  for (int i = beg + lane; i < end; i += 32) {
-    const unsigned t = got[i].x;
-    if (t < (unsigned)pl.vocab) {
-      if (i == 0 || got[i - 1].x != t) atomicOr(&pl.seen[t >> 5], 1u << (t & 31));
-      if (i == pl.n - 1 || got[i + 1].x >= (unsigned)pl.vocab) *pl.kept = i + 1;
-    }
-  }
+  for (int i = beg + lane; i < end; i += 32)
+    if (got[i].x < (unsigned)pl.vocab && (i == pl.n - 1 || got[i + 1].x >= (unsigned)pl.vocab)) *pl.kept = i + 1;
 }
 
 // ---------------------------------------------------------------- sums
@@ -257,33 +271,13 @@ __device__ __forceinline__ void put_sum(TT* p, const float* sum, float scale, in
   store_row<W>(p, v);
 }
 
-// First `chunks` blocks of the grid's x: a chunk's sums over blockDim.x * W columns.
-// The others, unless the gradient is added to what is there: rows without a token, 32
-// at a time (one word of `seen`), all their stores independent.
+// A chunk's sums over blockDim.x * W columns.
 template <typename TO, typename TT, int W>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
   TT* table = static_cast<TT*>(a.d_table);
-  if ((int)blockIdx.x >= pl.chunks) {
-    if (c >= pl.dim) return;
-    const float zero[W] = {};
-    const int words = (pl.vocab + 31) / 32;
-    for (int w = blockIdx.x - pl.chunks; w < words; w += gridDim.x - pl.chunks) {
-      const uint32_t seen = pl.seen[w];
-      const int n = min(32, pl.vocab - w * 32);
-      TT* row = table + (size_t)w * 32 * pl.dim + c;
-      if (seen == 0 && n == 32) {
-#pragma unroll 8
-        for (int v = 0; v < 32; ++v) store_row<W>(row + (size_t)v * pl.dim, zero);
-      } else {
-        for (int v = 0; v < n; ++v)
-          if (!(seen >> v & 1)) store_row<W>(row + (size_t)v * pl.dim, zero);
-      }
-    }
-    return;
-  }
   __shared__ uint2 s_pair[kChunk];
   const uint2* order = pl.order;
   const int kept = *pl.kept, i0 = blockIdx.x * kChunk, n = min(kChunk, kept - i0);
@@ -328,7 +322,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
 // each addition rounds off summed beside them.  A CTA looks at the ends of kJoinChunks
 // chunks, over 32 * W columns.  A token of few chunks is one warp's; those of more are
 // taken by all warps together, a run of chunks each.
-constexpr int kJoinWarps = 8, kJoinChunks = 32, kJoinAlone = 12;
+constexpr int kJoinWarps = 8, kJoinChunks = 8, kJoinAlone = 12;
 
 template <int W>
 struct Sum {
@@ -366,12 +360,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
     const int b = b0 + lane, next = (b + 1) * kChunk;   // a token that goes on reaches the chunk's end
     unsigned t = 0;
     bool goes_on = false;
-    if (next < kept) {
+    if (lane < kJoinChunks && next < kept) {
       t = order[next - 1].x;
       const unsigned after = order[next].x, before = b > 0 ? order[b * kChunk - 1].x : ~0u;
       goes_on = after == t && before != t;
     }
-    if (warp == 0) s_last[lane] = 0;
+    if (warp == 0 && lane < kJoinChunks) s_last[lane] = 0;
     __syncthreads();
     unsigned todo = __ballot_sync(0xffffffffu, goes_on);
     const int chunks = (kept + kChunk - 1) / kChunk;
@@ -556,10 +550,10 @@ cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
   // few rows: a thread a vector, so that the latency is one chain of loads; many: more
   // loads in flight than CTAs could start
   const bool few = groups <= (long long)sms * 2048;
-  const long long per = 256 * (few ? 1 : 8);
+  const long long per = 256 * (few ? 1 : 4);
   const unsigned grid = (unsigned)std::min<long long>((groups + per - 1) / per, (long long)sms * 512);
   return few ? launch_pdl(embed_kernel<TT, TO, W, 1>, dim3(grid), dim3(256), 0, s, a)
-             : launch_pdl(embed_kernel<TT, TO, W, 8>, dim3(grid), dim3(256), 0, s, a);
+             : launch_pdl(embed_kernel<TT, TO, W, 4>, dim3(grid), dim3(256), 0, s, a);
 }
 template <typename TT, typename TO>
 cudaError_t lookup_w(const EmbedArgs& a, int sms, cudaStream_t s) {
@@ -577,11 +571,13 @@ int passes_of(int vocab) {
   return (bits + kDigitBits - 1) / kDigitBits;
 }
 
-cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, cudaStream_t s) {
+cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, size_t zero_bytes, int sms, cudaStream_t s) {
   int ctas = 1;
   while (ctas < kMaxCluster && ctas * 4096 < pl.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  // CTAs that zero: two an SM, fewer for a small table
+  const long long zero = std::min<long long>(2 * sms, (long long)((zero_bytes + 65535) / 65536));
+  cfg.gridDim = dim3((unsigned)(ctas + (zero + ctas - 1) / ctas * ctas));
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = kSortBytes;
   cfg.stream = s;
@@ -593,7 +589,7 @@ cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, cudaStream_t s) 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab));
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab), table, zero_bytes);
 }
 
 template <typename TO, typename TT, int W>
@@ -604,13 +600,11 @@ cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* la
     return launch_pdl(embed_small_kernel<TO, TT, W>, dim3((unsigned)std::min<long long>((long long)words * tiles32, sms * 8)),
                       dim3(32 * kSmallWarps), 0, s, pl, a);
   }
-  cudaError_t e = sort(pl, a.tokens, s);
+  cudaError_t e = sort(pl, a.tokens, a.d_table, a.accumulate ? 0 : sizeof(TT) * (size_t)pl.vocab * pl.dim, sms, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   const int threads = std::min(256, tiles32 * 32), tiles = (groups + threads - 1) / threads;
-  // rows to zero: enough CTAs beside the chunks' to fill the SMs a few times
-  const int zero = a.accumulate ? 0 : std::min(words, std::max(1, sms * 16 * (256 / threads) / tiles));
-  e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks + zero, tiles), dim3(threads), 0, s, pl, a);
+  e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
   if (e != cudaSuccess) return e;
   *launches += 2;
   return launch_pdl(embed_join_kernel<TT, W>, dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, tiles32), dim3(32 * kJoinWarps), 0, s, pl, a);
@@ -643,7 +637,6 @@ EmbedBwdPlan embed_bwd_plan(void* ws, int n, int dim, int vocab) {
   pl.kept = reinterpret_cast<int32_t*>(take(256));
   pl.order = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
   pl.spare = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
-  pl.seen = reinterpret_cast<uint32_t*>(take(4 * (((size_t)vocab + 31) / 32)));
   pl.part = reinterpret_cast<float*>(take(sizeof(float) * 2 * (size_t)pl.chunks * dim));
   pl.bytes = off;
   return pl;

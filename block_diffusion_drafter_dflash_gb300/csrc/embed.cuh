@@ -24,7 +24,6 @@ struct EmbedBwdPlan {
   int32_t* kept;            // tokens inside the vocabulary
   uint2* order;             // [n] (token, position), sorted
   uint2* spare;             // [n] between the passes
-  uint32_t* seen;           // [vocab bits] tokens that occur
   float* part;              // [chunks][2][dim] sums of a chunk's first and last token where they go on outside
   size_t bytes;
 };
