@@ -50,7 +50,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
 constexpr long long kBudget = 400000000LL;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxParts = 32, kTailWaves = 3;   // parts of a tile of the hidden states' gradient, waves of them
+constexpr int kTailWaves = 3;   // waves of parts of cut tiles (the hidden states' gradient), at most
 constexpr size_t kPieceBytes = size_t(192) << 20;
 
 enum Use { kStats, kGrad, kHidden, kWeight };
@@ -180,6 +180,19 @@ __device__ __forceinline__ void split_weight(const CePlan& pl, const float* w, i
   }
 }
 
+// The parts of a cut tile that cost least, in K blocks: their waves, each with a start and
+// an end worth 8, and their sums' way through memory.  A warp tries all.
+__device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int bn, int groups) {
+  const int tiles = (kept + pl.tile - 1) / pl.tile * ((pl.dim + bn - 1) / bn), rest = tiles % groups, all = pl.piece / 64;
+  const int p = (threadIdx.x & 31) + 1;
+  float cost = 1e30f;
+  if (p == 1) cost = all + 8.f;
+  else if (rest && rest * p <= kTailWaves * groups && p * 4 <= all)
+    cost = ((rest * p + groups - 1) / groups) * ((float)all / p + 8.f) + 8.f * rest * p / groups;
+  const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
+  return __ffs(__ballot_sync(0xffffffffu, __float_as_uint(cost) == least));
+}
+
 // ---------------------------------------------------------------- rows that count
 // Kept rows in their order: where each came from, its target and statistics, and
 // its hidden state as planes.  Every CTA counts the kept rows before its own.
@@ -187,7 +200,7 @@ __device__ __forceinline__ void split_weight(const CePlan& pl, const float* w, i
 constexpr int kGatherThreads = 256;
 
 template <typename T, int PL, bool BWD>
-__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per, int ctas) {
+__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per, int ctas, int groups) {
   griddep_wait();
   griddep_trigger();
   if (PL == 3 && (int)blockIdx.x >= ctas) {   // the head's first piece
@@ -215,9 +228,13 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
   __syncthreads();
   before = s_before;
   total = s_total;
-  if (blockIdx.x == 0 && tid == 0) {
-    *pl.status = 0;
-    *pl.kept = total;
+  if (blockIdx.x == 0 && warp == 0) {
+    const int parts = BWD ? parts_of_cut(pl, total, PL == 1 ? 256 : 128, groups) : 1;
+    if (lane == 0) {
+      *pl.status = 0;
+      pl.kept[0] = total;
+      pl.kept[1] = parts;
+    }
   }
   const T* hidden = static_cast<const T*>(t.hidden);
   T* d_hidden = static_cast<T*>(t.d_hidden);
@@ -439,17 +456,8 @@ struct Items {
       blocks = USE == kHidden ? (cols + 63) / 64 : pl.dim_pad / 64;
     }
     whole = m_tiles * n_tiles;
-    parts = 1;
-    if (USE == kHidden) {
-      const int rest = whole % groups, all = pl.piece / 64;   // (the same cut for every piece)
-      // in K blocks: the parts' waves, each with a start and an end worth 8, and their sums' way through memory
-      float best = all + 8.f;
-      for (int p = 2; p <= kMaxParts && rest * p <= kTailWaves * groups && p * 4 <= all; ++p) {
-        const float cost = ((rest * p + groups - 1) / groups) * ((float)all / p + 8.f) + 8.f * rest * p / groups;
-        if (rest && cost < best) best = cost, parts = p;
-      }
-      if (parts > 1) whole -= rest;
-    }
+    parts = USE == kHidden ? pl.kept[1] : 1;
+    if (parts > 1) whole -= whole % groups;
   }
   __device__ __forceinline__ int count() const { return whole + (m_tiles * n_tiles - whole) * parts; }
   // first row and column of the item's tile, and its K blocks
@@ -932,7 +940,7 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
   using C = GemmCfg<PL, G>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
-                             pl, t, per, ctas);
+                             pl, t, per, ctas, gemm_groups(G, sms));
   ++*launches;
   if (e != cudaSuccess) return e;
   CUtensorMap mh, mw;
@@ -968,7 +976,7 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
   using C = GemmCfg<PL, G>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
-                             pl, t, per, ctas);
+                             pl, t, per, ctas, gemm_groups(G, sms));
   ++*launches;
   if (e != cudaSuccess) return e;
   // operands with the product's K along their rows (boxes of 64 x rows of the tile) or across them (64 x 64)

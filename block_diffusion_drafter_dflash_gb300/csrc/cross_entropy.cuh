@@ -19,7 +19,7 @@ struct CePlan {
   int rows_pad, dim_pad; // multiples of a tile's rows (256 or, for fp32 tensors, 128) and of 64
   int piece;             // vocabulary columns of a piece (a multiple of 256)
   int32_t* status;
-  int32_t* kept;         // rows kept
+  int32_t* kept;         // [2] rows kept; parts of a cut tile (the hidden states' gradient)
   int32_t* row_of;       // [rows_pad] the caller's row
   int32_t* target;       // [rows_pad]
   __nv_bfloat16* h;      // [planes][rows_pad][dim_pad]; zero behind the dim and the last kept row's tile
