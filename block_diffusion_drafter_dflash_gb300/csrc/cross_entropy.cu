@@ -12,12 +12,14 @@
 // on the device alone: grids are sized for all rows, and CTAs take items while
 // there are any.
 //
-// One GEMM kernel with four uses:
-//   stats    z of a tile of 128 rows x 256 vocabulary columns, reduced in registers
-//            to a (maximum, sum) pair a row and half tile, and the target's z
+// One GEMM kernel with these uses:
+//   stats    z of a tile of rows x vocabulary columns, reduced in registers to a
+//            (maximum, sum) pair a row and half tile, and the target's z
 //   grad     z again, turned into G: a piece of it is stored, rounded to bf16
 //   hidden   dH += G W over a piece (W read with its vocabulary axis along K)
 //   weight   dW = G' H of a piece's rows of the head (both along the rows)
+//   grads    the last two in one launch, where both are small (choosing between them
+//            tile by tile costs large ones 5 %)
 // A piece is as many columns as keep G within kPieceBytes.
 //
 // bf16: the two CTAs of a cluster share a tile of 256 x 256 (tcgen05 cta_group::2, each
@@ -51,19 +53,20 @@ constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
 constexpr long long kBudget = 400000000LL;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTailWaves = 3;   // waves of parts of cut tiles (the hidden states' gradient), at most
+constexpr int kDirectPiece = 1024;
 constexpr size_t kPieceBytes = size_t(192) << 20;
 
-enum Use { kStats, kGrad, kHidden, kWeight };
+enum Use { kStats, kGrad, kHidden, kWeight, kGrads };
 
-// PL planes; G CTAs share a tile.
-template <int PL, int G>
+// PL planes; G CTAs share a tile of BN columns.
+template <int PL, int G, int BN>
 struct GemmCfg {
   static constexpr int kCtas = G;
-  static constexpr int kTM = kBM * kCtas, kBN = PL == 1 ? 256 : 128;   // the tile
+  static constexpr int kTM = kBM * kCtas, kBN = BN;   // the tile
   static constexpr int kOwnN = kBN / kCtas;                // rows of the second operand that a CTA holds
   static constexpr int kA = kBM * 128, kB = kOwnN * 128;   // bytes of a K block of 64
   static constexpr int kStage = PL * (kA + kB);
-  static constexpr int kStages = PL == 3 ? 2 : G == 2 ? 6 : 4;
+  static constexpr int kStages = PL == 3 ? 2 : kOwnN == 128 ? 6 : 4;
   static constexpr int kOut = kEpiWarps * 4096;            // rows staged on their way out, 32 x 64 a warp
   static constexpr int kAccCols = kBN;                     // tensor-memory columns of an accumulator
   static constexpr int kNC = kBN / 2;                      // columns of an epilogue thread
@@ -73,14 +76,17 @@ struct GemmCfg {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
+template <int PL> struct Tensor { using T = float; };
+template <> struct Tensor<1> { using T = __nv_bfloat16; };
+
 struct GemmArgs {
   CePlan pl;
   int v0, cols;          // the piece's first vocabulary column, how many there are
   int first;             // hidden: the sums start here
   int part0;             // stats: the piece's first pair
   float scale2, scale2_lo;   // log2(e) / T and its rounding residual
-  void* d_weight;
-  int f32_out;
+  void* d_hidden;
+  int64_t d_row_stride;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -182,14 +188,14 @@ __device__ __forceinline__ void split_weight(const CePlan& pl, const float* w, i
 
 // The parts of a cut tile that cost least, in K blocks: their waves, each with a start and
 // an end worth 8, and their sums' way through memory.  A warp tries all.
-__device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int bn, int groups) {
-  const int tiles = (kept + pl.tile - 1) / pl.tile * ((pl.dim + bn - 1) / bn), rest = tiles % groups, all = pl.piece / 64;
+__device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int groups) {
+  const int tiles = (kept + pl.tile - 1) / pl.tile * ((pl.dim + pl.bn - 1) / pl.bn), rest = tiles % groups, all = pl.piece / 64;
   const int p = (threadIdx.x & 31) + 1;
   float cost = 1e30f;
   if (p == 1) cost = all + 8.f;
-  else if (rest && rest * p <= kTailWaves * groups && p * 4 <= all)
+  else if (!pl.direct && rest && rest * p <= kTailWaves * groups && p * 4 <= all)
     cost = ((rest * p + groups - 1) / groups) * ((float)all / p + 8.f) + 8.f * rest * p / groups;
-  const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
+  const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));   // (costs are positive)
   return __ffs(__ballot_sync(0xffffffffu, __float_as_uint(cost) == least));
 }
 
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
   before = s_before;
   total = s_total;
   if (blockIdx.x == 0 && warp == 0) {
-    const int parts = BWD ? parts_of_cut(pl, total, PL == 1 ? 256 : 128, groups) : 1;
+    const int parts = BWD ? parts_of_cut(pl, total, groups) : 1;
     if (lane == 0) {
       *pl.status = 0;
       pl.kept[0] = total;
@@ -308,12 +314,10 @@ __global__ void __launch_bounds__(256) ce_split_weight_kernel(CePlan pl, const f
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 // K-major: a row's 64 values run along K.  MN-major: they run along M or N, the
 // rows along K, and the tile of the next 64 is 64 rows further.
-template <bool MN>
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
-  return (addr >> 4) | ((MN ? 8192u >> 4 : 1u) << 16);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, bool mn) {
+  return (addr >> 4) | ((mn ? 8192u >> 4 : 1u) << 16);
 }
-template <bool MN>
-__host__ __device__ constexpr uint32_t k_step() { return MN ? 16 * 128 >> 4 : 32 >> 4; }   // 16 along K
+__host__ __device__ constexpr uint32_t k_step(bool mn) { return mn ? 16 * 128 >> 4 : 32 >> 4; }   // 16 along K
 
 __device__ __forceinline__ bool elect() {
   uint32_t e;
@@ -439,45 +443,53 @@ __device__ __forceinline__ void red_add4(float* p, float a, float b, float c, fl
 // The hidden states' gradient has few tiles and a long K: the tiles that would not
 // fill the last wave of CTAs are cut along K into as many parts as make that wave
 // shortest; each part has its sums in memory of its own, and they are added in order
-// at the end.
-template <int PL, int G, int USE>
+// at the end.  The head's gradient (many short tiles) comes behind.
+template <int PL, int G, int BN, int USE>
 struct Items {
-  using C = GemmCfg<PL, G>;
+  using C = GemmCfg<PL, G, BN>;
   int m_tiles, n_tiles, blocks;
   int whole, parts;   // tiles that are not cut; parts of each of the others
-  __device__ __forceinline__ Items(const CePlan& pl, int cols, int kept, int groups) {
-    if (USE == kWeight) {
-      m_tiles = (cols + C::kTM - 1) / C::kTM;
-      n_tiles = (pl.dim + C::kBN - 1) / C::kBN;
-      blocks = (kept + 63) / 64;
-    } else {
-      m_tiles = (kept + C::kTM - 1) / C::kTM;
-      n_tiles = ((USE == kHidden ? pl.dim : cols) + C::kBN - 1) / C::kBN;
-      blocks = USE == kHidden ? (cols + 63) / 64 : pl.dim_pad / 64;
-    }
+  int w_from, w_n, w_blocks, n;   // first item, column tiles and blocks of the head's gradient; all items
+  __device__ __forceinline__ Items(const GemmArgs& a, int kept, int groups) {
+    const CePlan& pl = a.pl;
+    m_tiles = (kept + C::kTM - 1) / C::kTM;
+    constexpr bool kGradient = USE == kHidden || USE == kWeight || USE == kGrads;
+    n_tiles = ((kGradient ? pl.dim : a.cols) + C::kBN - 1) / C::kBN;
+    blocks = kGradient ? (a.cols + 63) / 64 : pl.dim_pad / 64;
+    parts = USE == kHidden || USE == kGrads ? pl.kept[1] : 1;
     whole = m_tiles * n_tiles;
-    parts = USE == kHidden ? pl.kept[1] : 1;
-    if (parts > 1) whole -= whole % groups;
+    const int rest = parts > 1 ? whole % groups : 0;
+    whole -= rest;
+    n = whole + rest * parts;
+    if (USE == kWeight || USE == kGrads) {
+      if (USE == kWeight) n = 0;
+      w_from = n;
+      w_n = n_tiles;
+      w_blocks = (kept + 63) / 64;
+      n += (a.cols + C::kTM - 1) / C::kTM * w_n;
+    }
   }
-  __device__ __forceinline__ int count() const { return whole + (m_tiles * n_tiles - whole) * parts; }
+  __device__ __forceinline__ bool weight(int item) const { return USE == kWeight || (USE == kGrads && item >= w_from); }
   // first row and column of the item's tile, and its K blocks
   __device__ __forceinline__ void get(int item, int& m0, int& n0, int& b0, int& b1) const {
-    int tile = item;
     b0 = 0;
+    if (weight(item)) {   // along a row of tiles: G's columns stay in L2
+      const int tile = item - w_from;
+      n0 = tile % w_n * C::kBN;
+      m0 = tile / w_n * C::kTM;
+      b1 = w_blocks;
+      return;
+    }
+    int tile = item;
     b1 = blocks;
-    if (USE == kHidden && item >= whole) {   // the same part of all tiles side by side
+    if ((USE == kHidden || USE == kGrads) && item >= whole) {   // the same part of all tiles side by side
       const int rest = m_tiles * n_tiles - whole, part = (item - whole) / rest;
       tile = whole + (item - whole) - part * rest;
       b0 = (int)((long long)blocks * part / parts);
       b1 = (int)((long long)blocks * (part + 1) / parts);
     }
-    if (USE == kWeight) {   // along a row of tiles: G's columns stay in L2
-      n0 = tile % n_tiles * C::kBN;
-      m0 = tile / n_tiles * C::kTM;
-    } else {
-      m0 = tile % m_tiles * C::kTM;
-      n0 = tile / m_tiles * C::kBN;
-    }
+    m0 = tile % m_tiles * C::kTM;
+    n0 = tile / m_tiles * C::kBN;
   }
 };
 
@@ -499,14 +511,28 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* map, uint8_t* stag
   if (lane == 0) tma_store(map, stage, x, y);
 }
 
-template <int PL, int G, int USE>
+// The same of 32 fp32 values.
+__device__ __forceinline__ void store_rows_f32(const CUtensorMap* map, uint8_t* stage, int lane, int x, int y, const float* v) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) tma_store(map, stage, x, y);
+}
+
+template <int PL, int G, int BN, int USE>
 __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                   const __grid_constant__ CUtensorMap map_b,
+                                                                  const __grid_constant__ CUtensorMap map_wa,
+                                                                  const __grid_constant__ CUtensorMap map_wb,
                                                                   const __grid_constant__ CUtensorMap map_out,
                                                                   const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<PL, G>;
+  using C = GemmCfg<PL, G, BN>;
   constexpr int S = C::kStages;
-  constexpr bool kAMN = USE == kWeight, kBMN = USE == kWeight || USE == kHidden;
+  constexpr bool kBMN = USE != kStats && USE != kGrad;   // the second operand across its rows; the first too for the head's gradient
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   GemmBars* bars = reinterpret_cast<GemmBars*>(sm + (size_t)S * C::kStage + C::kOut);
@@ -536,15 +562,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   griddep_wait();
   griddep_trigger();
   const int kept = *pl.kept;
-  const Items<PL, G, USE> items(pl, a.cols, kept, groups);
-  const int n_items = items.count();
+  const Items<PL, G, BN, USE> items(a, kept, groups);
+  const int n_items = items.n;
 
   if (warp == 0) {
     if (lane == 0) {   // ---------------------------------------------------- loads
       int it = 0;
       bool ok = true;
-      // rows between the planes of each operand
-      const int a_plane = pl.rows_pad, b_plane = USE == kWeight ? pl.rows_pad : pl.piece;
       // a bf16 head is read where the caller has it
       const int v0 = PL == 1 ? a.v0 : 0;
       for (int item = group; item < n_items && ok; item += groups) {
@@ -552,6 +576,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         items.get(item, m0, n0, b0, b1);
         m0 += rank * kBM;
         n0 += rank * C::kOwnN;
+        const bool w = items.weight(item);
+        const CUtensorMap *ma = USE == kGrads && w ? &map_wa : &map_a, *mb = USE == kGrads && w ? &map_wb : &map_b;
+        const int a_plane = pl.rows_pad, b_plane = w ? pl.rows_pad : pl.piece;   // rows between an operand's planes
         for (int kb = b0; kb < b1; ++kb, ++it) {
           const int s = it % S;
           if (it >= S && !ptx::mbar_wait(bars->empty + s, ((it / S) & 1) ^ 1, kBudget, pl.status)) {
@@ -565,19 +592,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
 #pragma unroll
           for (int p = 0; p < PL; ++p) {
             uint8_t* ta = st + p * C::kA;
-            if (kAMN) {
+            if (w) {
 #pragma unroll
-              for (int i = 0; i < kBM / 64; ++i) tma_tile<G>(ta + i * 8192, &map_a, bar, m0 + 64 * i, p * a_plane + kb * 64);
+              for (int i = 0; i < kBM / 64; ++i) tma_tile<G>(ta + i * 8192, ma, bar, m0 + 64 * i, p * a_plane + kb * 64);
             } else {
-              tma_tile<G>(ta, &map_a, bar, kb * 64, p * a_plane + m0);
+              tma_tile<G>(ta, ma, bar, kb * 64, p * a_plane + m0);
             }
             uint8_t* tb = st + PL * C::kA + p * C::kB;
             if (kBMN) {
-              const int row = p * b_plane + (USE == kHidden ? v0 : 0) + kb * 64;
+              const int row = p * b_plane + (w ? 0 : v0) + kb * 64;
 #pragma unroll
-              for (int i = 0; i < C::kOwnN / 64; ++i) tma_tile<G>(tb + i * 8192, &map_b, bar, n0 + 64 * i, row);
+              for (int i = 0; i < C::kOwnN / 64; ++i) tma_tile<G>(tb + i * 8192, mb, bar, n0 + 64 * i, row);
             } else {
-              tma_tile<G>(tb, &map_b, bar, kb * 64, p * b_plane + v0 + n0);
+              tma_tile<G>(tb, mb, bar, kb * 64, p * b_plane + v0 + n0);
             }
           }
         }
@@ -590,8 +617,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   } else if (warp == 1 && rank == 0) {   // --------------------------------- MMAs
     // The whole warp runs this, so that what it computes is uniform; one elected
     // lane issues each group of MMAs with the commits behind it.
-    constexpr uint32_t id = ptx::idesc_bf16_f32(C::kTM, C::kBN) | (kAMN ? 1u << 15 : 0u) | (kBMN ? 1u << 16 : 0u);
-    constexpr uint32_t ka = k_step<kAMN>(), kb_ = k_step<kBMN>();
+    constexpr uint32_t kId = ptx::idesc_bf16_f32(C::kTM, C::kBN) | (kBMN ? 1u << 16 : 0u);
+    constexpr uint32_t kb_ = k_step(kBMN);
     bool ok = true;
     auto wait = [&](uint64_t* b, uint32_t p) {
       if (!__all_sync(0xffffffffu, try_wait_cluster(b, p))) {
@@ -607,6 +634,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     for (int item = group; item < n_items && ok; item += groups) {
       int m0, n0, b0, b1;
       items.get(item, m0, n0, b0, b1);
+      const bool w = items.weight(item);
+      const uint32_t id = kId | (w ? 1u << 15 : 0u), ka = k_step(w);
       int sums = 0;
       for (int kb = b0; kb < b1 && ok; ++seq) {
         const int buf = seq & 1, use = seq >> 1;
@@ -621,7 +650,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         for (; kb < end; ++kb, ++it) {
           const int s = it % S;
           if (!wait(bars->full + s, (it / S) & 1)) break;
-          const uint32_t da = desc_lo<kAMN>(base + s * C::kStage), db = desc_lo<kBMN>(base + s * C::kStage + PL * C::kA);
+          const uint32_t da = desc_lo(base + s * C::kStage, w), db = desc_lo(base + s * C::kStage + PL * C::kA, kBMN);
           if (elect()) {
             if constexpr (PL == 1) {
 #pragma unroll
@@ -661,9 +690,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
       int m0, n0, b0, b1;
       items.get(item, m0, n0, b0, b1);
       m0 += rank * kBM;
-      const int row = m0 + lane_row;   // (a vocabulary row of the piece for kWeight)
+      const int row = m0 + lane_row;   // (a vocabulary row of the piece for the head's gradient)
       // what the row needs at the end
-      const bool in = USE != kStats && USE != kGrad ? false : row < kept;
+      const bool in = (USE == kStats || USE == kGrad) && row < kept;
       const int target = in ? pl.target[row] : -1;
       const float2 l2 = USE == kGrad && in ? pl.lse2[row] : make_float2(0.f, 0.f);
       const float gain = USE == kGrad && in ? pl.gain[row] : 0.f;
@@ -746,7 +775,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
             for (int j = 0; j < NC; ++j) acc[j] -= __bfloat162float(__float2bfloat16_rn(acc[j]));
           }
         }
-      } else if constexpr (USE == kHidden) {
+      } else if (items.weight(item)) {
+        // (rows behind the head's last and columns behind the dim are cut off by the map)
+        constexpr int kCols = PL == 1 ? 64 : 32;
+#pragma unroll
+        for (int j0 = 0; j0 < NC; j0 += kCols)
+          if (m0 + 32 * (warp & 3) < a.cols && col + j0 < pl.dim) {
+            if constexpr (PL == 1) store_rows(&map_out, stage, lane, col + j0, a.v0 + m0 + 32 * (warp & 3), acc + j0);
+            else store_rows_f32(&map_out, stage, lane, col + j0, a.v0 + m0 + 32 * (warp & 3), acc + j0);
+          }
+      } else if (pl.direct) {   // the one piece of a small vocabulary: to the caller's rows
+        if (row < kept) {
+          using T = typename Tensor<PL>::T;
+          T* out = static_cast<T*>(a.d_hidden) + pl.row_of[row] * a.d_row_stride + col;
+          const bool vec = rows_vec(static_cast<T*>(a.d_hidden), a.d_row_stride);
+          const int left = pl.dim - col;   // a multiple of 8
+#pragma unroll
+          for (int j = 0; j < NC; j += 8)
+            if (j < left) set8(out + j, vec, acc + j);
+        }
+      } else {
         // whole tiles to their place, parts of a tile to a tile of their own; a piece
         // adds to what the pieces before it left (each value once a launch: the order
         // of the additions is fixed)
@@ -763,18 +811,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           for (int j = 0; j < NC; j += 4)
             if (j < left) red_add4(out + j, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
-      } else if constexpr (PL == 1) {
-        // (rows behind the head's last and columns behind the dim are cut off by the map)
-#pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 64)
-          if (m0 + 32 * (warp & 3) < a.cols && col + j0 < pl.dim)
-            store_rows(&map_out, stage, lane, col + j0, a.v0 + m0 + 32 * (warp & 3), acc + j0);
-      } else if (row < a.cols) {
-        float* out = static_cast<float*>(a.d_weight) + (size_t)(a.v0 + row) * pl.dim + col;
-        const int left = pl.dim - col;   // a multiple of 8
-#pragma unroll
-        for (int j = 0; j < NC; j += 8)
-          if (j < left) set8(out + j, true, acc + j);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -838,34 +874,34 @@ __global__ void __launch_bounds__(kMergeThreads) ce_merge_kernel(CePlan pl, int 
 // order.
 constexpr int kFinishThreads = 256;
 
-template <typename T, int PL, int G>
+template <typename T, int PL, int G, int BN>
 __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
   griddep_wait();
   griddep_trigger();
-  using C = GemmCfg<PL, G>;
+  using C = GemmCfg<PL, G, BN>;
   const int kept = *pl.kept;
-  const Items<PL, G, kHidden> items(pl, pl.piece, kept, groups_of_ctas);
-  const int rest = items.m_tiles * items.n_tiles - items.whole;
+  const int m_tiles = (kept + C::kTM - 1) / C::kTM, tiles = m_tiles * ((pl.dim + C::kBN - 1) / C::kBN), parts = pl.kept[1];
+  const int rest = parts > 1 ? tiles % groups_of_ctas : 0, whole = tiles - rest;
   const bool vec = rows_vec(d_hidden, stride);
   const size_t step = (size_t)rest * C::kTM * C::kBN;
   for (int r = blockIdx.x; r < kept; r += gridDim.x) {
     T* out = d_hidden + pl.row_of[r] * stride;
     for (int c = threadIdx.x * 8; c < pl.dim; c += kFinishThreads * 8) {
-      const int tile = c / C::kBN * items.m_tiles + r / C::kTM;
+      const int tile = c / C::kBN * m_tiles + r / C::kTM;
       float sum[8];
-      if (tile < items.whole) {
+      if (tile < whole) {
         get8(pl.acc + (size_t)r * pl.dim_pad + c, true, sum);
       } else {
-        const float* src = pl.tail + ((size_t)(tile - items.whole) * C::kTM + r % C::kTM) * C::kBN + c % C::kBN;
+        const float* src = pl.tail + ((size_t)(tile - whole) * C::kTM + r % C::kTM) * C::kBN + c % C::kBN;
         get8(src, true, sum);
-        for (int p = 1; p < items.parts; p += 4) {
+        for (int p = 1; p < parts; p += 4) {
           float v[4][8];
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (p + u < items.parts) get8(src + (p + u) * step, true, v[u]);
+            if (p + u < parts) get8(src + (p + u) * step, true, v[u]);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (p + u < items.parts) {
+            if (p + u < parts) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) sum[j] += v[u][j];
             }
@@ -877,11 +913,11 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan
 }
 
 // ---------------------------------------------------------------- host side
-template <int PL, int G>
+template <int PL, int G, int BN>
 cudaError_t prepare() {
-  for (auto kernel : {ce_gemm_kernel<PL, G, kStats>, ce_gemm_kernel<PL, G, kGrad>, ce_gemm_kernel<PL, G, kHidden>,
-                      ce_gemm_kernel<PL, G, kWeight>}) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmCfg<PL, G>::kBytes);
+  for (auto kernel : {ce_gemm_kernel<PL, G, BN, kStats>, ce_gemm_kernel<PL, G, BN, kGrad>, ce_gemm_kernel<PL, G, BN, kHidden>,
+                      ce_gemm_kernel<PL, G, BN, kWeight>, ce_gemm_kernel<PL, G, BN, kGrads>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GemmCfg<PL, G, BN>::kBytes);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -889,14 +925,14 @@ cudaError_t prepare() {
 
 int gemm_groups(int ctas, int sms) { return std::max(1, sms / ctas); }
 
-template <int PL, int G, int USE>
-cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, int sms, int* launches,
-                 cudaStream_t s) {
+template <int PL, int G, int BN, int USE>
+cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& wa, const CUtensorMap& wb,
+                 const CUtensorMap& mo, int sms, int* launches, cudaStream_t s) {
   ++*launches;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(G * gemm_groups(G, sms));
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = GemmCfg<PL, G>::kBytes;
+  cfg.dynamicSmemBytes = GemmCfg<PL, G, BN>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -913,7 +949,7 @@ cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<PL, G, USE>, ma, mb, mo, a);
+  return cudaLaunchKernelEx(&cfg, ce_gemm_kernel<PL, G, BN, USE>, ma, mb, wa, wb, mo, a);
 }
 
 struct Scale {
@@ -935,9 +971,9 @@ int split_ctas(const CePlan& pl, int sms) {
   return (int)std::min<long long>(sms * 6, ((long long)pl.piece * (pl.dim_pad / 8) + 1023) / 1024);
 }
 
-template <typename T, int PL, int G>
+template <typename T, int PL, int G, int BN>
 cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
-  using C = GemmCfg<PL, G>;
+  using C = GemmCfg<PL, G, BN>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
                              pl, t, per, ctas, gemm_groups(G, sms));
@@ -961,7 +997,7 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    e = gemm<PL, G, kStats>(a, mh, mw, mw, sms, launches, s);
+    e = gemm<PL, G, BN, kStats>(a, mh, mw, mh, mw, mw, sms, launches, s);
     if (e != cudaSuccess) return e;
     a.part0 += 2 * ((a.cols + C::kBN - 1) / C::kBN);
   }
@@ -971,16 +1007,16 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
                     dim3(kMergeThreads), 0, s, pl, a.part0, t.loss, t.lse);
 }
 
-template <typename T, int PL, int G>
+template <typename T, int PL, int G, int BN>
 cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
-  using C = GemmCfg<PL, G>;
+  using C = GemmCfg<PL, G, BN>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
   cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
                              pl, t, per, ctas, gemm_groups(G, sms));
   ++*launches;
   if (e != cudaSuccess) return e;
   // operands with the product's K along their rows (boxes of 64 x rows of the tile) or across them (64 x 64)
-  CUtensorMap h_k, h_mn, w_k, w_mn, g_k, g_mn, g_out, dw_out;
+  CUtensorMap h_k, h_mn, w_k, w_mn, g_k, g_mn, g_out, dw_out{};
   const void* w = PL == 1 ? t.weight : pl.w;
   const int w_dim = PL == 1 ? pl.dim : pl.dim_pad, w_rows = PL == 1 ? pl.vocab : PL * pl.piece;
   if (!encode_activation_map(&h_k, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM) ||
@@ -990,14 +1026,19 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
       !encode_activation_map(&g_k, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, kBM) ||
       !encode_activation_map(&g_mn, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 64) ||
       !encode_activation_map(&g_out, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 32) ||
-      !(PL == 1 && t.d_weight ? encode_activation_map(&dw_out, t.d_weight, pl.dim, pl.vocab, pl.dim, 32) : (dw_out = g_out, true)))
+      (t.d_weight && !(PL == 1 ? encode_activation_map(&dw_out, t.d_weight, pl.dim, pl.vocab, pl.dim, 32)
+                               : encode_f32_map(&dw_out, t.d_weight, pl.dim, pl.vocab, 32))))
     return cudaErrorInvalidValue;
   GemmArgs a{};
   a.pl = pl;
   const Scale sc = scale_of(t.temperature);
   a.scale2 = sc.hi;
   a.scale2_lo = sc.lo;
-  a.d_weight = t.d_weight;
+  a.d_hidden = t.d_hidden;
+  a.d_row_stride = t.d_row_stride;
+  // (the tiles of a piece's two gradients)
+  const long long tiles = (long long)(pl.rows_pad / pl.tile + (pl.piece + pl.tile - 1) / pl.tile) * ((pl.dim + BN - 1) / BN);
+  const bool both = t.d_hidden && t.d_weight && tiles <= 4LL * gemm_groups(G, sms);
   for (int v0 = 0; v0 < pl.vocab; v0 += pl.piece) {
     a.v0 = v0;
     a.cols = std::min(pl.piece, pl.vocab - v0);
@@ -1007,13 +1048,17 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
       ++*launches;
       if (e != cudaSuccess) return e;
     }
-    if ((e = gemm<PL, G, kGrad>(a, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_hidden && (e = gemm<PL, G, kHidden>(a, g_k, w_mn, g_out, sms, launches, s)) != cudaSuccess) return e;
-    if (t.d_weight && (e = gemm<PL, G, kWeight>(a, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
+    if ((e = gemm<PL, G, BN, kGrad>(a, h_k, w_k, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (both) {
+      if ((e = gemm<PL, G, BN, kGrads>(a, g_k, w_mn, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
+      continue;
+    }
+    if (t.d_hidden && (e = gemm<PL, G, BN, kHidden>(a, g_k, w_mn, g_k, w_mn, g_out, sms, launches, s)) != cudaSuccess) return e;
+    if (t.d_weight && (e = gemm<PL, G, BN, kWeight>(a, g_mn, h_mn, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
   }
-  if (!t.d_hidden) return cudaSuccess;
+  if (!t.d_hidden || pl.direct) return cudaSuccess;
   ++*launches;
-  return launch_pdl(ce_finish_hidden_kernel<T, PL, G>, dim3(std::min(pl.rows, sms * 64)), dim3(kFinishThreads), 0, s, pl,
+  return launch_pdl(ce_finish_hidden_kernel<T, PL, G, BN>, dim3(std::min(pl.rows, sms * 64)), dim3(kFinishThreads), 0, s, pl,
                     static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_groups(G, sms));
 }
 
@@ -1025,14 +1070,18 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.dim = dim;
   pl.vocab = vocab;
   pl.planes = f32 ? 3 : 1;
-  // a pair of CTAs shares 256 rows, unless there is one CTA's worth of them (then the
-  // second would only hold up half the loads: 15 rows of 4,096 against 151,936 in 238 us,
-  // alone 2xx)
-  pl.ctas = f32 || rows <= kBM || sms < 2 ? 1 : 2;
+  // Tiles.  A pair of CTAs shares 256 x 256, unless there is one CTA's worth of rows
+  // (the second would only hold up half the loads: 15 rows of 4,096 against 151,936 in
+  // 237 us, alone 198); where tiles of 128 x 128 fit one wave their K, the time of such
+  // a call, takes half as long a block.
+  const long long tiles128 = (long long)((rows + kBM - 1) / kBM) * ((vocab + 127) / 128);
+  const bool small = !f32 && tiles128 <= sms;
+  pl.bn = f32 || small ? 128 : 256;
+  pl.ctas = f32 || small || rows <= kBM || sms < 2 ? 1 : 2;
   pl.tile = kBM * pl.ctas;
   pl.rows_pad = (rows + pl.tile - 1) / pl.tile * pl.tile;
   pl.dim_pad = (dim + 63) / 64 * 64;
-  const int bn = f32 ? GemmCfg<3, 1>::kBN : GemmCfg<1, 1>::kBN;
+  const int bn = pl.bn;
   // pieces of equal size, as few as the limit allows
   const size_t column = 2 * (size_t)pl.planes * (backward ? std::max(pl.rows_pad, f32 ? pl.dim_pad : 0) : pl.dim_pad);
   const long long limit = std::max<long long>(256, (long long)(kPieceBytes / column) / 256 * 256);
@@ -1066,7 +1115,9 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
     pl.lse2 = reinterpret_cast<float2*>(take(8 * R));
     pl.gain = reinterpret_cast<float*>(take(4 * R));
     pl.g = reinterpret_cast<__nv_bfloat16*>(take(2 * pl.planes * R * pl.piece));
-    if (want_hidden) {
+    // a small vocabulary's K is short: no tile is cut, and the tiles go to the caller's rows
+    pl.direct = pl.piece >= vocab && pl.piece <= kDirectPiece;
+    if (want_hidden && !pl.direct) {
       pl.acc = reinterpret_cast<float*>(take(4 * R * pl.dim_pad));
       pl.tail = reinterpret_cast<float*>(take(4 * (size_t)kTailWaves * sms * kBM * bn));
     }
@@ -1075,22 +1126,27 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   return pl;
 }
 
-cudaError_t ce_prepare_f32() { return prepare<3, 1>(); }
+cudaError_t ce_prepare_f32() { return prepare<3, 1, 128>(); }
 cudaError_t ce_prepare_bf16() {
-  const cudaError_t e = prepare<1, 1>();
-  return e == cudaSuccess ? prepare<1, 2>() : e;
+  for (cudaError_t e : {prepare<1, 1, 128>(), prepare<1, 1, 256>(), prepare<1, 2, 256>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 cudaError_t ce_forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   *launches = 0;
-  if (pl.planes == 3) return forward<float, 3, 1>(pl, t, sms, launches, s);
-  return pl.ctas == 2 ? forward<__nv_bfloat16, 1, 2>(pl, t, sms, launches, s) : forward<__nv_bfloat16, 1, 1>(pl, t, sms, launches, s);
+  if (pl.planes == 3) return forward<float, 3, 1, 128>(pl, t, sms, launches, s);
+  if (pl.bn == 128) return forward<__nv_bfloat16, 1, 1, 128>(pl, t, sms, launches, s);
+  return pl.ctas == 2 ? forward<__nv_bfloat16, 1, 2, 256>(pl, t, sms, launches, s)
+                      : forward<__nv_bfloat16, 1, 1, 256>(pl, t, sms, launches, s);
 }
 
 cudaError_t ce_backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   *launches = 0;
-  if (pl.planes == 3) return backward<float, 3, 1>(pl, t, sms, launches, s);
-  return pl.ctas == 2 ? backward<__nv_bfloat16, 1, 2>(pl, t, sms, launches, s) : backward<__nv_bfloat16, 1, 1>(pl, t, sms, launches, s);
+  if (pl.planes == 3) return backward<float, 3, 1, 128>(pl, t, sms, launches, s);
+  if (pl.bn == 128) return backward<__nv_bfloat16, 1, 1, 128>(pl, t, sms, launches, s);
+  return pl.ctas == 2 ? backward<__nv_bfloat16, 1, 2, 256>(pl, t, sms, launches, s)
+                      : backward<__nv_bfloat16, 1, 1, 256>(pl, t, sms, launches, s);
 }
 
 }  // namespace dflash

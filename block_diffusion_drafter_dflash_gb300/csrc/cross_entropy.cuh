@@ -15,7 +15,8 @@ namespace dflash {
 struct CePlan {
   int rows, dim, vocab;
   int planes;            // bf16 planes of an operand: 1 (bf16 tensors) or 3 (fp32 tensors)
-  int ctas, tile;        // CTAs that share a tile, its rows
+  int direct;            // gradient: the hidden states' gradient needs no sums in memory
+  int ctas, tile, bn;    // CTAs that share a tile, its rows and columns
   int rows_pad, dim_pad; // multiples of a tile's rows (256 or, for fp32 tensors, 128) and of 64
   int piece;             // vocabulary columns of a piece (a multiple of 256)
   int32_t* status;

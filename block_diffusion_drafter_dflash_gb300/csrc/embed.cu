@@ -30,72 +30,87 @@ namespace cg = cooperative_groups;
 
 constexpr int kChunk = kEmbedChunk;
 
-// ---------------------------------------------------------------- rows in vectors of W values
+// ---------------------------------------------------------------- columns of a thread
+// A warp takes 32 * W columns.  Where rows allow it (S = 1) a lane has W neighbours, one
+// 16-byte access of the wider type; else (S = 32: an odd dim, an odd address) every 32nd,
+// so that the warp's narrow accesses lie side by side and a row's bookkeeping still serves
+// W values.  `left`: columns from the lane's first to the row's end.
+template <int W, int S>
+__device__ __forceinline__ int first_column(int unit) {
+  return (unit >> 5) * 32 * W + (unit & 31) * (S == 1 ? W : 1);
+}
 template <typename T, int W>
 struct alignas(sizeof(T) * W) Vec {
   T v[W];
 };
-// Accesses of at most 16 bytes.
-template <int W, typename T>
-__device__ __forceinline__ void load_row(const T* p, float* v) {
-  constexpr int P = W * sizeof(T) > 16 ? 16 / sizeof(T) : W;
+template <int W, int S, typename T>
+__device__ __forceinline__ void load_row(const T* p, int left, float* v) {
+  if constexpr (S == 1) {
+    const Vec<T, W> x = *reinterpret_cast<const Vec<T, W>*>(p);
 #pragma unroll
-  for (int k = 0; k < W; k += P) {
-    const Vec<T, P> x = *reinterpret_cast<const Vec<T, P>*>(p + k);
+    for (int j = 0; j < W; ++j) v[j] = to_f32<T>(x.v[j]);
+  } else {
 #pragma unroll
-    for (int j = 0; j < P; ++j) v[k + j] = to_f32<T>(x.v[j]);
+    for (int j = 0; j < W; ++j) v[j] = j * S < left ? to_f32<T>(p[j * S]) : 0.f;
   }
 }
 // STREAM: what is written is not read again soon.
-template <int W, bool STREAM = false, typename T>
-__device__ __forceinline__ void store_row(T* p, const float* v) {
-  constexpr int P = W * sizeof(T) > 16 ? 16 / sizeof(T) : W;
+template <int W, int S, bool STREAM = false, typename T>
+__device__ __forceinline__ void store_row(T* p, int left, const float* v) {
+  if constexpr (S == 1) {
+    Vec<T, W> x;
 #pragma unroll
-  for (int k = 0; k < W; k += P) {
-    Vec<T, P> x;
+    for (int j = 0; j < W; ++j) x.v[j] = from_f32<T>(v[j]);
+    if constexpr (STREAM && W * sizeof(T) == 16) __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));
+    else *reinterpret_cast<Vec<T, W>*>(p) = x;
+  } else {
 #pragma unroll
-    for (int j = 0; j < P; ++j) x.v[j] = from_f32<T>(v[k + j]);
-    if constexpr (STREAM && P * sizeof(T) == 16) __stcs(reinterpret_cast<uint4*>(p + k), *reinterpret_cast<const uint4*>(&x));
-    else *reinterpret_cast<Vec<T, P>*>(p + k) = x;
+    for (int j = 0; j < W; ++j)
+      if (j * S < left) p[j * S] = from_f32<T>(v[j]);
   }
 }
-// The widest vector (8, 4, 2 or 1 values, at most 16 bytes of the wider type, so that a
-// warp's accesses have no gaps) that both sides' rows allow: rows start at multiples of it.
-int width_of(const void* a, int64_t a_stride, int a_size, const void* b, int64_t b_stride, int b_size, int dim) {
-  for (int w = 16 / std::max(a_size, b_size); w > 1; w /= 2) {
-    auto fits = [&](const void* p, int64_t stride, int size) {
-      const uintptr_t bytes = w * size;
-      return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (uintptr_t)(stride * size) % bytes == 0;
-    };
-    if (dim % w == 0 && fits(a, a_stride, a_size) && fits(b, b_stride, b_size)) return w;
-  }
-  return 1;
+// Values of a lane and their step.
+template <typename A, typename B, bool VEC>
+struct Columns {
+  static constexpr int kWidest = sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B);
+  static constexpr int W = VEC ? 16 / kWidest : 4, S = VEC ? 1 : 32;
+};
+template <typename A, typename B>
+bool rows_fit(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int dim) {
+  constexpr int W = Columns<A, B, true>::W;
+  auto fits = [&](const void* p, int64_t stride, int size) {
+    return reinterpret_cast<uintptr_t>(p) % (W * size) == 0 && stride % W == 0;
+  };
+  return dim % W == 0 && fits(a, a_stride, sizeof(A)) && fits(b, b_stride, sizeof(B));
 }
 
 // ---------------------------------------------------------------- lookup
-// kLookups: vectors of a thread, all loaded before the first is stored.
-template <typename TT, typename TO, int W, int kLookups>
+// kLookups: accesses of a thread, all loaded before the first is stored.
+template <typename TT, typename TO, bool VEC, int kLookups>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_wait();
   griddep_trigger();
-  const unsigned groups = a.dim / W;
-  const long long n = (long long)a.n * groups, step = (long long)gridDim.x * (256 * kLookups);
+  constexpr int W = Columns<TT, TO, VEC>::W, S = Columns<TT, TO, VEC>::S;
+  const unsigned units = S == 1 ? a.dim / W : (a.dim + 32 * W - 1) / (32 * W) * 32;   // of a row
+  const long long n = (long long)a.n * units, step = (long long)gridDim.x * (256 * kLookups);
   const TT* table = static_cast<const TT*>(a.table);
   TO* out = static_cast<TO*>(a.out);
   for (long long i0 = blockIdx.x * (256LL * kLookups) + threadIdx.x; i0 < n; i0 += step) {
     float v[kLookups][W];
     TO* to[kLookups];
+    int left[kLookups];
 #pragma unroll
     for (int u = 0; u < kLookups; ++u) {
       const long long i = i0 + u * 256;
-      to[u] = nullptr;
+      left[u] = 0;
       if (i < n) {
-        const int r = n < (1LL << 32) ? (unsigned)i / groups : (int)(i / groups);
-        const int c = (int)(i - (long long)r * groups) * W;
+        const int r = n < (1LL << 32) ? (unsigned)i / units : (int)(i / units);
+        const int unit = (int)(i - (long long)r * units), c = S == 1 ? unit * W : first_column<W, S>(unit);
         const unsigned t = a.tokens[r];
         to[u] = out + r * a.out_stride + c;
-        if (t < (unsigned)a.vocab) {
-          load_row<W>(table + (size_t)t * a.dim + c, v[u]);
+        left[u] = a.dim - c;
+        if (t < (unsigned)a.vocab && left[u] > 0) {
+          load_row<W, S>(table + (size_t)t * a.dim + c, left[u], v[u]);
         } else {
 #pragma unroll
           for (int j = 0; j < W; ++j) v[u][j] = 0.f;
@@ -104,10 +119,10 @@ __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < kLookups; ++u)
-      if (to[u]) {
+      if (left[u] > 0) {
 #pragma unroll
         for (int j = 0; j < W; ++j) v[u][j] *= a.scale;
-        store_row<W, (kLookups > 1)>(to[u], v[u]);   // (without: 134 MB of output at 27 us instead of 22.5)
+        store_row<W, S, (kLookups > 1)>(to[u], left[u], v[u]);   // (without: 134 MB of output at 27 us instead of 22.5)
       }
   }
 }
@@ -257,26 +272,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
 
 // ---------------------------------------------------------------- sums
 // A chunk's (or a whole token's) sum into the table's gradient.
-template <typename TT, int W>
-__device__ __forceinline__ void put_sum(TT* p, const float* sum, float scale, int accumulate) {
+template <int W, int S, typename TT>
+__device__ __forceinline__ void put_sum(TT* p, int left, const float* sum, float scale, int accumulate) {
   float v[W];
 #pragma unroll
   for (int j = 0; j < W; ++j) v[j] = sum[j] * scale;
   if (accumulate) {
     float o[W];
-    load_row<W>(p, o);
+    load_row<W, S>(p, left, o);
 #pragma unroll
     for (int j = 0; j < W; ++j) v[j] = fmaf(sum[j], scale, o[j]);
   }
-  store_row<W>(p, v);
+  store_row<W, S>(p, left, v);
 }
 
 // A chunk's sums over blockDim.x * W columns.
-template <typename TO, typename TT, int W>
+template <typename TO, typename TT, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * W;
+  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
+  const int c = first_column<W, S>(blockIdx.y * blockDim.x + threadIdx.x), left = pl.dim - c;
   TT* table = static_cast<TT*>(a.d_table);
   __shared__ uint2 s_pair[kChunk];
   const uint2* order = pl.order;
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
     float v[U][W];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i + u < n) load_row<W>(d_out + (int64_t)s_pair[i + u].y * a.stride + c, v[u]);
+      if (i + u < n) load_row<W, S>(d_out + (int64_t)s_pair[i + u].y * a.stride + c, left, v[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = i + u;
@@ -306,9 +322,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
         if (last || s_pair[k + 1].x != s_pair[k].x) {
           const bool head = first && from_before, tail = last && goes_on;
           if (head || tail)   // (a chunk of one token alone has one sum, as its first)
-            store_row<W>(pl.part + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * pl.dim + c, sum);
+            store_row<W, S>(pl.part + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * pl.pitch + c, left, sum);
           else
-            put_sum<TT, W>(table + (size_t)s_pair[k].x * pl.dim + c, sum, a.scale, a.accumulate);
+            put_sum<W, S>(table + (size_t)s_pair[k].x * pl.dim + c, left, sum, a.scale, a.accumulate);
           first = false;
 #pragma unroll
           for (int j = 0; j < W; ++j) sum[j] = 0.f;
@@ -346,15 +362,16 @@ struct Sum {
   }
 };
 
-template <typename TT, int W>
+template <typename TO, typename TT, bool VEC>
 __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
+  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
   __shared__ int s_last[kJoinChunks];              // a chunk's token's last chunk; 0: none begins here and goes on
   __shared__ Sum<W> s_sum[kJoinWarps][32];
   const uint2* order = pl.order;
   const int kept = *pl.kept, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b0 = blockIdx.x * kJoinChunks, c = (blockIdx.y * 32 + lane) * W;
+  const int b0 = blockIdx.x * kJoinChunks, c = first_column<W, S>(blockIdx.y * 32 + lane), left = pl.dim - c;
   {
     // lane i: whether the last token of chunk b0 + i begins there and goes on
     const int b = b0 + lane, next = (b + 1) * kChunk;   // a token that goes on reaches the chunk's end
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
       float v[U][W];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (k + u < to) load_row<W>(pl.part + (size_t)(k + u) * 2 * pl.dim + c, v[u]);
+        if (k + u < to) load_row<W, S>(pl.part + (size_t)(k + u) * 2 * pl.pitch + c, left, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (k + u < to) sum.add(v[u]);
@@ -404,7 +421,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
   auto put = [&](const Sum<W>& sum, int b) {
     float v[W];
     sum.done(v);
-    put_sum<TT, W>(table + (size_t)order[(b + 1) * kChunk - 1].x * pl.dim, v, a.scale, a.accumulate);
+    put_sum<W, S>(table + (size_t)order[(b + 1) * kChunk - 1].x * pl.dim, left, v, a.scale, a.accumulate);
   };
   int mine = 0;
   for (int i = 0; i < kJoinChunks; ++i) {
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
     Sum<W> sum;
     sum.zero();
     float v[W];
-    load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, v);   // b's own: its last token's
+    load_row<W, S>(pl.part + ((size_t)b * 2 + 1) * pl.pitch + c, left, v);   // b's own: its last token's
     sum.add(v);
     add_chunks(sum, b + 1, last + 1);
     put(sum, b);
@@ -428,7 +445,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
     if (in) {
       if (warp == 0) {
         float v[W];
-        load_row<W>(pl.part + ((size_t)b * 2 + 1) * pl.dim + c, v);
+        load_row<W, S>(pl.part + ((size_t)b * 2 + 1) * pl.pitch + c, left, v);
         sum.add(v);
       }
       add_chunks(sum, b + 1 + warp * share, min(last + 1, b + 1 + (warp + 1) * share));
@@ -451,32 +468,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
 // One launch: each CTA puts the tokens in order itself (by counting those before each)
 // and takes words of 32 table rows x 32 * W columns: a warp sums a token's rows in
 // order, eight warps together those of more than kSmallAlone.
-constexpr int kSmall = 512, kSmallWarps = 8, kSmallAlone = 16;
+constexpr int kSmall = 256, kSmallWarps = 8, kSmallAlone = 16;
 
-template <typename TO, typename TT, int W>
+template <typename TO, typename TT, bool VEC>
 __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  __shared__ uint32_t s_raw[kSmall], s_token[kSmall + 1];
+  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
+  __shared__ alignas(16) uint64_t s_key[kSmall];
+  __shared__ uint32_t s_token[kSmall + 1];
   __shared__ uint16_t s_pos[kSmall];
   __shared__ Sum<W> s_sum[kSmallWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = pl.n;
-  for (int i = tid; i < n; i += 32 * kSmallWarps) s_raw[i] = min((unsigned)a.tokens[i], (unsigned)pl.vocab);
+  static_assert(kSmall == 32 * kSmallWarps, "a token a thread");
+  const uint32_t mine = tid < n ? min((unsigned)a.tokens[tid], (unsigned)pl.vocab) : ~0u;
+  const uint64_t key = (uint64_t)mine << 32 | tid;
+  s_key[tid] = key;
   __syncthreads();
-  for (int i = tid; i < n; i += 32 * kSmallWarps) {
-    const uint32_t t = s_raw[i];
+  if (tid < n) {
     int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) rank += s_raw[j] < t || (s_raw[j] == t && j < i);
-    s_token[rank] = t;
-    s_pos[rank] = (uint16_t)i;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 2) {   // (behind the last token: larger than any)
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(s_key + j);
+      rank += (k.x < key) + (k.y < key);
+    }
+    s_token[rank] = mine;
+    s_pos[rank] = (uint16_t)tid;
   }
   if (tid == 0) s_token[n] = ~0u;
   __syncthreads();
   const int words = (pl.vocab + 31) / 32, tiles = (pl.dim + 32 * W - 1) / (32 * W);
   const TO* d_out = static_cast<const TO*>(a.d_out);
   for (long long item = blockIdx.x; item < (long long)words * tiles; item += gridDim.x) {
-    const int w = (int)(item / tiles), c = ((int)(item - (long long)w * tiles) * 32 + lane) * W;
+    const int w = (int)(item / tiles), c = first_column<W, S>((int)(item - (long long)w * tiles) * 32 + lane), left = pl.dim - c;
     const bool in = c < pl.dim;
     TT* table = static_cast<TT*>(a.d_table) + c;
     auto add_rows = [&](Sum<W>& sum, int from, int to) {
@@ -485,7 +509,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
         float v[U][W];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (k + u < to) load_row<W>(d_out + (int64_t)s_pos[k + u] * a.stride + c, v[u]);
+          if (k + u < to) load_row<W, S>(d_out + (int64_t)s_pos[k + u] * a.stride + c, left, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (k + u < to) sum.add(v[u]);
@@ -508,7 +532,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
       const float zero[W] = {};
       if (in)
         for (int v = warp; v < rows; v += kSmallWarps)
-          if (!(seen >> v & 1)) store_row<W>(table + (size_t)(w * 32 + v) * pl.dim, zero);
+          if (!(seen >> v & 1)) store_row<W, S>(table + (size_t)(w * 32 + v) * pl.dim, left, zero);
     }
     for (int turn = 0; at < end_word; ++turn) {
       const uint32_t t = s_token[at];
@@ -520,7 +544,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
         if (turn % kSmallWarps == warp && in) {
           add_rows(sum, at, end);
           sum.done(v);
-          put_sum<TT, W>(table + (size_t)t * pl.dim, v, a.scale, a.accumulate);
+          put_sum<W, S>(table + (size_t)t * pl.dim, left, v, a.scale, a.accumulate);
         }
       } else {
         const int share = (end - at + kSmallWarps - 1) / kSmallWarps;
@@ -534,7 +558,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
             for (int j = 0; j < W; ++j) sum.e[j] += s_sum[x][lane].e[j];
           }
           sum.done(v);
-          put_sum<TT, W>(table + (size_t)t * pl.dim, v, a.scale, a.accumulate);
+          put_sum<W, S>(table + (size_t)t * pl.dim, left, v, a.scale, a.accumulate);
         }
         __syncthreads();
       }
@@ -544,25 +568,22 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
 }
 
 // ---------------------------------------------------------------- host side
-template <typename TT, typename TO, int W>
+template <typename TT, typename TO, bool VEC>
 cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
-  const long long groups = (long long)a.n * (a.dim / W);
-  // few rows: a thread a vector, so that the latency is one chain of loads; many: more
+  constexpr int W = Columns<TT, TO, VEC>::W;
+  const long long units = (long long)a.n * (VEC ? a.dim / W : (a.dim + 32 * W - 1) / (32 * W) * 32);
+  // few rows: a thread an access, so that the latency is one chain of loads; many: more
   // loads in flight than CTAs could start
-  const bool few = groups <= (long long)sms * 2048;
+  const bool few = units <= (long long)sms * 2048;
   const long long per = 256 * (few ? 1 : 4);
-  const unsigned grid = (unsigned)std::min<long long>((groups + per - 1) / per, (long long)sms * 512);
-  return few ? launch_pdl(embed_kernel<TT, TO, W, 1>, dim3(grid), dim3(256), 0, s, a)
-             : launch_pdl(embed_kernel<TT, TO, W, 4>, dim3(grid), dim3(256), 0, s, a);
+  const unsigned grid = (unsigned)std::min<long long>((units + per - 1) / per, (long long)sms * 512);
+  return few ? launch_pdl(embed_kernel<TT, TO, VEC, 1>, dim3(grid), dim3(256), 0, s, a)
+             : launch_pdl(embed_kernel<TT, TO, VEC, 4>, dim3(grid), dim3(256), 0, s, a);
 }
 template <typename TT, typename TO>
-cudaError_t lookup_w(const EmbedArgs& a, int sms, cudaStream_t s) {
-  switch (width_of(a.table, a.dim, sizeof(TT), a.out, a.out_stride, sizeof(TO), a.dim)) {
-    case 8: return lookup<TT, TO, 8>(a, sms, s);
-    case 4: return lookup<TT, TO, 4>(a, sms, s);
-    case 2: return lookup<TT, TO, 2>(a, sms, s);
-    default: return lookup<TT, TO, 1>(a, sms, s);
-  }
+cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
+  return rows_fit<TT, TO>(a.table, a.dim, a.out, a.out_stride, a.dim) ? lookup<TT, TO, true>(a, sms, s)
+                                                                      : lookup<TT, TO, false>(a, sms, s);
 }
 
 int passes_of(int vocab) {
@@ -573,7 +594,7 @@ int passes_of(int vocab) {
 
 cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, size_t zero_bytes, int sms, cudaStream_t s) {
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 4096 < pl.n) ctas *= 2;
+  while (ctas < kMaxCluster && ctas * 1024 < pl.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   // CTAs that zero: two an SM, fewer for a small table
   const long long zero = std::min<long long>(2 * sms, (long long)((zero_bytes + 65535) / 65536));
@@ -592,31 +613,28 @@ cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, siz
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab), table, zero_bytes);
 }
 
-template <typename TO, typename TT, int W>
+template <typename TO, typename TT, bool VEC>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
-  const int groups = pl.dim / W, tiles32 = (groups + 31) / 32, words = (pl.vocab + 31) / 32;
+  constexpr int W = Columns<TO, TT, VEC>::W;
+  const int tiles32 = (pl.dim + 32 * W - 1) / (32 * W), words = (pl.vocab + 31) / 32;
   if (pl.n <= kSmall) {
     ++*launches;
-    return launch_pdl(embed_small_kernel<TO, TT, W>, dim3((unsigned)std::min<long long>((long long)words * tiles32, sms * 8)),
+    return launch_pdl(embed_small_kernel<TO, TT, VEC>, dim3((unsigned)std::min<long long>((long long)words * tiles32, sms * 2)),
                       dim3(32 * kSmallWarps), 0, s, pl, a);
   }
   cudaError_t e = sort(pl, a.tokens, a.d_table, a.accumulate ? 0 : sizeof(TT) * (size_t)pl.vocab * pl.dim, sms, s);
   if (e != cudaSuccess) return e;
   ++*launches;
-  const int threads = std::min(256, tiles32 * 32), tiles = (groups + threads - 1) / threads;
-  e = launch_pdl(embed_sum_kernel<TO, TT, W>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
+  const int threads = std::min(256, tiles32 * 32), tiles = (tiles32 * 32 + threads - 1) / threads;
+  e = launch_pdl(embed_sum_kernel<TO, TT, VEC>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
   if (e != cudaSuccess) return e;
   *launches += 2;
-  return launch_pdl(embed_join_kernel<TT, W>, dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, tiles32), dim3(32 * kJoinWarps), 0, s, pl, a);
+  return launch_pdl(embed_join_kernel<TO, TT, VEC>, dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, tiles32), dim3(32 * kJoinWarps), 0, s, pl, a);
 }
 template <typename TO, typename TT>
-cudaError_t sums_w(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
-  switch (width_of(a.d_out, a.stride, sizeof(TO), a.d_table, pl.dim, sizeof(TT), pl.dim)) {
-    case 8: return sums<TO, TT, 8>(pl, a, sms, launches, s);
-    case 4: return sums<TO, TT, 4>(pl, a, sms, launches, s);
-    case 2: return sums<TO, TT, 2>(pl, a, sms, launches, s);
-    default: return sums<TO, TT, 1>(pl, a, sms, launches, s);
-  }
+cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
+  return rows_fit<TO, TT>(a.d_out, a.stride, a.d_table, pl.dim, pl.dim) ? sums<TO, TT, true>(pl, a, sms, launches, s)
+                                                                        : sums<TO, TT, false>(pl, a, sms, launches, s);
 }
 
 }  // namespace
@@ -626,6 +644,7 @@ EmbedBwdPlan embed_bwd_plan(void* ws, int n, int dim, int vocab) {
   pl.n = n;
   pl.vocab = vocab;
   pl.dim = dim;
+  pl.pitch = (dim + 7) / 8 * 8;
   pl.chunks = (n + kChunk - 1) / kChunk;
   char* p = static_cast<char*>(ws);
   size_t off = 0;
@@ -637,7 +656,7 @@ EmbedBwdPlan embed_bwd_plan(void* ws, int n, int dim, int vocab) {
   pl.kept = reinterpret_cast<int32_t*>(take(256));
   pl.order = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
   pl.spare = reinterpret_cast<uint2*>(take(sizeof(uint2) * (size_t)n));
-  pl.part = reinterpret_cast<float*>(take(sizeof(float) * 2 * (size_t)pl.chunks * dim));
+  pl.part = reinterpret_cast<float*>(take(sizeof(float) * 2 * (size_t)pl.chunks * pl.pitch));
   pl.bytes = off;
   return pl;
 }
@@ -647,16 +666,16 @@ cudaError_t embed_backward_prepare() {
 }
 
 cudaError_t embed_launch(const EmbedArgs& a, bool table_f32, bool out_f32, int sms, cudaStream_t s) {
-  if (table_f32) return out_f32 ? lookup_w<float, float>(a, sms, s) : lookup_w<float, __nv_bfloat16>(a, sms, s);
-  return out_f32 ? lookup_w<__nv_bfloat16, float>(a, sms, s) : lookup_w<__nv_bfloat16, __nv_bfloat16>(a, sms, s);
+  if (table_f32) return out_f32 ? lookup<float, float>(a, sms, s) : lookup<float, __nv_bfloat16>(a, sms, s);
+  return out_f32 ? lookup<__nv_bfloat16, float>(a, sms, s) : lookup<__nv_bfloat16, __nv_bfloat16>(a, sms, s);
 }
 
 cudaError_t embed_backward_launch(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, bool out_f32, bool table_f32, int sms,
                                   int* launches, cudaStream_t s) {
   *launches = 0;
-  if (out_f32) return table_f32 ? sums_w<float, float>(pl, a, sms, launches, s) : sums_w<float, __nv_bfloat16>(pl, a, sms, launches, s);
-  return table_f32 ? sums_w<__nv_bfloat16, float>(pl, a, sms, launches, s)
-                   : sums_w<__nv_bfloat16, __nv_bfloat16>(pl, a, sms, launches, s);
+  if (out_f32) return table_f32 ? sums<float, float>(pl, a, sms, launches, s) : sums<float, __nv_bfloat16>(pl, a, sms, launches, s);
+  return table_f32 ? sums<__nv_bfloat16, float>(pl, a, sms, launches, s)
+                   : sums<__nv_bfloat16, __nv_bfloat16>(pl, a, sms, launches, s);
 }
 
 }  // namespace dflash

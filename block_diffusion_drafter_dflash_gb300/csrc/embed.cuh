@@ -20,11 +20,12 @@ struct EmbedArgs {
 // Scratch of a gradient call, carved from the caller's workspace.
 struct EmbedBwdPlan {
   int n, vocab, dim;
+  int pitch;                // values between the chunks' sums
   int chunks;               // of kEmbedChunk sorted tokens
   int32_t* kept;            // tokens inside the vocabulary
   uint2* order;             // [n] (token, position), sorted
   uint2* spare;             // [n] between the passes
-  float* part;              // [chunks][2][dim] sums of a chunk's first and last token where they go on outside
+  float* part;              // [chunks][2][pitch] sums of a chunk's first and last token where they go on outside
   size_t bytes;
 };
 constexpr int kEmbedChunk = 32;

@@ -35,6 +35,8 @@ size_t dense_smem(int stages);   // shared memory of the persistent many-row ker
 // [rows][row_stride] bf16 read in 64 x box_rows boxes.  128-byte swizzle.
 bool encode_weight_map(void* map, const void* base, int inner, int rows, int box_rows = kHalfN);
 bool encode_activation_map(void* map, const void* base, int inner, int rows, int row_stride, int box_rows);
+// An fp32 matrix [rows][inner] in 32 x box_rows boxes.
+bool encode_f32_map(void* map, const void* base, int inner, int rows, int box_rows);
 size_t tensor_map_bytes();
 
 template <class Epi>
