@@ -33,7 +33,10 @@
 // fp32 tensors enter as three bf16 planes each (x = h + m + l, 24 bits), every
 // product as six (h h, h m, m h, m m, h l, l h; what is left out is below 2^-24),
 // the five small ones with a sum of their own that spans more blocks.  One CTA a tile
-// of 128 x 128.
+// of 128 x 128.  The head's planes exist in shared memory alone: four more warps read
+// its fp32 rows a block ahead into registers and write the planes where the MMAs take
+// them.  (As a copy in memory, a piece at a time: 28 rows of 2,824 against 129,969 in
+// 1,343 us; its 1.47 GB read once are 216.)
 #include <cuda.h>
 
 #include <algorithm>
@@ -49,7 +52,8 @@ namespace {
 
 constexpr int kBM = 128;                 // rows of a CTA's part of a tile: the lanes of tensor memory
 constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = 128 + 32 * kEpiWarps;
+constexpr int kConvWarps = 8;            // fp32: warps that turn the head into planes
+template <int PL> constexpr int gemm_threads() { return 128 + 32 * kEpiWarps + (PL == 3 ? 32 * kConvWarps : 0); }
 constexpr long long kBudget = 400000000LL;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTailWaves = 3;   // waves of parts of cut tiles (the hidden states' gradient), at most
@@ -83,8 +87,8 @@ struct GemmArgs {
   CePlan pl;
   int v0, cols;          // the piece's first vocabulary column, how many there are
   int first;             // hidden: the sums start here
-  int part0;             // stats: the piece's first pair
   float scale2, scale2_lo;   // log2(e) / T and its rounding residual
+  const float* weight;   // fp32 tensors
   void* d_hidden;
   int64_t d_row_stride;
 };
@@ -96,30 +100,40 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---------------------------------------------------------------- planes
-// x as one bf16, or as three whose sum has all its 24 bits.
-template <int PL>
-__device__ __forceinline__ void split_planes(float x, __nv_bfloat16* p) {
-  p[0] = __float2bfloat16_rn(x);
-  if constexpr (PL == 3) {
-    if (__hisinf(p[0]) && !isinf(x)) p[0] = __float2bfloat16_rz(x);
-    x -= __bfloat162float(p[0]);
-    p[1] = __float2bfloat16_rn(x);
-    p[2] = __float2bfloat16_rn(x - __bfloat162float(p[1]));
-  }
+// Two values as a register of two bf16, the first in the lower half.
+__device__ __forceinline__ uint32_t pack_rn(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
 }
-__device__ __forceinline__ uint32_t pack2(__nv_bfloat16 a, __nv_bfloat16 b) {
-  return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+__device__ __forceinline__ uint32_t pack_rz(float x, float y) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
 }
-// Eight values as planes `stride` elements apart, 16 bytes each.
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Eight values as planes `stride` elements apart, 16 bytes each: rounded to one bf16, or as
+// three whose sum has all 24 bits (the first one cut off, so that no finite value rounds
+// to infinity).
 template <int PL>
 __device__ __forceinline__ void put8(__nv_bfloat16* dst, size_t stride, const float* v) {
-  __nv_bfloat16 p[8][PL];
+  uint32_t w[PL][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) split_planes<PL>(v[j], p[j]);
+  for (int j = 0; j < 4; ++j) {
+    float x = v[2 * j], y = v[2 * j + 1];
+    if constexpr (PL == 1) {
+      w[0][j] = pack_rn(x, y);
+    } else {
+      w[0][j] = pack_rz(x, y);
+      x -= low_of(w[0][j]);
+      y -= high_of(w[0][j]);
+      w[1][j] = pack_rn(x, y);
+      w[2][j] = pack_rn(x - low_of(w[1][j]), y - high_of(w[1][j]));
+    }
+  }
 #pragma unroll
-  for (int k = 0; k < PL; ++k)
-    *reinterpret_cast<uint4*>(dst + k * stride) =
-        make_uint4(pack2(p[0][k], p[1][k]), pack2(p[2][k], p[3][k]), pack2(p[4][k], p[5][k]), pack2(p[6][k], p[7][k]));
+  for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * stride) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
 }
 // Eight values at p; `vec`: whether 16-byte accesses may be used.
 __device__ __forceinline__ void get8(const float* p, bool vec, float* v) {
@@ -164,28 +178,6 @@ __device__ __forceinline__ bool rows_vec(const T* p, int64_t stride) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * (int64_t)sizeof(T))) & 15) == 0;
 }
 
-// A piece of an fp32 head as three planes, zero behind its last row and column: the
-// share of CTA `cta` of `ctas` of 256 threads.
-__device__ __forceinline__ void split_weight(const CePlan& pl, const float* w, int v0, int cta, int ctas) {
-  const unsigned groups = pl.dim_pad / 8;
-  const size_t plane = (size_t)pl.piece * pl.dim_pad;
-  const unsigned n = (unsigned)pl.piece * groups;   // at most kPieceBytes / 48, or 256 * 8192
-  constexpr int U = 4;
-  for (unsigned i0 = cta * 256u + threadIdx.x; i0 < n; i0 += U * 256u * ctas) {
-    float v[U][8] = {};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned i = i0 + u * 256u * ctas, r = i / groups, c = (i - r * groups) * 8;
-      if (i < n && v0 + (int)r < pl.vocab && (int)c < pl.dim) get8(w + (size_t)(v0 + r) * pl.dim + c, true, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const unsigned i = i0 + u * 256u * ctas;
-      if (i < n) put8<3>(pl.w + (size_t)i * 8, plane, v[u]);
-    }
-  }
-}
-
 // The parts of a cut tile that cost least, in K blocks: their waves, each with a start and
 // an end worth 8, and their sums' way through memory.  A warp tries all.
 __device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int groups) {
@@ -206,13 +198,9 @@ __device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int grou
 constexpr int kGatherThreads = 256;
 
 template <typename T, int PL, bool BWD>
-__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per, int ctas, int groups) {
+__global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, CeTensors t, int per, int groups) {
   griddep_wait();
   griddep_trigger();
-  if (PL == 3 && (int)blockIdx.x >= ctas) {   // the head's first piece
-    split_weight(pl, static_cast<const float*>(t.weight), 0, blockIdx.x - ctas, gridDim.x - ctas);
-    return;
-  }
   __shared__ int s_before, s_total, s_warp[kGatherThreads / 32], s_list[kGatherThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_before = s_total = 0;
@@ -297,16 +285,10 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(CePlan pl, Ce
   }
   // the last tile's rows behind the kept ones
   const int end = min((total + pl.tile - 1) / pl.tile * pl.tile, pl.rows_pad);
-  for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += ctas * (kGatherThreads / 32)) {
+  for (int p = total + blockIdx.x * (kGatherThreads / 32) + warp; p < end; p += gridDim.x * (kGatherThreads / 32)) {
     __nv_bfloat16* dst = pl.h + (size_t)p * pl.dim_pad;
     for (int c = lane * 8; c < pl.dim_pad; c += 256) put8<PL>(dst + c, plane, zero);
   }
-}
-
-__global__ void __launch_bounds__(256) ce_split_weight_kernel(CePlan pl, const float* w, int v0) {
-  griddep_wait();
-  griddep_trigger();
-  split_weight(pl, w, v0, blockIdx.x, gridDim.x);
 }
 
 // ---------------------------------------------------------------- tensor-core pieces
@@ -524,7 +506,7 @@ __device__ __forceinline__ void store_rows_f32(const CUtensorMap* map, uint8_t* 
 }
 
 template <int PL, int G, int BN, int USE>
-__global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
+__global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                   const __grid_constant__ CUtensorMap map_b,
                                                                   const __grid_constant__ CUtensorMap map_wa,
                                                                   const __grid_constant__ CUtensorMap map_wb,
@@ -532,6 +514,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
                                                                   const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<PL, G, BN>;
   constexpr int S = C::kStages;
+  constexpr bool kConv = PL == 3 && USE != kWeight;   // the second operand comes from the warps that convert
   constexpr bool kBMN = USE != kStats && USE != kGrad;   // the second operand across its rows; the first too for the head's gradient
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -541,7 +524,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
   const int rank = G == 2 ? blockIdx.x & 1 : 0, group = blockIdx.x / G, groups = gridDim.x / G;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      ptx::mbar_init(bars->full + s, 1);
+      ptx::mbar_init(bars->full + s, 1 + (kConv ? kConvWarps : 0));
       ptx::mbar_init(bars->empty + s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -569,8 +552,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     if (lane == 0) {   // ---------------------------------------------------- loads
       int it = 0;
       bool ok = true;
-      // a bf16 head is read where the caller has it
-      const int v0 = PL == 1 ? a.v0 : 0;
       for (int item = group; item < n_items && ok; item += groups) {
         int m0, n0, b0, b1;
         items.get(item, m0, n0, b0, b1);
@@ -578,7 +559,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
         n0 += rank * C::kOwnN;
         const bool w = items.weight(item);
         const CUtensorMap *ma = USE == kGrads && w ? &map_wa : &map_a, *mb = USE == kGrads && w ? &map_wb : &map_b;
-        const int a_plane = pl.rows_pad, b_plane = w ? pl.rows_pad : pl.piece;   // rows between an operand's planes
+        const int plane = pl.rows_pad;   // rows between an operand's planes
+        const bool conv = kConv && !w;   // the head of fp32 tensors is not loaded here
         for (int kb = b0; kb < b1; ++kb, ++it) {
           const int s = it % S;
           if (it >= S && !ptx::mbar_wait(bars->empty + s, ((it / S) & 1) ^ 1, kBudget, pl.status)) {
@@ -588,23 +570,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
           uint8_t* st = sm + (size_t)s * C::kStage;
           // the bytes of both CTAs count at the first one's barrier
           const uint32_t bar = G == 2 ? at_rank(bars->full + s, 0) : ptx::smem_u32(bars->full + s);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(bars->full + s, G * C::kStage);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(bars->full + s, conv ? PL * C::kA : G * C::kStage);
 #pragma unroll
           for (int p = 0; p < PL; ++p) {
             uint8_t* ta = st + p * C::kA;
             if (w) {
 #pragma unroll
-              for (int i = 0; i < kBM / 64; ++i) tma_tile<G>(ta + i * 8192, ma, bar, m0 + 64 * i, p * a_plane + kb * 64);
+              for (int i = 0; i < kBM / 64; ++i) tma_tile<G>(ta + i * 8192, ma, bar, m0 + 64 * i, p * plane + kb * 64);
             } else {
-              tma_tile<G>(ta, ma, bar, kb * 64, p * a_plane + m0);
+              tma_tile<G>(ta, ma, bar, kb * 64, p * plane + m0);
             }
+            if (conv) continue;
             uint8_t* tb = st + PL * C::kA + p * C::kB;
             if (kBMN) {
-              const int row = p * b_plane + (w ? 0 : v0) + kb * 64;
+              const int row = w ? p * plane + kb * 64 : a.v0 + kb * 64;
 #pragma unroll
               for (int i = 0; i < C::kOwnN / 64; ++i) tma_tile<G>(tb + i * 8192, mb, bar, n0 + 64 * i, row);
             } else {
-              tma_tile<G>(tb, mb, bar, kb * 64, p * b_plane + v0 + n0);
+              tma_tile<G>(tb, mb, bar, kb * 64, a.v0 + n0);
             }
           }
         }
@@ -677,7 +660,66 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
     if (elect()) commit_own<G>(&bars->done);
     __syncwarp();
     ptx::mbar_wait(&bars->done, 0, kBudget, nullptr);   // what was issued ends before the CTAs do
-  } else if (warp >= 4) {   // ---------------------------------------------- sums
+  } else if (kConv && warp >= 4 + kEpiWarps) {   // ------------------------ the head's planes
+    // A thread takes kPasses runs of eight values of a block: a run is 16 bytes of each
+    // plane's row, in the 128-byte swizzle that a tensor map's load would give it.
+    constexpr int kRunsRow = kBMN ? C::kBN / 8 : 8;           // runs in a row of the block
+    constexpr int kRowsPass = 32 * kConvWarps / kRunsRow, kPasses = (kBMN ? 64 : C::kBN) / kRowsPass;
+    const int t = threadIdx.x - 32 * (4 + kEpiWarps), run = t % kRunsRow, row0 = t / kRunsRow;
+    struct Block {   // a K block of an item
+      int item, n0, kb, end;
+      bool more;
+    };
+    auto open = [&](Block& x) {   // the next item's first block, if there is one
+      for (; x.item < n_items; x.item += groups) {
+        int m0, b0;
+        items.get(x.item, m0, x.n0, b0, x.end);
+        x.kb = b0;
+        if (b0 < x.end) return;
+      }
+      x.more = false;
+    };
+    auto next = [&](Block& x) {
+      if (++x.kb < x.end) return;
+      x.item += groups;
+      open(x);
+    };
+    // the head's value (row r, column c) of the block, nullptr behind its ends
+    auto at = [&](const Block& x, int r, int c) -> const float* {
+      const int v = kBMN ? x.kb * 64 + r : x.n0 + r, d = kBMN ? x.n0 + c : x.kb * 64 + c;
+      return x.more && !items.weight(x.item) && v < a.cols && d < pl.dim ? a.weight + (size_t)(a.v0 + v) * pl.dim + d : nullptr;
+    };
+    float4 buf[kPasses][2];   // of the block whose values are on their way
+    Block cur{group, 0, 0, 0, true};
+    open(cur);
+    auto fetch = [&](int p) {
+      const float4* src = reinterpret_cast<const float4*>(at(cur, row0 + p * kRowsPass, 8 * run));
+      buf[p][0] = src ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      buf[p][1] = src ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) fetch(p);
+    for (int it = 0; cur.more; ++it) {
+      const int s = it % S;
+      const bool skip = items.weight(cur.item);   // (that block's second operand comes by TMA)
+      next(cur);
+      if (it >= S && !__all_sync(0xffffffffu, ptx::mbar_wait(bars->empty + s, ((it / S) & 1) ^ 1, kBudget, pl.status))) break;
+      uint8_t* planes = sm + (size_t)s * C::kStage + PL * C::kA;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        if (!skip) {
+          const int r = row0 + p * kRowsPass;
+          const float v[8] = {buf[p][0].x, buf[p][0].y, buf[p][0].z, buf[p][0].w, buf[p][1].x, buf[p][1].y, buf[p][1].z, buf[p][1].w};
+          put8<PL>(reinterpret_cast<__nv_bfloat16*>(planes + (kBMN ? (run >> 3) * 8192 : 0) + r * 128 + (((run & 7) ^ (r & 7)) << 4)),
+                   C::kB / 2, v);
+        }
+        fetch(p);
+      }
+      ptx::fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bars->full + s);
+    }
+  } else if (warp >= 4 && warp < 4 + kEpiWarps) {   // ---------------------- sums
     constexpr int NC = C::kNC;
     const int half = (warp - 4) >> 2, lane_row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -753,7 +795,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ce_gemm_kernel(const __grid_c
             s += part;
             m = nm;
           }
-          pl.part[(size_t)(a.part0 + 2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
+          pl.part[(size_t)(2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
         }
       } else if constexpr (USE == kGrad) {
         const int left = in ? a.cols - col : 0, tgt = target - a.v0 - col;
@@ -931,7 +973,7 @@ cudaError_t gemm(const GemmArgs& a, const CUtensorMap& ma, const CUtensorMap& mb
   ++*launches;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(G * gemm_groups(G, sms));
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(gemm_threads<PL>());
   cfg.dynamicSmemBytes = GemmCfg<PL, G, BN>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -967,73 +1009,62 @@ Scale scale_of(float temperature) {
 int gather_rows(int rows) { return std::max(8, (rows + 1023) / 1024); }
 // (and at least as many as fill a tile's padding a row a warp)
 constexpr int kTilePad = 2 * kBM / (kGatherThreads / 32);
-int split_ctas(const CePlan& pl, int sms) {
-  return (int)std::min<long long>(sms * 6, ((long long)pl.piece * (pl.dim_pad / 8) + 1023) / 1024);
-}
-
 template <typename T, int PL, int G, int BN>
 cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   using C = GemmCfg<PL, G, BN>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
-  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
-                             pl, t, per, ctas, gemm_groups(G, sms));
+  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, false>, dim3(ctas), dim3(kGatherThreads), 0, s,
+                             pl, t, per, gemm_groups(G, sms));
   ++*launches;
   if (e != cudaSuccess) return e;
   CUtensorMap mh, mw;
-  bool ok = encode_activation_map(&mh, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM);
-  ok = ok && (PL == 1 ? encode_activation_map(&mw, t.weight, pl.dim, pl.vocab, pl.dim, C::kOwnN)
-                      : encode_activation_map(&mw, pl.w, pl.dim_pad, PL * pl.piece, pl.dim_pad, C::kOwnN));
-  if (!ok) return cudaErrorInvalidValue;
+  if (!encode_activation_map(&mh, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM)) return cudaErrorInvalidValue;
+  mw = mh;
+  if (PL == 1 && !encode_activation_map(&mw, t.weight, pl.dim, pl.vocab, pl.dim, C::kOwnN)) return cudaErrorInvalidValue;
   GemmArgs a{};
   a.pl = pl;
   const Scale sc = scale_of(t.temperature);
   a.scale2 = sc.hi;
   a.scale2_lo = sc.lo;
-  for (int v0 = 0; v0 < pl.vocab; v0 += pl.piece) {
-    a.v0 = v0;
-    a.cols = std::min(pl.piece, pl.vocab - v0);
-    if (PL == 3 && v0 > 0) {
-      e = launch_pdl(ce_split_weight_kernel, dim3(split_ctas(pl, sms)), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
-      ++*launches;
-      if (e != cudaSuccess) return e;
-    }
-    e = gemm<PL, G, BN, kStats>(a, mh, mw, mh, mw, mw, sms, launches, s);
-    if (e != cudaSuccess) return e;
-    a.part0 += 2 * ((a.cols + C::kBN - 1) / C::kBN);
-  }
+  a.weight = static_cast<const float*>(t.weight);
+  a.cols = pl.vocab;
+  e = gemm<PL, G, BN, kStats>(a, mh, mw, mh, mw, mw, sms, launches, s);
+  if (e != cudaSuccess) return e;
+  const int parts = 2 * ((pl.vocab + BN - 1) / BN);
   ++*launches;
   const bool few = pl.rows <= 4 * sms;
   return launch_pdl(few ? ce_merge_kernel<4> : ce_merge_kernel<32>, dim3(few ? (pl.rows + 3) / 4 : (pl.rows + 31) / 32),
-                    dim3(kMergeThreads), 0, s, pl, a.part0, t.loss, t.lse);
+                    dim3(kMergeThreads), 0, s, pl, parts, t.loss, t.lse);
 }
 
 template <typename T, int PL, int G, int BN>
 cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launches, cudaStream_t s) {
   using C = GemmCfg<PL, G, BN>;
   const int per = gather_rows(pl.rows), ctas = std::max((pl.rows + per - 1) / per, kTilePad);
-  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas + (PL == 3 ? split_ctas(pl, sms) : 0)), dim3(kGatherThreads), 0, s,
-                             pl, t, per, ctas, gemm_groups(G, sms));
+  cudaError_t e = launch_pdl(ce_gather_kernel<T, PL, true>, dim3(ctas), dim3(kGatherThreads), 0, s,
+                             pl, t, per, gemm_groups(G, sms));
   ++*launches;
   if (e != cudaSuccess) return e;
   // operands with the product's K along their rows (boxes of 64 x rows of the tile) or across them (64 x 64)
   CUtensorMap h_k, h_mn, w_k, w_mn, g_k, g_mn, g_out, dw_out{};
-  const void* w = PL == 1 ? t.weight : pl.w;
-  const int w_dim = PL == 1 ? pl.dim : pl.dim_pad, w_rows = PL == 1 ? pl.vocab : PL * pl.piece;
   if (!encode_activation_map(&h_k, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, kBM) ||
       !encode_activation_map(&h_mn, pl.h, pl.dim_pad, PL * pl.rows_pad, pl.dim_pad, 64) ||
-      !encode_activation_map(&w_k, w, w_dim, w_rows, w_dim, C::kOwnN) ||
-      !encode_activation_map(&w_mn, w, w_dim, w_rows, w_dim, 64) ||
       !encode_activation_map(&g_k, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, kBM) ||
       !encode_activation_map(&g_mn, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 64) ||
       !encode_activation_map(&g_out, pl.g, pl.piece, PL * pl.rows_pad, pl.piece, 32) ||
       (t.d_weight && !(PL == 1 ? encode_activation_map(&dw_out, t.d_weight, pl.dim, pl.vocab, pl.dim, 32)
                                : encode_f32_map(&dw_out, t.d_weight, pl.dim, pl.vocab, 32))))
     return cudaErrorInvalidValue;
+  w_k = w_mn = h_k;   // (fp32: not read)
+  if (PL == 1 && (!encode_activation_map(&w_k, t.weight, pl.dim, pl.vocab, pl.dim, C::kOwnN) ||
+                  !encode_activation_map(&w_mn, t.weight, pl.dim, pl.vocab, pl.dim, 64)))
+    return cudaErrorInvalidValue;
   GemmArgs a{};
   a.pl = pl;
   const Scale sc = scale_of(t.temperature);
   a.scale2 = sc.hi;
   a.scale2_lo = sc.lo;
+  a.weight = static_cast<const float*>(t.weight);
   a.d_hidden = t.d_hidden;
   a.d_row_stride = t.d_row_stride;
   // (the tiles of a piece's two gradients)
@@ -1043,11 +1074,6 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
     a.v0 = v0;
     a.cols = std::min(pl.piece, pl.vocab - v0);
     a.first = v0 == 0;
-    if (PL == 3 && v0 > 0) {
-      e = launch_pdl(ce_split_weight_kernel, dim3(split_ctas(pl, sms)), dim3(256), 0, s, pl, static_cast<const float*>(t.weight), v0);
-      ++*launches;
-      if (e != cudaSuccess) return e;
-    }
     if ((e = gemm<PL, G, BN, kGrad>(a, h_k, w_k, h_k, w_k, g_out, sms, launches, s)) != cudaSuccess) return e;
     if (both) {
       if ((e = gemm<PL, G, BN, kGrads>(a, g_k, w_mn, g_mn, h_mn, dw_out, sms, launches, s)) != cudaSuccess) return e;
@@ -1083,10 +1109,10 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.dim_pad = (dim + 63) / 64 * 64;
   const int bn = pl.bn;
   // pieces of equal size, as few as the limit allows
-  const size_t column = 2 * (size_t)pl.planes * (backward ? std::max(pl.rows_pad, f32 ? pl.dim_pad : 0) : pl.dim_pad);
+  const size_t column = 2 * (size_t)pl.planes * pl.rows_pad;
   const long long limit = std::max<long long>(256, (long long)(kPieceBytes / column) / 256 * 256);
   const long long all = ((long long)vocab + 255) / 256 * 256;
-  if (!backward && !f32) {
+  if (!backward) {
     pl.piece = (int)all;   // nothing is stored
   } else {
     const long long n = (all + limit - 1) / limit;
@@ -1106,10 +1132,8 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   pl.row_of = reinterpret_cast<int32_t*>(take(4 * R));
   pl.target = reinterpret_cast<int32_t*>(take(4 * R));
   pl.h = reinterpret_cast<__nv_bfloat16*>(take(2 * pl.planes * R * pl.dim_pad));
-  if (f32) pl.w = reinterpret_cast<__nv_bfloat16*>(take(6 * (size_t)pl.piece * pl.dim_pad));
   if (!backward) {
-    const size_t pieces = (size_t)((vocab + pl.piece - 1) / pl.piece);
-    pl.part = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * pieces * ((pl.piece + bn - 1) / bn) * R));
+    pl.part = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * (size_t)((vocab + bn - 1) / bn) * R));
     pl.picked = reinterpret_cast<float*>(take(4 * R));
   } else {
     pl.lse2 = reinterpret_cast<float2*>(take(8 * R));

@@ -24,7 +24,6 @@ struct CePlan {
   int32_t* row_of;       // [rows_pad] the caller's row
   int32_t* target;       // [rows_pad]
   __nv_bfloat16* h;      // [planes][rows_pad][dim_pad]; zero behind the dim and the last kept row's tile
-  __nv_bfloat16* w;      // [3][piece][dim_pad] a piece of the head (fp32 tensors)
   float2* part;          // forward: [parts][rows_pad] (maximum, sum) of each half tile of columns
   float* picked;         // forward: [rows_pad] the target's exponent
   float2* lse2;          // gradient: [rows_pad] lse log2(e) as a rounded value and its residual

@@ -151,8 +151,8 @@ __device__ void zero_fill(void* table, size_t bytes, int cta, int ctas) {
   char* p = static_cast<char*>(table);
   const size_t head = min(bytes, (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), vecs = (bytes - head) / 16;
   uint4* v = reinterpret_cast<uint4*>(p + head);
-  const size_t step = (size_t)ctas * kSortThreads;
-  for (size_t i = (size_t)cta * kSortThreads + threadIdx.x; i < vecs; i += step) __stcs(v + i, make_uint4(0, 0, 0, 0));
+  const size_t step = (size_t)ctas * blockDim.x;
+  for (size_t i = (size_t)cta * blockDim.x + threadIdx.x; i < vecs; i += step) __stcs(v + i, make_uint4(0, 0, 0, 0));
   if (cta == 0) {   // the ends, in the two bytes of the smaller type
     if (threadIdx.x < head / 2) reinterpret_cast<uint16_t*>(p)[threadIdx.x] = 0;
     const size_t tail = head + vecs * 16;
@@ -465,9 +465,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPla
 }
 
 // ---------------------------------------------------------------- few tokens
-// One launch: each CTA puts the tokens in order itself (by counting those before each)
-// and takes words of 32 table rows x 32 * W columns: a warp sums a token's rows in
-// order, eight warps together those of more than kSmallAlone.
+// One launch: each CTA puts the tokens in order itself (by counting those before each).
+// Words of 32 table rows that have a token are taken 32 * W columns at a time: a warp
+// sums a token's rows in order, eight warps together those of more than kSmallAlone; the
+// other words are zeroed as the bytes that they are.
 constexpr int kSmall = 256, kSmallWarps = 8, kSmallAlone = 16;
 
 template <typename TO, typename TT, bool VEC>
@@ -477,7 +478,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
   constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
   __shared__ alignas(16) uint64_t s_key[kSmall];
   __shared__ uint32_t s_token[kSmall + 1];
-  __shared__ uint16_t s_pos[kSmall];
+  __shared__ uint16_t s_pos[kSmall], s_first[kSmall];   // s_first: the first token of each word that has one
+  __shared__ int s_words;
   __shared__ Sum<W> s_sum[kSmallWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = pl.n;
   static_assert(kSmall == 32 * kSmallWarps, "a token a thread");
@@ -498,9 +500,38 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
   if (tid == 0) s_token[n] = ~0u;
   __syncthreads();
   const int words = (pl.vocab + 31) / 32, tiles = (pl.dim + 32 * W - 1) / (32 * W);
+  if (warp == 0) {
+    int count = 0;
+    for (int i = lane; i < (n + 31) / 32 * 32; i += 32) {
+      const bool first = i < n && s_token[i] < (unsigned)pl.vocab && (i == 0 || s_token[i] / 32 != s_token[i - 1] / 32);
+      const unsigned votes = __ballot_sync(0xffffffffu, first);
+      if (first) s_first[count + __popc(votes & ((1u << lane) - 1))] = (uint16_t)i;
+      count += __popc(votes);
+    }
+    if (lane == 0) s_words = count;
+  }
+  __syncthreads();
+  const int taken = s_words * tiles;
   const TO* d_out = static_cast<const TO*>(a.d_out);
-  for (long long item = blockIdx.x; item < (long long)words * tiles; item += gridDim.x) {
-    const int w = (int)(item / tiles), c = first_column<W, S>((int)(item - (long long)w * tiles) * 32 + lane), left = pl.dim - c;
+  // the first token that is at least v
+  auto find = [&](uint32_t v) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_token[mid] >= v) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+  };
+  for (int item = blockIdx.x; item < taken + (a.accumulate ? 0 : words); item += gridDim.x) {
+    if (item >= taken) {
+      const uint32_t v = (item - taken) * 32u;
+      const int at = find(v);
+      if (at < n && s_token[at] < min(v + 32, (unsigned)pl.vocab)) continue;
+      const size_t row = sizeof(TT) * (size_t)pl.dim;
+      zero_fill(static_cast<char*>(a.d_table) + v * row, min(32u, pl.vocab - v) * row, 0, 1);
+      continue;
+    }
+    const int w = s_token[s_first[item / tiles]] / 32, c = first_column<W, S>(item % tiles * 32 + lane), left = pl.dim - c;
     const bool in = c < pl.dim;
     TT* table = static_cast<TT*>(a.d_table) + c;
     auto add_rows = [&](Sum<W>& sum, int from, int to) {
@@ -514,15 +545,6 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
         for (int u = 0; u < U; ++u)
           if (k + u < to) sum.add(v[u]);
       }
-    };
-    // the first token that is at least v
-    auto find = [&](uint32_t v) {
-      int lo = 0, hi = n;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s_token[mid] >= v) hi = mid; else lo = mid + 1;
-      }
-      return lo;
     };
     int at = find(w * 32), end_word = find(min(w * 32 + 32, pl.vocab));
     const int rows = min(32, pl.vocab - w * 32);
@@ -593,8 +615,12 @@ int passes_of(int vocab) {
 }
 
 cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, size_t zero_bytes, int sms, cudaStream_t s) {
+  // More CTAs sort sooner (8,192 tokens: 16 us with two), but large clusters leave SMs
+  // without zeroing CTAs (1.2 GB: 186 us beside two, 198 beside eight): few beside a large
+  // table, whose zeroing takes longer anyway.
+  const int share = zero_bytes > (size_t)64 << 20 ? 4096 : 1024;
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 1024 < pl.n) ctas *= 2;
+  while (ctas < kMaxCluster && ctas * share < pl.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   // CTAs that zero: two an SM, fewer for a small table
   const long long zero = std::min<long long>(2 * sms, (long long)((zero_bytes + 65535) / 65536));
@@ -619,7 +645,7 @@ cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* la
   const int tiles32 = (pl.dim + 32 * W - 1) / (32 * W), words = (pl.vocab + 31) / 32;
   if (pl.n <= kSmall) {
     ++*launches;
-    return launch_pdl(embed_small_kernel<TO, TT, VEC>, dim3((unsigned)std::min<long long>((long long)words * tiles32, sms * 2)),
+    return launch_pdl(embed_small_kernel<TO, TT, VEC>, dim3((unsigned)std::min<long long>((long long)words + (long long)pl.n * tiles32, sms * 2)),
                       dim3(32 * kSmallWarps), 0, s, pl, a);
   }
   cudaError_t e = sort(pl, a.tokens, a.d_table, a.accumulate ? 0 : sizeof(TT) * (size_t)pl.vocab * pl.dim, sms, s);
