@@ -665,6 +665,7 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
     // plane's row, in the 128-byte swizzle that a tensor map's load would give it.
     constexpr int kRunsRow = kBMN ? C::kBN / 8 : 8;           // runs in a row of the block
     constexpr int kRowsPass = 32 * kConvWarps / kRunsRow, kPasses = (kBMN ? 64 : C::kBN) / kRowsPass;
+    static_assert(kRowsPass % 8 == 0 || PL != 3, "one swizzle a thread");
     const int t = threadIdx.x - 32 * (4 + kEpiWarps), run = t % kRunsRow, row0 = t / kRunsRow;
     struct Block {   // a K block of an item
       int item, n0, kb, end;
@@ -684,34 +685,39 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
       x.item += groups;
       open(x);
     };
-    // the head's value (row r, column c) of the block, nullptr behind its ends
-    auto at = [&](const Block& x, int r, int c) -> const float* {
-      const int v = kBMN ? x.kb * 64 + r : x.n0 + r, d = kBMN ? x.n0 + c : x.kb * 64 + c;
-      return x.more && !items.weight(x.item) && v < a.cols && d < pl.dim ? a.weight + (size_t)(a.v0 + v) * pl.dim + d : nullptr;
-    };
     float4 buf[kPasses][2];   // of the block whose values are on their way
     Block cur{group, 0, 0, 0, true};
     open(cur);
-    auto fetch = [&](int p) {
-      const float4* src = reinterpret_cast<const float4*>(at(cur, row0 + p * kRowsPass, 8 * run));
-      buf[p][0] = src ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-      buf[p][1] = src ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // where this thread's first run of the block lies, and how many of its rows there are
+    const size_t step = (size_t)kRowsPass * pl.dim;
+    const float* src = nullptr;
+    int left = 0;
+    auto aim = [&] {
+      const int v = kBMN ? cur.kb * 64 + row0 : cur.n0 + row0, d = 8 * run + (kBMN ? cur.n0 : cur.kb * 64);
+      left = cur.more && !items.weight(cur.item) && d < pl.dim ? a.cols - v : 0;
+      src = a.weight + (size_t)(a.v0 + v) * pl.dim + d;
     };
+    auto fetch = [&](int p) {
+      const bool in = p * kRowsPass < left;
+      const float4* x = reinterpret_cast<const float4*>(src + p * step);
+      buf[p][0] = in ? __ldg(x) : make_float4(0.f, 0.f, 0.f, 0.f);
+      buf[p][1] = in ? __ldg(x + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    uint8_t* const planes = sm + PL * C::kA + row0 * 128 + (((run & 7) ^ (row0 & 7)) << 4) + (kBMN ? (run >> 3) * 8192 : 0);
+    aim();
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) fetch(p);
     for (int it = 0; cur.more; ++it) {
       const int s = it % S;
       const bool skip = items.weight(cur.item);   // (that block's second operand comes by TMA)
       next(cur);
+      aim();
       if (it >= S && !__all_sync(0xffffffffu, ptx::mbar_wait(bars->empty + s, ((it / S) & 1) ^ 1, kBudget, pl.status))) break;
-      uint8_t* planes = sm + (size_t)s * C::kStage + PL * C::kA;
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
-        if (!skip) {
-          const int r = row0 + p * kRowsPass;
+        if (!skip) {   // (rows 8 apart have the same swizzle)
           const float v[8] = {buf[p][0].x, buf[p][0].y, buf[p][0].z, buf[p][0].w, buf[p][1].x, buf[p][1].y, buf[p][1].z, buf[p][1].w};
-          put8<PL>(reinterpret_cast<__nv_bfloat16*>(planes + (kBMN ? (run >> 3) * 8192 : 0) + r * 128 + (((run & 7) ^ (r & 7)) << 4)),
-                   C::kB / 2, v);
+          put8<PL>(reinterpret_cast<__nv_bfloat16*>(planes + (size_t)s * C::kStage + p * kRowsPass * 128), C::kB / 2, v);
         }
         fetch(p);
       }
