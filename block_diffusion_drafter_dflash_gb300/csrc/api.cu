@@ -1709,6 +1709,17 @@ int32_t dflash_linear_cross_entropy(const void* hidden, int32_t dtype, int64_t r
   int32_t rc = ce_check(hidden, row_stride, weight, targets, rows, dim, vocab, dtype, temperature, workspace);
   if (rc) return rc;
   if (rows > 0 && (!loss || !lse)) return fail(DFLASH_ERR_INVALID_ARG, "loss or lse is NULL");
+  if (reinterpret_cast<uintptr_t>(loss) % 4 || reinterpret_cast<uintptr_t>(lse) % 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "loss or lse is not aligned to its type");
+  {
+    const long long es = dtype == DFLASH_DTYPE_F32 ? 4 : 2;
+    const Span out[2] = {Span(loss, rows, 4, 4), Span(lse, rows, 4, 4)};
+    const Span in[3] = {Span(hidden, rows, row_stride * es, dim * es), Span(weight, vocab, dim * es, dim * es), Span(targets, rows, 4, 4)};
+    if (overlap(out[0], out[1])) return fail(DFLASH_ERR_INVALID_ARG, "loss and lse overlap");
+    for (const Span& o : out)
+      for (const Span& i : in)
+        if (overlap(o, i)) return fail(DFLASH_ERR_INVALID_ARG, "loss or lse overlaps an operand");
+  }
   const int sms = current_sms();
   if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
   const bool f32 = dtype == DFLASH_DTYPE_F32;
@@ -1754,6 +1765,9 @@ int32_t dflash_linear_cross_entropy_backward(const void* hidden, int32_t dtype, 
   const bool same = d_hidden == hidden && (rows <= 1 || row_stride == d_row_stride);
   if ((!same && overlap(dh, h)) || overlap(dh, w) || overlap(dw, h) || overlap(dw, w) || overlap(dh, dw))
     return fail(DFLASH_ERR_INVALID_ARG, "a gradient overlaps an operand or the other gradient");
+  for (const void* p : {static_cast<const void*>(targets), static_cast<const void*>(lse), static_cast<const void*>(d_loss)})
+    if (overlap(dh, Span(p, rows, 4, 4)) || overlap(dw, Span(p, rows, 4, 4)))
+      return fail(DFLASH_ERR_INVALID_ARG, "a gradient overlaps targets, lse or d_loss");
   const int sms = current_sms();
   if (sms <= 0) return fail(DFLASH_ERR_CUDA, "no current device");
   const CePlan pl = ce_plan(workspace, std::max(rows, 1), dim, vocab, f32, true, true, sms);

@@ -155,6 +155,29 @@ def test_infinities_and_nan_stay_in_their_row():
     assert bool(d.isfinite().all())
 
 
+def test_a_table_past_32_bits():
+    """2.4 G values: a lookup and a gradient in rows behind 2^31, among them the last; rows of zeros everywhere else."""
+    V, D, n = 590_000, 4096, 700
+    g = torch.Generator(device="cuda").manual_seed(8)
+    t = torch.randint(V - 3000, V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    t[:3] = torch.tensor([V - 1, 0, V - 1])
+    table = torch.zeros((V, D), dtype=BF16, device="cuda")
+    table[t.long()] = torch.randn((n, D), generator=g, device="cuda").to(BF16)
+    out = torch.empty((n, D), dtype=BF16, device="cuda")
+    _df().dflash_embed_tokens(table, t, out)
+    assert torch.equal(out, table[t.long()])
+    d_out = torch.randn((n, D), generator=g, device="cuda")
+    for k in (n, 200):                                    # the sorted form, and the one launch of few tokens
+        table.fill_(7.0)
+        d = backward(d_out[:k], t[:k], V, BF16, ws=_df().dflash_embed_tokens_backward_workspace(k, D, V))
+        low, high = d[:1], d[V - 3000:]
+        check(low, d_out[1:2], torch.zeros(1, dtype=torch.int32, device="cuda"), 1, 1.0)
+        rest = torch.where(t[:k] >= V - 3000, t[:k] - (V - 3000), -1)
+        check(high, d_out[:k], rest, 3000, 1.0)
+        assert not bool(d[1:V - 3000].any())
+        del d
+
+
 def test_long_runs_keep_fp32():
     """120,000 terms of one token whose sum is a thousandth of their absolute values' root of squares."""
     n, D = 120000, 16

@@ -157,6 +157,57 @@ def test_vocabularies_of_several_pieces(dtype, R, D, V):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R,D,V", [(3, 65536, 100), (1 << 20, 8, 20), (1, 8, 70001)])
+def test_the_largest_dim_and_row_count_and_the_smallest_dim(R, D, V, dtype):
+    h, w, t = operands(R, D, V, dtype, 6, ignored=0.0 if R < 10 else 0.1)
+    got = forward(h, w, t)
+    check_forward(h, w, t, 1.0, got)
+    d_loss = torch.rand(R, device="cuda") / R
+    check_backward(h, w, t, 1.0, got[1], d_loss, backward(h, w, t, got[1], d_loss))
+
+
+def test_a_head_past_32_bits():
+    """A head of 2.4 G values, its gradient and a piece's first row past 2^31; the rows' own logits in 64 bits."""
+    R, D, V = 3, 4096, 590_000
+    g = torch.Generator(device="cuda").manual_seed(30)
+    w = torch.empty((V, D), dtype=BF16, device="cuda")
+    for v in range(0, V, 65536):
+        w[v:v + 65536] = torch.randn((min(65536, V - v), D), generator=g, device="cuda") / math.sqrt(D)
+    t = torch.tensor([V - 1, 7, 550_000], dtype=torch.int32, device="cuda")
+    h = (torch.randn((R, D), generator=g, device="cuda") + 8 * w[t.long()].float()).to(BF16)
+    got = forward(h, w, t)
+    z = torch.cat([h.double() @ w[v:v + 65536].double().t() for v in range(0, V, 65536)], dim=1)
+    a = torch.cat([h.double().abs() @ w[v:v + 65536].double().abs().t() for v in range(0, V, 65536)], dim=1)
+    lse = torch.logsumexp(z, dim=1)
+    p = torch.softmax(z, dim=1)
+    dz = _c(D) * a + 3 * U * z.abs()
+    e = dz + 3 * U * lse[:, None].abs() + 4 * U
+    d_lse = (p * e).sum(1) + U * (32 + 8 + 2 * (V / 128 + 1) / 16 + 16) + 2 * U * (lse.abs() + 1)
+    assert bool(((got[1].double() - lse).abs() <= d_lse).all())
+    picked = z.gather(1, t.long()[:, None])[:, 0]
+    tol = d_lse + dz.gather(1, t.long()[:, None])[:, 0] + 3 * U * (lse.abs() + picked.abs())
+    assert bool(((got[0].double() - (lse - picked)).abs() <= tol).all())
+    d_loss = torch.tensor([0.5, -1.0, 2.0], device="cuda")
+    d_h, d_w = backward(h, w, t, lse.float(), d_loss)
+    p[torch.arange(R), t.long()] -= 1.0
+    gr = p * d_loss.double()[:, None]
+    dg = d_loss.double().abs()[:, None] * torch.softmax(z, dim=1) * (torch.expm1(e + U * lse.abs()[:, None]) + 2 * U) + 3 * U * gr.abs()
+    dg = dg + _half_step(BF16) * (gr.abs() + dg) + 3 * 2.0 ** -126
+    rows = torch.cat([torch.arange(0, 200), torch.arange(549_900, 550_100), torch.arange(V - 200, V)]).cuda()
+    want = gr[:, rows].t() @ h.double()
+    tol = dg[:, rows].t() @ h.double().abs() + _c(R) * (gr.abs() + dg)[:, rows].t() @ h.double().abs()
+    tol = tol + _half_step(BF16) * (want.abs() + tol)
+    assert bool(((d_w[rows].double() - want).abs() <= tol).all())
+    want, tol = 0.0, 0.0
+    for v in range(0, V, 65536):
+        x = w[v:v + 65536].double()
+        want = want + gr[:, v:v + 65536] @ x
+        tol = tol + dg[:, v:v + 65536] @ x.abs() + (_c(V) + 80 * U) * ((gr.abs() + dg)[:, v:v + 65536] @ x.abs())
+    tol = tol + _half_step(BF16) * (want.abs() + tol)
+    assert bool(((d_h.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pad,offset,temp", [(8, 0, 0.7), (3, 0, 1.5), (1, 1, 1.0), (40, 8, 1.0)])
 def test_strides_alignment_and_temperature(dtype, pad, offset, temp):
     R, D, V = 200, 136, 777

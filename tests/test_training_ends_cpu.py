@@ -28,7 +28,10 @@ SHARED = [
 ]
 
 
-@pytest.mark.parametrize("kw,code", SHARED + [(dict(loss=None), -1), (dict(lse=None), -1)])
+@pytest.mark.parametrize("kw,code", SHARED + [
+    (dict(loss=None), -1), (dict(lse=None), -1), (dict(loss=4 * P + 2), -1),
+    (dict(loss=5 * P + 4), -1), (dict(loss=P + 64), -1), (dict(lse=2 * P), -1), (dict(lse=3 * P + 4), -1),   # one over another
+])
 def test_loss_refusals(L, kw, code):  # noqa: F811
     assert _loss(L, **kw) == code
     assert len(L.dflash_last_error()) > 0
@@ -46,6 +49,7 @@ def _loss_grad(L, hidden=P, dtype=0, stride=16, weight=2 * P, targets=3 * P, row
     (dict(d_hidden=P + 4), -1), (dict(d_hidden=P, d_stride=17), -1),     # the hidden states' place, but not their rows
     (dict(d_hidden=2 * P + 64), -1), (dict(d_weight=2 * P), -1), (dict(d_weight=P + 16), -1),
     (dict(d_hidden=8 * P + 16), -1),                                     # the other gradient
+    (dict(d_hidden=4 * P), -1), (dict(d_weight=5 * P), -1), (dict(d_hidden=3 * P + 4), -1),     # lse, d_loss, targets
 ])
 def test_loss_gradient_refusals(L, kw, code):  # noqa: F811
     assert _loss_grad(L, **kw) == code
