@@ -132,7 +132,8 @@ constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMaxCluster = 8;
 constexpr int kBatch = 8;   // steps of 32 pairs that a warp loads together
-constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + kMaxCluster + 1);
+constexpr int kHeld = kSortThreads * kBatch;   // pairs that a CTA can hold
+constexpr size_t kSortBytes = sizeof(uint32_t) * kBins * (kSortWarps + kMaxCluster + 1) + sizeof(uint2) * kHeld;
 
 // The lanes that have this lane's digit (kBins: none), by a vote on each bit.
 __device__ __forceinline__ unsigned same_digit(unsigned d) {
@@ -152,6 +153,7 @@ __device__ void zero_fill(void* table, size_t bytes, int cta, int ctas) {
   const size_t head = min(bytes, (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), vecs = (bytes - head) / 16;
   uint4* v = reinterpret_cast<uint4*>(p + head);
   const size_t step = (size_t)ctas * blockDim.x;
+#pragma unroll 4
   for (size_t i = (size_t)cta * blockDim.x + threadIdx.x; i < vecs; i += step) __stcs(v + i, make_uint4(0, 0, 0, 0));
   if (cta == 0) {   // the ends, in the two bytes of the smaller type
     if (threadIdx.x < head / 2) reinterpret_cast<uint16_t*>(p)[threadIdx.x] = 0;
@@ -160,12 +162,14 @@ __device__ void zero_fill(void* table, size_t bytes, int cta, int ctas) {
   }
 }
 
-// The first cluster sorts, the others zero the gradient.  Each warp owns a contiguous share of the pairs.  A pass counts its
-// digits, turns the counts into places (digits first, then CTAs, then warps, so equal
-// digits keep their order) and moves the pairs.  Tokens outside the vocabulary sort
-// behind all others.
+// The first cluster sorts, the others zero the gradient.  Each warp owns a contiguous
+// share of the pairs.  A pass ranks them by digit within the warp, turns the warps'
+// counts into places (digits first, then CTAs, then warps, so equal digits keep their
+// order) and moves the pairs.  Tokens outside the vocabulary sort behind all others.
+// Up to kHeld pairs a CTA stay in registers within a pass and in the cluster's shared
+// memory between passes; more go through memory.
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPlan pl, const int32_t* tokens, int passes, void* table,
-                                                                         size_t zero_bytes) {
+                                                                     size_t zero_bytes) {
   griddep_wait();
   griddep_trigger();
   cg::cluster_group cluster = cg::this_cluster();
@@ -174,47 +178,69 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
     zero_fill(table, zero_bytes, blockIdx.x - ctas, gridDim.x - ctas);
     return;
   }
-  extern __shared__ uint32_t sh[];
-  uint32_t* count = sh;                          // [warps][bins]
-  uint32_t* total = sh + kBins * kSortWarps;     // [CTAs][bins] of every CTA
-  uint32_t* place = total + kBins * kMaxCluster; // [bins] first place of the CTA's pairs
-  __shared__ uint32_t s_scan[kBins / 32];
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  uint2* held = reinterpret_cast<uint2*>(sort_smem);                 // [kHeld]
+  uint32_t* count = reinterpret_cast<uint32_t*>(held + kHeld);       // [warps][bins]
+  uint32_t* total = count + kBins * kSortWarps;                      // [CTAs][bins] of every CTA
+  uint32_t* place = total + kBins * kMaxCluster;                     // [bins] first place of the CTA's pairs
+  __shared__ uint32_t s_scan[kBins / 32], s_valid, s_valids[kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned below = (1u << lane) - 1;
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // all CTAs run before any is written to
   const long long all_warps = (long long)ctas * kSortWarps, me = (long long)cta * kSortWarps + warp;
-  const int share = (int)(((pl.n + all_warps - 1) / all_warps + 31) / 32 * 32);
+  const int share = (int)(((pl.n + all_warps - 1) / all_warps + 31) / 32 * 32);   // of a warp
   const int beg = (int)min((long long)pl.n, me * share), end = (int)min((long long)pl.n, (me + 1) * share);
-  if (cta == 0 && tid == 0) *pl.kept = 0;
+  const bool hold = share <= 32 * kBatch;
+  const unsigned of_cta = (unsigned)share * kSortWarps;   // (at most kHeld if held)
+  if (tid == 0) s_valid = 0;
+  uint2 p[kBatch];
+  uint32_t rank[kBatch];
   for (int pass = 0; pass < passes; ++pass) {
-    const bool last_odd = (passes - pass) & 1;   // the last pass writes `order`
+    const bool last = pass == passes - 1, last_odd = (passes - pass) & 1;   // the last pass writes `order`
     const uint2* src = last_odd ? pl.spare : pl.order;
     uint2* dst = last_odd ? pl.order : pl.spare;
     const int shift = pass * kDigitBits;
-    auto pair_at = [&](int i) {
-      if (pass) return src[i];
-      const unsigned t = tokens[i];
-      return make_uint2(min(t, (unsigned)pl.vocab), i);
-    };
-    for (int i = tid; i < kBins * kSortWarps; i += kSortThreads) count[i] = 0;
-    __syncthreads();
-    uint32_t* mine = count + warp * kBins;
-    uint2 p[kBatch];
     auto load_batch = [&](int i) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (i + u * 32 + lane < end) p[u] = pair_at(i + u * 32 + lane);
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = i + u * 32 + lane;
+        if (k < end) {
+          if (pass == 0) p[u] = make_uint2(min((unsigned)tokens[k], (unsigned)pl.vocab), k);
+          else p[u] = hold ? held[k - cta * of_cta] : src[k];
+        }
+      }
     };
-    for (int i = beg; i < end; i += 32 * kBatch) {
-      load_batch(i);
+    // this batch's ranks among the warp's equal digits; `mine`: what comes before
+    uint32_t* mine = count + warp * kBins;
+    auto rank_batch = [&](int i) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         if (i + u * 32 < end) {
           const bool in = i + u * 32 + lane < end;
           const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
           const unsigned same = same_digit(d);
-          if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
+          const uint32_t before = in ? mine[d] : 0;
+          rank[u] = before + __popc(same & below);
+          __syncwarp();
+          if (in && (same & below) == 0) mine[d] = before + __popc(same);
           __syncwarp();
         }
+    };
+    load_batch(beg);
+    for (int i = tid; i < kBins * kSortWarps; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    uint32_t valid = 0;
+    for (int i = beg; i < end; i += 32 * kBatch) {
+      if (i != beg) load_batch(i);
+      rank_batch(i);
+      if (pass == 0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) valid += i + u * 32 + lane < end && p[u].x < (unsigned)pl.vocab;
+      }
+    }
+    if (pass == 0) {
+      valid = __reduce_add_sync(0xffffffffu, valid);
+      if (lane == 0 && valid) atomicAdd(&s_valid, valid);
     }
     __syncthreads();
     if (pass == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -228,7 +254,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
       }
       for (int c = 0; c < ctas; ++c) cluster.map_shared_rank(total, c)[cta * kBins + tid] = sum;
     }
-    cluster.sync();
+    if (pass == 0 && tid == kBins) cluster.map_shared_rank(s_valids, 0)[cta] = s_valid;
+    cluster.sync();   // totals are there, and all pairs of the pass in registers (if held)
+    if (pass == 0 && cta == 0 && tid == kBins) {
+      uint32_t sum = 0;
+      for (int c = 0; c < ctas; ++c) sum += s_valids[c];
+      *pl.kept = (int)sum;
+    }
     uint32_t before = 0, all = 0, run = 0;
     if (tid < kBins) {
       for (int c = 0; c < ctas; ++c) {
@@ -245,29 +277,31 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPla
     }
     __syncthreads();
     if (tid < kBins) {
-      for (int w = 0; w < warp; ++w) run += s_scan[w];
+#pragma unroll
+      for (int w = 0; w < kBins / 32; ++w) run += w < warp ? s_scan[w] : 0;
       place[tid] = run - all + before;
     }
     __syncthreads();
     for (int i = beg; i < end; i += 32 * kBatch) {
-      if (share > 32 * kBatch) load_batch(i);   // (otherwise they are still here)
+      if (!hold) {   // again, from the warp's first place on
+        load_batch(i);
+        rank_batch(i);
+      }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        if (i + u * 32 < end) {
-          const bool in = i + u * 32 + lane < end;
-          const unsigned d = in ? p[u].x >> shift & (kBins - 1) : kBins;
-          const unsigned same = same_digit(d);
-          if (in) dst[place[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p[u];
-          __syncwarp();
-          if (in && lane == __ffs(same) - 1) mine[d] += __popc(same);
-          __syncwarp();
+        if (i + u * 32 + lane < end) {
+          const unsigned d = p[u].x >> shift & (kBins - 1);
+          const unsigned to = place[d] + rank[u] + (hold ? mine[d] : 0);
+          if (last || !hold) dst[to] = p[u];
+          else cluster.map_shared_rank(held, to / of_cta)[to % of_cta] = p[u];
         }
     }
-    cluster.sync();   // the pairs are where the next pass reads them, and `total` may change
+    // the pairs are where the next pass reads them, and `total` may change (the last
+    // pass ends with the kernel)
+    if (!last) cluster.sync();
   }
-  const uint2* got = pl.order;
-  for (int i = beg + lane; i < end; i += 32)
-    if (got[i].x < (unsigned)pl.vocab && (i == pl.n - 1 || got[i + 1].x >= (unsigned)pl.vocab)) *pl.kept = i + 1;
+  // no CTA leaves while another may still write its totals or pairs: the last pass' writes
+  // to shared memory lie before its cluster.sync
 }
 
 // ---------------------------------------------------------------- sums
@@ -615,10 +649,10 @@ int passes_of(int vocab) {
 }
 
 cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, size_t zero_bytes, int sms, cudaStream_t s) {
-  // More CTAs sort sooner (8,192 tokens: 16 us with two), but large clusters leave SMs
-  // without zeroing CTAs (1.2 GB: 186 us beside two, 198 beside eight): few beside a large
-  // table, whose zeroing takes longer anyway.
-  const int share = zero_bytes > (size_t)64 << 20 ? 4096 : 1024;
+  // CTAs that sort: as few as hold the pairs beside a large table (zeroing 1.2 GB takes
+  // 186 us beside two, 198 beside eight, which leave SMs without a CTA that zeroes);
+  // otherwise as many as have a step a warp to do (5,470 tokens: 17 us with one).
+  const int share = zero_bytes > (size_t)64 << 20 ? kHeld : kSortThreads;
   int ctas = 1;
   while (ctas < kMaxCluster && ctas * share < pl.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
