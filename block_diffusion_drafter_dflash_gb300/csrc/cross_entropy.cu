@@ -99,6 +99,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// two fp32 values at once
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t r, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // ---------------------------------------------------------------- planes
 // Two values as a register of two bf16, the first in the lower half.
 __device__ __forceinline__ uint32_t pack_rn(float x, float y) {
@@ -762,7 +785,8 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
             float v[16];
             ptx::tmem_ld16(at + j0, v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j0 + j] += v[j];
+            for (int j = 0; j < 16; j += 2)
+              split2(add2(two(acc[j0 + j], acc[j0 + j + 1]), two(v[j], v[j + 1])), acc[j0 + j], acc[j0 + j + 1]);
           }
         };
         if (PL == 3 && (++sums == C::kSmallSums || kb + C::kSumBlocks >= b1)) {
@@ -778,40 +802,66 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
       if (!ok) break;
       const int col = n0 + c_half;     // within the piece, or the dim
       if constexpr (USE == kStats) {
-        if (in) {
-          const int left = a.cols - col;                     // columns that there are
-          const int tgt = target - a.v0 - col;
-          float m = -INFINITY, s = 0.f;
+        const int left = a.cols - col;                     // columns that there are
+        const int tgt = target - a.v0 - col;
+        const uint64_t scale = two(a.scale2, a.scale2);
 #pragma unroll
-          for (int j0 = 0; j0 < NC; j0 += 32) {
-            if (j0 >= left) break;
-            float gm = -INFINITY;
+        for (int j = 0; j < NC; j += 2) split2(mul2(two(acc[j], acc[j + 1]), scale), acc[j], acc[j + 1]);
+        if (left < NC) {
 #pragma unroll
-            for (int j = j0; j < j0 + 32; ++j) {
-              acc[j] *= a.scale2;
-              if (j >= left) acc[j] = -INFINITY;
-              if (j == tgt) pl.picked[row] = acc[j];
-              gm = fmaxf(gm, acc[j]);
-            }
-            const float nm = fmaxf(m, gm), ref = nm == -INFINITY ? 0.f : nm;
-            s *= ex2(m - ref);
-            float part = 0.f;
-#pragma unroll
-            for (int j = j0; j < j0 + 32; ++j) part += ex2(acc[j] - ref);
-            s += part;
-            m = nm;
-          }
-          pl.part[(size_t)(2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
+          for (int j = 0; j < NC; ++j)
+            if (j >= left) acc[j] = -INFINITY;
         }
+        if (__any_sync(0xffffffffu, in && (unsigned)tgt < (unsigned)NC)) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (in && j == tgt) pl.picked[row] = acc[j];
+        }
+        float m = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int j0 = 0; j0 < NC; j0 += 32) {
+          float gm = acc[j0];
+#pragma unroll
+          for (int j = j0 + 1; j < j0 + 32; ++j) gm = fmaxf(gm, acc[j]);
+          const float nm = fmaxf(m, gm), ref = nm == -INFINITY ? 0.f : nm;
+          s *= ex2(m - ref);
+          const uint64_t less = two(-ref, -ref);
+          float part[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = j0; j < j0 + 32; j += 2) {
+            float x, y;
+            split2(add2(two(acc[j], acc[j + 1]), less), x, y);
+            part[0] += ex2(x);
+            part[1] += ex2(y);
+          }
+          s += part[0] + part[1];
+          m = nm;
+        }
+        if (in) pl.part[(size_t)(2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
       } else if constexpr (USE == kGrad) {
         const int left = in ? a.cols - col : 0, tgt = target - a.v0 - col;
+        const uint64_t scale = two(a.scale2, a.scale2), less = two(-l2.x, -l2.x);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          float e = fmaf(acc[j], a.scale2, -l2.x);
-          if (PL == 3) e = fmaf(acc[j], a.scale2_lo, e - l2.y);
-          e = ex2(e);
-          if (j == tgt) e -= 1.f;
-          acc[j] = j < left ? gain * e : 0.f;
+        for (int j = 0; j < NC; j += 2) {
+          const uint64_t z = two(acc[j], acc[j + 1]);
+          uint64_t e = fma2(z, scale, less);
+          if (PL == 3) e = fma2(z, two(a.scale2_lo, a.scale2_lo), add2(e, two(-l2.y, -l2.y)));
+          split2(e, acc[j], acc[j + 1]);
+          acc[j] = ex2(acc[j]);
+          acc[j + 1] = ex2(acc[j + 1]);
+        }
+        if (__any_sync(0xffffffffu, (unsigned)tgt < (unsigned)NC)) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (j == tgt) acc[j] -= 1.f;
+        }
+        const uint64_t times = two(gain, gain);
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) split2(mul2(two(acc[j], acc[j + 1]), times), acc[j], acc[j + 1]);
+        if (__any_sync(0xffffffffu, left < NC)) {   // behind the head's last row, and rows behind the kept ones
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (j >= left) acc[j] = 0.f;
         }
 #pragma unroll
         for (int p = 0; p < PL; ++p) {   // a plane, then what it leaves
