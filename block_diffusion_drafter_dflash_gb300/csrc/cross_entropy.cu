@@ -429,6 +429,25 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return done != 0;
 }
+// 32 columns of this warp's lanes; used after tmem_loaded.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// Waits for this thread's loads; no use of the n values moves before it.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < N; ++j) asm volatile("" : "+f"(v[j]));
+}
 template <int G>
 __device__ __forceinline__ void sync_tile_ctas() {
   if constexpr (G == 2) {
@@ -768,8 +787,10 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
       const float2 l2 = USE == kGrad && in ? pl.lse2[row] : make_float2(0.f, 0.f);
       const float gain = USE == kGrad && in ? pl.gain[row] : 0.f;
       float acc[NC];
+      if (b0 == b1) {
 #pragma unroll
-      for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+        for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+      }
       int sums = 0;
       for (int kb = b0; kb < b1; kb += C::kSumBlocks, ++seq) {
         const int buf = seq & 1;
@@ -789,12 +810,19 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
               split2(add2(two(acc[j0 + j], acc[j0 + j + 1]), two(v[j], v[j + 1])), acc[j0 + j], acc[j0 + j + 1]);
           }
         };
+        const uint32_t at = tmem + lanes + buf * C::kAccCols + c_half;
+        if (kb == b0) {   // the first sum as it is
+#pragma unroll
+          for (int j0 = 0; j0 < NC; j0 += 32) tmem_load32(at + j0, acc + j0);
+          tmem_loaded<NC>(acc);
+        } else {
+          drain(at);
+        }
         if (PL == 3 && (++sums == C::kSmallSums || kb + C::kSumBlocks >= b1)) {
           drain(tmem + lanes + (2 + (small_seq & 1)) * C::kAccCols + c_half);
           sums = 0;
           ++small_seq;
         }
-        drain(tmem + lanes + buf * C::kAccCols + c_half);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(free0 + buf * 8);
