@@ -414,8 +414,12 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
                "r"(ptx::smem_u32(src)), "r"(x), "r"(y)
                : "memory");
 }
+// Arrival at a barrier of the pair's first CTA.  It says that this warp has read its part of
+// tensor memory (tcgen05.wait::ld and the fence before it see to that) and hands over no
+// other memory, so it releases at the scope of the CTA: at the cluster's it would wait for
+// the epilogue's global stores at every sum.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // As ptx::mbar_try_wait, for what a thread of the other CTA did before it arrived.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -776,16 +780,39 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
     const uint32_t free0 = G == 2 ? at_rank(bars->acc_free, 0) : ptx::smem_u32(bars->acc_free);
     int seq = 0, small_seq = 0;
     bool ok = true;
+    // what a row needs at the end of its tile, loaded while the tile before is at work
+    struct Row {
+      int target;
+      float2 l2;
+      float gain;
+    };
+    auto row_of_item = [&](int item) {
+      Row r{-1, make_float2(0.f, 0.f), 0.f};
+      if ((USE == kStats || USE == kGrad) && item < n_items) {
+        int m0, n0, b0, b1;
+        items.get(item, m0, n0, b0, b1);
+        const int row = m0 + rank * kBM + lane_row;
+        if (row < kept) {
+          r.target = pl.target[row];
+          if (USE == kGrad) {
+            r.l2 = pl.lse2[row];
+            r.gain = pl.gain[row];
+          }
+        }
+      }
+      return r;
+    };
+    Row next = row_of_item(group);
     for (int item = group; item < n_items && ok; item += groups) {
       int m0, n0, b0, b1;
       items.get(item, m0, n0, b0, b1);
       m0 += rank * kBM;
       const int row = m0 + lane_row;   // (a vocabulary row of the piece for the head's gradient)
-      // what the row needs at the end
       const bool in = (USE == kStats || USE == kGrad) && row < kept;
-      const int target = in ? pl.target[row] : -1;
-      const float2 l2 = USE == kGrad && in ? pl.lse2[row] : make_float2(0.f, 0.f);
-      const float gain = USE == kGrad && in ? pl.gain[row] : 0.f;
+      const int target = next.target;
+      const float2 l2 = next.l2;
+      const float gain = next.gain;
+      next = row_of_item(item + groups);
       float acc[NC];
       if (b0 == b1) {
 #pragma unroll
@@ -867,38 +894,40 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
         }
         if (in) pl.part[(size_t)(2 * (n0 / C::kBN) + half) * pl.rows_pad + row] = make_float2(m, s);
       } else if constexpr (USE == kGrad) {
-        const int left = in ? a.cols - col : 0, tgt = target - a.v0 - col;
-        const uint64_t scale = two(a.scale2, a.scale2), less = two(-l2.x, -l2.x);
+        // 64 columns at a time: one half's values are made while the other's leave
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-          const uint64_t z = two(acc[j], acc[j + 1]);
-          uint64_t e = fma2(z, scale, less);
-          if (PL == 3) e = fma2(z, two(a.scale2_lo, a.scale2_lo), add2(e, two(-l2.y, -l2.y)));
-          split2(e, acc[j], acc[j + 1]);
-          acc[j] = ex2(acc[j]);
-          acc[j + 1] = ex2(acc[j + 1]);
-        }
-        if (__any_sync(0xffffffffu, (unsigned)tgt < (unsigned)NC)) {
+        for (int h = 0; h < NC; h += 64) {
+          float* g = acc + h;
+          const int left = in ? a.cols - col - h : 0, tgt = target - a.v0 - col - h;
+          const uint64_t scale = two(a.scale2, a.scale2), less = two(-l2.x, -l2.x), times = two(gain, gain);
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (j == tgt) acc[j] -= 1.f;
-        }
-        const uint64_t times = two(gain, gain);
+          for (int j = 0; j < 64; j += 2) {
+            const uint64_t z = two(g[j], g[j + 1]);
+            uint64_t e = fma2(z, scale, less);
+            if (PL == 3) e = fma2(z, two(a.scale2_lo, a.scale2_lo), add2(e, two(-l2.y, -l2.y)));
+            split2(e, g[j], g[j + 1]);
+            g[j] = ex2(g[j]);
+            g[j + 1] = ex2(g[j + 1]);
+          }
+          if (__any_sync(0xffffffffu, (unsigned)tgt < 64u)) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) split2(mul2(two(acc[j], acc[j + 1]), times), acc[j], acc[j + 1]);
-        if (__any_sync(0xffffffffu, left < NC)) {   // behind the head's last row, and rows behind the kept ones
+            for (int j = 0; j < 64; ++j)
+              if (j == tgt) g[j] -= 1.f;
+          }
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (j >= left) acc[j] = 0.f;
-        }
+          for (int j = 0; j < 64; j += 2) split2(mul2(two(g[j], g[j + 1]), times), g[j], g[j + 1]);
+          if (__any_sync(0xffffffffu, left < 64)) {   // behind the head's last row, and rows behind the kept ones
 #pragma unroll
-        for (int p = 0; p < PL; ++p) {   // a plane, then what it leaves
+            for (int j = 0; j < 64; ++j)
+              if (j >= left) g[j] = 0.f;
+          }
 #pragma unroll
-          for (int j0 = 0; j0 < NC; j0 += 64)
-            store_rows(&map_out, stage, lane, col + j0, p * pl.rows_pad + m0 + 32 * (warp & 3), acc + j0);
-          if (p + 1 < PL) {
+          for (int p = 0; p < PL; ++p) {   // a plane, then what it leaves
+            store_rows(&map_out, stage, lane, col + h, p * pl.rows_pad + m0 + 32 * (warp & 3), g);
+            if (p + 1 < PL) {
 #pragma unroll
-            for (int j = 0; j < NC; ++j) acc[j] -= __bfloat162float(__float2bfloat16_rn(acc[j]));
+              for (int j = 0; j < 64; ++j) g[j] -= __bfloat162float(__float2bfloat16_rn(g[j]));
+            }
           }
         }
       } else if (items.weight(item)) {
