@@ -88,7 +88,7 @@ struct GemmArgs {
   int v0, cols;          // the piece's first vocabulary column, how many there are
   int first;             // hidden: the sums start here
   float scale2, scale2_lo;   // log2(e) / T and its rounding residual
-  const float* weight;   // fp32 tensors
+  const void* weight;
   void* d_hidden;
   int64_t d_row_stride;
 };
@@ -195,6 +195,14 @@ __device__ __forceinline__ void set8(__nv_bfloat16* p, bool vec, const float* v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = __float2bfloat16_rn(v[j]);
   }
+}
+// Eight values plus f times those at p (16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void add_rest(const T* p, float f, float* v) {
+  float w[8];
+  get8(p, true, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = fmaf(f, w[j], v[j]);
 }
 template <typename T>
 __device__ __forceinline__ bool rows_vec(const T* p, int64_t stride) {
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
     auto aim = [&] {
       const int v = kBMN ? cur.kb * 64 + row0 : cur.n0 + row0, d = 8 * run + (kBMN ? cur.n0 : cur.kb * 64);
       left = cur.more && !items.weight(cur.item) && d < pl.dim ? a.cols - v : 0;
-      src = a.weight + (size_t)(a.v0 + v) * pl.dim + d;
+      src = static_cast<const float*>(a.weight) + (size_t)(a.v0 + v) * pl.dim + d;
     };
     auto fetch = [&](int p) {
       const bool in = p * kRowsPass < left;
@@ -909,13 +917,18 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
             g[j] = ex2(g[j]);
             g[j + 1] = ex2(g[j + 1]);
           }
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) split2(mul2(two(g[j], g[j + 1]), times), g[j], g[j + 1]);
           if (__any_sync(0xffffffffu, (unsigned)tgt < 64u)) {
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              if (j == tgt) g[j] -= 1.f;
+              if (j == tgt) {
+                g[j] -= gain;
+                // the target's value is often the row's largest by far: what its rounding
+                // leaves is made good in the hidden states' gradient
+                if (PL == 1) pl.rest[row] = g[j] - __bfloat162float(__float2bfloat16_rn(g[j]));
+              }
           }
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) split2(mul2(two(g[j], g[j + 1]), times), g[j], g[j + 1]);
           if (__any_sync(0xffffffffu, left < 64)) {   // behind the head's last row, and rows behind the kept ones
 #pragma unroll
             for (int j = 0; j < 64; ++j)
@@ -944,10 +957,15 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
           using T = typename Tensor<PL>::T;
           T* out = static_cast<T*>(a.d_hidden) + pl.row_of[row] * a.d_row_stride + col;
           const bool vec = rows_vec(static_cast<T*>(a.d_hidden), a.d_row_stride);
+          const T* w = static_cast<const T*>(a.weight) + (size_t)pl.target[row] * pl.dim + col;
+          const float rest = PL == 1 ? pl.rest[row] : 0.f;
           const int left = pl.dim - col;   // a multiple of 8
 #pragma unroll
           for (int j = 0; j < NC; j += 8)
-            if (j < left) set8(out + j, vec, acc + j);
+            if (j < left) {
+              if (PL == 1) add_rest(w + j, rest, acc + j);
+              set8(out + j, vec, acc + j);
+            }
         }
       } else {
         // whole tiles to their place, parts of a tile to a tile of their own; a piece
@@ -1030,7 +1048,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_merge_kernel(CePlan pl, int 
 constexpr int kFinishThreads = 256;
 
 template <typename T, int PL, int G, int BN>
-__global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan pl, T* d_hidden, int64_t stride, int groups_of_ctas) {
+__global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan pl, const T* weight, T* d_hidden, int64_t stride, int groups_of_ctas) {
   griddep_wait();
   griddep_trigger();
   using C = GemmCfg<PL, G, BN>;
@@ -1041,6 +1059,8 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan
   const size_t step = (size_t)rest * C::kTM * C::kBN;
   for (int r = blockIdx.x; r < kept; r += gridDim.x) {
     T* out = d_hidden + pl.row_of[r] * stride;
+    const T* w = weight + (size_t)pl.target[r] * pl.dim;
+    const float rest_r = PL == 1 ? pl.rest[r] : 0.f;
     for (int c = threadIdx.x * 8; c < pl.dim; c += kFinishThreads * 8) {
       const int tile = c / C::kBN * m_tiles + r / C::kTM;
       float sum[8];
@@ -1062,6 +1082,7 @@ __global__ void __launch_bounds__(kFinishThreads) ce_finish_hidden_kernel(CePlan
             }
         }
       }
+      if (PL == 1) add_rest(w + c, rest_r, sum);
       set8(out + c, vec, sum);
     }
   }
@@ -1139,7 +1160,7 @@ cudaError_t forward(const CePlan& pl, const CeTensors& t, int sms, int* launches
   const Scale sc = scale_of(t.temperature);
   a.scale2 = sc.hi;
   a.scale2_lo = sc.lo;
-  a.weight = static_cast<const float*>(t.weight);
+  a.weight = t.weight;
   a.cols = pl.vocab;
   e = gemm<PL, G, BN, kStats>(a, mh, mw, mh, mw, mw, sms, launches, s);
   if (e != cudaSuccess) return e;
@@ -1177,7 +1198,7 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
   const Scale sc = scale_of(t.temperature);
   a.scale2 = sc.hi;
   a.scale2_lo = sc.lo;
-  a.weight = static_cast<const float*>(t.weight);
+  a.weight = t.weight;
   a.d_hidden = t.d_hidden;
   a.d_row_stride = t.d_row_stride;
   // (the tiles of a piece's two gradients)
@@ -1198,7 +1219,7 @@ cudaError_t backward(const CePlan& pl, const CeTensors& t, int sms, int* launche
   if (!t.d_hidden || pl.direct) return cudaSuccess;
   ++*launches;
   return launch_pdl(ce_finish_hidden_kernel<T, PL, G, BN>, dim3(std::min(pl.rows, sms * 64)), dim3(kFinishThreads), 0, s, pl,
-                    static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_groups(G, sms));
+                    static_cast<const T*>(t.weight), static_cast<T*>(t.d_hidden), t.d_row_stride, gemm_groups(G, sms));
 }
 
 }  // namespace
@@ -1251,6 +1272,7 @@ CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, 
   } else {
     pl.lse2 = reinterpret_cast<float2*>(take(8 * R));
     pl.gain = reinterpret_cast<float*>(take(4 * R));
+    pl.rest = reinterpret_cast<float*>(take(4 * R));
     pl.g = reinterpret_cast<__nv_bfloat16*>(take(2 * pl.planes * R * pl.piece));
     // a small vocabulary's K is short: no tile is cut, and the tiles go to the caller's rows
     pl.direct = pl.piece >= vocab && pl.piece <= kDirectPiece;

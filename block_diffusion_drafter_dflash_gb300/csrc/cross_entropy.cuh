@@ -28,6 +28,7 @@ struct CePlan {
   float* picked;         // forward: [rows_pad] the target's exponent
   float2* lse2;          // gradient: [rows_pad] lse log2(e) as a rounded value and its residual
   float* gain;           // gradient: [rows_pad] d_loss / T
+  float* rest;           // gradient: [rows_pad] what G's rounding leaves of the target's value (bf16 tensors)
   __nv_bfloat16* g;      // gradient: [planes][rows_pad][piece] gradient of a piece of the logits
   float* acc;            // gradient: [rows_pad][dim_pad] sums of the hidden states' gradient
   float* tail;           // gradient: sums of the parts of its tiles that are cut
