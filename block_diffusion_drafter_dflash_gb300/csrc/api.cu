@@ -1684,6 +1684,7 @@ int32_t ce_check(const void* hidden, int64_t row_stride, const void* weight, con
   if (reinterpret_cast<uintptr_t>(hidden) % (dtype == DFLASH_DTYPE_F32 ? 4 : 2))
     return fail(DFLASH_ERR_INVALID_ARG, "hidden states are not aligned to their type");
   if (reinterpret_cast<uintptr_t>(weight) % 16) return fail(DFLASH_ERR_INVALID_ARG, "the head must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(targets) % 4) return fail(DFLASH_ERR_INVALID_ARG, "targets are not aligned to their type");
   if (!workspace) return fail(DFLASH_ERR_INVALID_ARG, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(DFLASH_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   return DFLASH_OK;
@@ -1753,6 +1754,8 @@ int32_t dflash_linear_cross_entropy_backward(const void* hidden, int32_t dtype, 
   if (rc) return rc;
   if (!d_hidden && !d_weight) return fail(DFLASH_ERR_INVALID_ARG, "d_hidden or d_weight is needed");
   if (rows > 0 && (!lse || !d_loss)) return fail(DFLASH_ERR_INVALID_ARG, "lse or d_loss is NULL");
+  if (reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(d_loss) % 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "lse or d_loss is not aligned to its type");
   const bool f32 = dtype == DFLASH_DTYPE_F32;
   const long long es = f32 ? 4 : 2;
   if (d_hidden && rows > 1 && d_row_stride < dim)
@@ -1815,7 +1818,7 @@ int32_t embed_rows(const void* rows, int32_t row_dtype, int64_t stride, int32_t 
                    int32_t dim, int32_t vocab, const int32_t* tokens) {
   const long long re = row_dtype == DFLASH_DTYPE_F32 ? 4 : 2, te = table_dtype == DFLASH_DTYPE_F32 ? 4 : 2;
   if (n > 1 && stride < dim) return fail(DFLASH_ERR_INVALID_ARG, "row stride %lld < dim %d", (long long)stride, dim);
-  if (reinterpret_cast<uintptr_t>(rows) % re || reinterpret_cast<uintptr_t>(table) % te)
+  if (reinterpret_cast<uintptr_t>(rows) % re || reinterpret_cast<uintptr_t>(table) % te || reinterpret_cast<uintptr_t>(tokens) % 4)
     return fail(DFLASH_ERR_INVALID_ARG, "a tensor is not aligned to its type");
   const Span r(rows, n, stride * re, dim * re), t(table, vocab, dim * te, dim * te), k(tokens, n, 4, 4);
   if (overlap(r, t) || overlap(r, k) || overlap(t, k)) return fail(DFLASH_ERR_INVALID_ARG, "the tensors overlap");

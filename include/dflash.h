@@ -522,7 +522,8 @@ int32_t dflash_clip_grad_norm(const void* const* grads_host, void* const* out_ho
  *   workspace   >= dflash_linear_cross_entropy_workspace_bytes(...) bytes,
  *               256-byte aligned; its first int32 is the call's status word (0
  *               or DFLASH_ERR_TIMEOUT), read with
- *               dflash_linear_cross_entropy_status
+ *               dflash_linear_cross_entropy_status; of one call (or captured
+ *               graph) at a time, as every workspace here and below
  * Precision.  bf16 tensors: exact products, fp32 sums.  fp32 tensors: products
  * of all 24 bits (three bf16 planes each, six products), fp32 sums.  Sums of the
  * tensor cores, which truncate, span at most 512 of the dim.
@@ -549,7 +550,8 @@ int32_t dflash_linear_cross_entropy(const void* hidden_dev, int32_t dtype, int64
  *   workspace     >= dflash_linear_cross_entropy_backward_workspace_bytes(...)
  * The gradients overlap neither each other nor an operand in any other way.
  * Precision: as the forward; G of bf16 tensors is rounded to one bf16 before its
- * products, G of fp32 tensors enters with all 24 bits.  Sums are added in a
+ * products (what that leaves of the target's value is added to d_hidden in
+ * fp32), G of fp32 tensors enters with all 24 bits.  Sums are added in a
  * fixed order: the same call gives the same bits on the same device.  rows = 0
  * zeroes d_weight. */
 size_t dflash_linear_cross_entropy_backward_workspace_bytes(int32_t rows, int32_t dim, int32_t vocab, int32_t dtype);

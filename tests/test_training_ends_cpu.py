@@ -23,7 +23,7 @@ SHARED = [
     (dict(vocab=0), -2), (dict(vocab=(1 << 24) + 1), -2), (dict(dtype=2), -1), (dict(temp=0.0), -1),
     (dict(temp=-1.0), -1), (dict(temp=INF), -1), (dict(temp=float("nan")), -1), (dict(temp=4.2e-39), -1),
     (dict(stride=15), -1), (dict(hidden=None), -1), (dict(weight=None), -1), (dict(targets=None), -1),
-    (dict(hidden=P + 2), -1), (dict(hidden=P + 1, dtype=1), -1), (dict(weight=2 * P + 8), -1), (dict(ws=None), -1),
+    (dict(hidden=P + 2), -1), (dict(hidden=P + 1, dtype=1), -1), (dict(targets=3 * P + 2), -1), (dict(weight=2 * P + 8), -1), (dict(ws=None), -1),
     (dict(ws=6 * P + 128), -1),
 ]
 
@@ -44,7 +44,7 @@ def _loss_grad(L, hidden=P, dtype=0, stride=16, weight=2 * P, targets=3 * P, row
 
 
 @pytest.mark.parametrize("kw,code", SHARED + [
-    (dict(lse=None), -1), (dict(d_loss=None), -1), (dict(d_hidden=None, d_weight=None), -1), (dict(d_stride=15), -1),
+    (dict(lse=None), -1), (dict(d_loss=None), -1), (dict(lse=4 * P + 1), -1), (dict(d_loss=5 * P + 2), -1), (dict(d_hidden=None, d_weight=None), -1), (dict(d_stride=15), -1),
     (dict(d_hidden=7 * P + 2), -1), (dict(d_weight=8 * P + 4), -1),
     (dict(d_hidden=P + 4), -1), (dict(d_hidden=P, d_stride=17), -1),     # the hidden states' place, but not their rows
     (dict(d_hidden=2 * P + 64), -1), (dict(d_weight=2 * P), -1), (dict(d_weight=P + 16), -1),
@@ -78,7 +78,7 @@ EMBED = [
     (dict(n=-1), -1), (dict(n=(1 << 24) + 1), -2), (dict(dim=0), -2), (dict(dim=65537, stride=65537), -2),
     (dict(vocab=0), -2), (dict(vocab=(1 << 24) + 1), -2), (dict(table_dtype=4), -1), (dict(out_dtype=-1), -1),
     (dict(scale=INF), -1), (dict(scale=float("nan")), -1), (dict(table=None), -1), (dict(tokens=None), -1),
-    (dict(out=None), -1), (dict(stride=4), -1), (dict(table=P + 2), -1), (dict(out=3 * P + 1, out_dtype=1), -1),
+    (dict(out=None), -1), (dict(stride=4), -1), (dict(table=P + 2), -1), (dict(out=3 * P + 1, out_dtype=1), -1), (dict(tokens=2 * P + 2), -1),
     (dict(out=P + 8), -1), (dict(out=2 * P + 4), -1), (dict(tokens=P + 16), -1),      # one tensor over another
 ]
 
