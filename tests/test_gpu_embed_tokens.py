@@ -240,3 +240,20 @@ def test_binding_refusals():
         df.dflash_embed_tokens_backward(f(6, 8), t, f(10, 8), ws[:512])
     with pytest.raises(df.DFlashError):
         df.dflash_embed_tokens(f(10, 8), t, f(6, 8), scale=math.inf)
+
+
+@pytest.mark.parametrize("table_dtype,out_dtype,D", [(F32, F32, 40), (BF16, BF16, 40), (F32, BF16, 33), (BF16, F32, 1300)])
+def test_runs_over_chunks(table_dtype, out_dtype, D):
+    """Runs of one token that begin and end at, before and behind every 32nd sorted token."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    for i, choice in enumerate([(1, 31, 32, 33), (32,), (64,), (31, 33), (63, 65), (96, 1), (32, 64, 96, 128), (1, 2, 62, 63, 64, 65, 66),
+                                (400, 31), (500,)]):
+        lengths = [choice[int(k)] for k in torch.randint(0, len(choice), (24,), generator=torch.Generator().manual_seed(i))]
+        t = torch.cat([torch.full((n,), 3 * v + 1) for v, n in enumerate(lengths)] + [torch.tensor([-1] * (i * 7))])
+        n, V = t.numel(), 3 * len(lengths)
+        t = t.to("cuda", torch.int32)[torch.randperm(n, generator=g, device="cuda")]
+        _, d_out = rows_of(n, D, out_dtype, g, 3)
+        d_out.copy_(torch.randn((n, D), generator=g, device="cuda"))
+        check(backward(d_out, t, V, table_dtype, 0.7), d_out, t, V, 0.7)
+        before = torch.randn((V, D), generator=g, device="cuda").to(table_dtype)
+        check(backward(d_out, t, V, table_dtype, 0.7, into=before.clone()), d_out, t, V, 0.7, before)
