@@ -33,10 +33,19 @@
 // fp32 tensors enter as three bf16 planes each (x = h + m + l, 24 bits), every
 // product as six (h h, h m, m h, m m, h l, l h; what is left out is below 2^-24),
 // the five small ones with a sum of their own that spans more blocks.  One CTA a tile
-// of 128 x 128.  The head's planes exist in shared memory alone: four more warps read
+// of 128 x 128.  The head's planes exist in shared memory alone: eight more warps read
 // its fp32 rows a block ahead into registers and write the planes where the MMAs take
-// them.  (As a copy in memory, a piece at a time: 28 rows of 2,824 against 129,969 in
-// 1,343 us; its 1.47 GB read once are 216.)
+// them.  (28 rows of 2,824 against 129,969: 457 us, with a copy of the planes in memory
+// 1,343; the head's 1.47 GB read once are 219.)
+//
+// Bounds.  Many rows: the tensor cores.  2,048 x 4,096 x 22,016: the loss at 1.89
+// PFLOP/s (pipe active in 97 % of the cycles), the gradient's three products at 1.83,
+// 1.72 and 1.74; 8,192 x 4,096 x 151,936 back to back 5.5 ms, at the power cap.  Few rows:
+// HBM, the head once for the loss (15 x 4,096 x 151,936: 198 us, 6.3 TB/s) and twice for a
+// gradient (44 x 4,240 x 94,344, both: 435 us).  A dim of a few hundred: the epilogue
+// (6,113 x 136 x 50,082: loss 107 us, of which the MMAs 44).  fp32: shared memory, which
+// the six products read planes from (a block of 64 takes 2,600 cycles, 1,536 of them
+// MMAs); 333 x 256 x 8,705 gradients in 51 to 60 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -226,6 +235,7 @@ __device__ __forceinline__ int parts_of_cut(const CePlan& pl, int kept, int grou
 // Kept rows in their order: where each came from, its target and statistics, and
 // its hidden state as planes.  Every CTA counts the kept rows before its own.
 // Ignored rows get their results here: loss and lse 0, or a gradient of zeros.
+// Latency for few rows (7 us for 777 x 2,560 alone), then HBM (4,096 x 4,096: 20 us).
 constexpr int kGatherThreads = 256;
 
 template <typename T, int PL, bool BWD>
@@ -1002,7 +1012,8 @@ __global__ void __launch_bounds__(gemm_threads<PL>(), 1) ce_gemm_kernel(const __
 // A row's pairs merged: lse = ln2 (M + log2 S), and the loss from the difference of
 // the exponents, which is exact where the target has the largest.
 // A CTA takes ROWS rows, its threads a share of the pairs each: 32 rows' pairs lie in
-// 256 bytes, but few rows need more CTAs.
+// 256 bytes, but few rows need more CTAs.  Latency: 6 us for 15 rows of 1,188 pairs and for
+// 777 of 252 (32 rows a CTA for the former: 14.7).
 constexpr int kMergeThreads = 512;
 
 template <int ROWS>
@@ -1044,7 +1055,7 @@ __global__ void __launch_bounds__(kMergeThreads) ce_merge_kernel(CePlan pl, int 
 }
 
 // The hidden states' gradient to the caller's rows, the parts of a cut tile added in
-// order.
+// order.  HBM and L2: 34 us for 4,096 x 4,096, 5 for 300 x 256.
 constexpr int kFinishThreads = 256;
 
 template <typename T, int PL, int G, int BN>

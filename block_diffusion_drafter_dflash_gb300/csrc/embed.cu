@@ -3,7 +3,8 @@
 //
 //   out_i = scale E[t_i]            dE[v] (+)= scale sum_{i: t_i = v} d_out_i
 //
-// The lookup is bound by HBM: rows out, and each distinct row of the table once.
+// The lookup is bound by HBM: rows out, and each distinct row of the table once (8,192 x
+// 4,096, bf16 to fp32, 138 MB: 24 us, 5.8 TB/s; 16 rows in 2.5 us).
 //
 // The gradient.  In a block drafter's training one token, the mask, collects nearly
 // all rows, so rows of the table are no unit of work.  One cluster sorts the
@@ -16,6 +17,11 @@
 // order.  No float atomics: the same call gives the same bits.  Sums are fp32, at most
 // kEmbedChunk terms, and the chunks' sums are added with their rounding errors carried
 // along.  Few tokens take one launch.
+//
+// What bounds it: HBM where the table is large (8,192 rows of 4,096 into 151,936 bf16:
+// 224 us, its 1.38 GB at 6.2 TB/s, of which sort and zeroing 185, sums 31, joins 11), the
+// sort and the latency of three launches where it is not (5,470 x 183 into 16,467: 23
+// us; 48 x 256, one launch, 5).
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -171,7 +177,8 @@ __device__ void zero_fill(void* table, size_t bytes, int cta, int ctas) {
 // counts into places (digits first, then CTAs, then warps, so equal digits keep their
 // order) and moves the pairs.  Tokens outside the vocabulary sort behind all others.
 // Up to kHeld pairs a CTA stay in registers within a pass and in the cluster's shared
-// memory between passes; more go through memory.
+// memory between passes; more go through memory.  (50,001 tokens of 32,003: 27 us, 32 with
+// all passes through memory, 39 with digits compared by match.any; 24,026 14.)
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(EmbedBwdPlan pl, const int32_t* tokens, int passes, void* table,
                                                                      size_t zero_bytes) {
   griddep_wait();
@@ -324,7 +331,10 @@ __device__ __forceinline__ void put_sum(TT* p, int left, const float* sum, float
   store_row<W, S>(p, left, v);
 }
 
-// A chunk's sums over blockDim.x * W columns.
+// A chunk's sums over blockDim.x * W columns: a CTA reads each row of d_out in its chunk
+// once (50,001 bf16 rows of 1,000 in 35 us, 5.7 TB/s with the rows written).  A token that
+// goes on is not followed into the next chunk: longer chains of loads cost what the joins
+// save (17,152 x 1,001 of 30,000 tokens: 63 us, with it 72).
 template <typename TO, typename TT, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
@@ -378,6 +388,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
 // each addition rounds off summed beside them.  A CTA looks at the ends of kJoinChunks
 // chunks, over 32 * W columns.  A token of few chunks is one warp's; those of more are
 // taken by all warps together, a run of chunks each.
+// Latency: order, the search for the token's end, its chunks' sums, the table; 11 us for
+// a token of 7,700 rows, 15 for 1,562 chunks of text.
 constexpr int kJoinWarps = 8, kJoinChunks = 8, kJoinAlone = 12;
 
 template <int W>
