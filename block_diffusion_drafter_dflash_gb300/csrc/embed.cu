@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
 // chunks, over 32 * W columns.  A token of few chunks is one warp's; those of more are
 // taken by all warps together, a run of chunks each.
 // Latency: order, the search for the token's end, its chunks' sums, the table; 11 us for
-// a token of 7,700 rows, 15 for 1,562 chunks of text.
+// a token of 7,700 rows, 15 for 1,562 chunks of text.  So CTAs an SM count (the whole gradient of
+// 50,001 x 1,000: three 77.6 us, four 72.5, five 73.7) and warps a CTA, for long
+// tokens (24,026 x 138, nine tenths one token: 35.5 us, with four warps 43).
 constexpr int kJoinWarps = 8, kJoinChunks = 8, kJoinAlone = 12;
 
 template <int W>
@@ -415,7 +417,7 @@ struct Sum {
 };
 
 template <typename TO, typename TT, bool VEC>
-__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 4) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
   constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
