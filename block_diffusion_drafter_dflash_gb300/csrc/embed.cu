@@ -23,6 +23,7 @@
 // sort and the latency of three launches where it is not (5,470 x 183 into 16,467: 23
 // us; 48 x 256, one launch, 5).
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -38,15 +39,16 @@ constexpr int kChunk = kEmbedChunk;
 
 // ---------------------------------------------------------------- columns of a thread
 // A warp takes 32 * W columns.  Where rows allow it (S = 1) a lane has W neighbours, one
-// 16-byte access of the wider type; else (S = 32: an odd dim, an odd address) every 32nd,
-// so that the warp's narrow accesses lie side by side and a row's bookkeeping still serves
-// W values.  `left`: columns from the lane's first to the row's end.
+// 16-byte access of one type and half or twice that of the other; where they do not (S = 32:
+// an odd dim, an odd address) every 32nd, so that the warp's narrow accesses lie side by side
+// and a row's bookkeeping still serves W values.  `left`: columns from the lane's first to
+// the row's end.
 template <int W, int S>
 __device__ __forceinline__ int first_column(int unit) {
   return (unit >> 5) * 32 * W + (unit & 31) * (S == 1 ? W : 1);
 }
 template <typename T, int W>
-struct alignas(sizeof(T) * W) Vec {
+struct alignas(sizeof(T) * W < 16 ? sizeof(T) * W : 16) Vec {
   T v[W];
 };
 template <int W, int S, typename T>
@@ -76,31 +78,42 @@ __device__ __forceinline__ void store_row(T* p, int left, const float* v) {
   }
 }
 // Values of a lane and their step.
-template <typename A, typename B, bool VEC, int NARROW = 4>
+enum Fit { kNarrow, kWide, kWider };   // 16 bytes of neither type, of the wider one, of the narrower one
+template <typename A, typename B, int FIT, int NARROW = 4>
 struct Columns {
-  static constexpr int kWidest = sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B);
-  static constexpr int W = VEC ? 16 / kWidest : NARROW, S = VEC ? 1 : 32;
+  static constexpr int kMost = sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B), kLeast = sizeof(A) + sizeof(B) - kMost;
+  static constexpr int W = FIT == kNarrow ? NARROW : 16 / (FIT == kWide ? kMost : kLeast), S = FIT == kNarrow ? 32 : 1;
 };
 // The lookup takes 8 narrow values a lane (20,000 rows of 2,561, bf16 to fp32: 52 us instead
 // of 61 with 4), the sums 4 (17,152 x 4,417, fp32, of 29,513 bf16 rows: 229 us, with 8 424).
-template <typename A, typename B, bool VEC>
-using Lookup = Columns<A, B, VEC, 8>;
-template <typename A, typename B>
+template <typename A, typename B, int FIT>
+using Lookup = Columns<A, B, FIT, 8>;
+template <typename A, typename B, int FIT>
 bool rows_fit(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int dim) {
-  constexpr int W = Columns<A, B, true>::W;
+  constexpr int W = Columns<A, B, FIT>::W;
   auto fits = [&](const void* p, int64_t stride, int size) {
-    return reinterpret_cast<uintptr_t>(p) % (W * size) == 0 && stride % W == 0;
+    const int unit = std::min(16, W * size);
+    return reinterpret_cast<uintptr_t>(p) % unit == 0 && stride * size % unit == 0;
   };
   return dim % W == 0 && fits(a, a_stride, sizeof(A)) && fits(b, b_stride, sizeof(B));
+}
+// run(FIT) of the widest accesses that the rows allow; WIDER: of the narrower type's 16 bytes
+template <typename A, typename B, bool WIDER, typename F>
+cudaError_t by_fit(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int dim, F run) {
+  if constexpr (WIDER && sizeof(A) != sizeof(B)) {
+    if (rows_fit<A, B, kWider>(a, a_stride, b, b_stride, dim)) return run(std::integral_constant<int, kWider>{});
+  }
+  if (rows_fit<A, B, kWide>(a, a_stride, b, b_stride, dim)) return run(std::integral_constant<int, kWide>{});
+  return run(std::integral_constant<int, kNarrow>{});
 }
 
 // ---------------------------------------------------------------- lookup
 // kLookups: accesses of a thread, all loaded before the first is stored.
-template <typename TT, typename TO, bool VEC, int kLookups>
+template <typename TT, typename TO, int FIT, int kLookups>
 __global__ void __launch_bounds__(256) embed_kernel(EmbedArgs a) {
   griddep_wait();
   griddep_trigger();
-  constexpr int W = Lookup<TT, TO, VEC>::W, S = Lookup<TT, TO, VEC>::S;
+  constexpr int W = Lookup<TT, TO, FIT>::W, S = Lookup<TT, TO, FIT>::S;
   const unsigned units = S == 1 ? a.dim / W : (a.dim + 32 * W - 1) / (32 * W) * 32;   // of a row
   const long long n = (long long)a.n * units, step = (long long)gridDim.x * (256 * kLookups);
   const TT* table = static_cast<const TT*>(a.table);
@@ -335,11 +348,11 @@ __device__ __forceinline__ void put_sum(TT* p, int left, const float* sum, float
 // once (50,001 bf16 rows of 1,000 in 35 us, 5.7 TB/s with the rows written).  A token that
 // goes on is not followed into the next chunk: longer chains of loads cost what the joins
 // save (17,152 x 1,001 of 30,000 tokens: 63 us, with it 72).
-template <typename TO, typename TT, bool VEC>
+template <typename TO, typename TT, int FIT>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
+  constexpr int W = Columns<TO, TT, FIT>::W, S = Columns<TO, TT, FIT>::S;
   const int c = first_column<W, S>(blockIdx.y * blockDim.x + threadIdx.x), left = pl.dim - c;
   TT* table = static_cast<TT*>(a.d_table);
   __shared__ uint2 s_pair[kChunk];
@@ -416,11 +429,11 @@ struct Sum {
   }
 };
 
-template <typename TO, typename TT, bool VEC>
+template <typename TO, typename TT, int FIT>
 __global__ void __launch_bounds__(32 * kJoinWarps, 4) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
+  constexpr int W = Columns<TO, TT, FIT>::W, S = Columns<TO, TT, FIT>::S;
   __shared__ int s_last[kJoinChunks];              // a chunk's token's last chunk; 0: none begins here and goes on
   __shared__ Sum<W> s_sum[kJoinWarps][32];
   const uint2* order = pl.order;
@@ -525,11 +538,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) embed_join_kernel(EmbedBwd
 // other words are zeroed as the bytes that they are.
 constexpr int kSmall = 256, kSmallWarps = 8, kSmallAlone = 16;
 
-template <typename TO, typename TT, bool VEC>
+template <typename TO, typename TT, int FIT>
 __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  constexpr int W = Columns<TO, TT, VEC>::W, S = Columns<TO, TT, VEC>::S;
+  constexpr int W = Columns<TO, TT, FIT>::W, S = Columns<TO, TT, FIT>::S;
   __shared__ alignas(16) uint64_t s_key[kSmall];
   __shared__ uint32_t s_token[kSmall + 1];
   __shared__ uint16_t s_pos[kSmall], s_first[kSmall];   // s_first: the first token of each word that has one
@@ -644,23 +657,25 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(EmbedBwdP
 }
 
 // ---------------------------------------------------------------- host side
-template <typename TT, typename TO, bool VEC>
+template <typename TT, typename TO, int FIT>
 cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
-  constexpr int W = Lookup<TT, TO, VEC>::W;
-  const long long units = (long long)a.n * (VEC ? a.dim / W : (a.dim + 32 * W - 1) / (32 * W) * 32);
+  constexpr int W = Lookup<TT, TO, FIT>::W;
+  const long long units = (long long)a.n * (FIT != kNarrow ? a.dim / W : (a.dim + 32 * W - 1) / (32 * W) * 32);
   // few rows: a thread an access, so that the latency is one chain of loads; many: two, which
   // keep more loads in flight (20,000 rows of 2,560, bf16 to fp32: 1, 2, 3, 4 and 8 in 69, 51, 57,
   // 62 and 83 us)
   const bool few = units <= (long long)sms * 2048;
   const long long per = 256 * (few ? 1 : 2);
   const unsigned grid = (unsigned)std::min<long long>((units + per - 1) / per, (long long)sms * 512);
-  return few ? launch_pdl(embed_kernel<TT, TO, VEC, 1>, dim3(grid), dim3(256), 0, s, a)
-             : launch_pdl(embed_kernel<TT, TO, VEC, 2>, dim3(grid), dim3(256), 0, s, a);
+  return few ? launch_pdl(embed_kernel<TT, TO, FIT, 1>, dim3(grid), dim3(256), 0, s, a)
+             : launch_pdl(embed_kernel<TT, TO, FIT, 2>, dim3(grid), dim3(256), 0, s, a);
 }
 template <typename TT, typename TO>
 cudaError_t lookup(const EmbedArgs& a, int sms, cudaStream_t s) {
-  return rows_fit<TT, TO>(a.table, a.dim, a.out, a.out_stride, a.dim) ? lookup<TT, TO, true>(a, sms, s)
-                                                                      : lookup<TT, TO, false>(a, sms, s);
+  // 16 bytes of the output a lane, so that a warp's streaming stores are whole lines (20,000 x
+  // 2,560, fp32 to bf16: 39 us instead of 45; bf16 to fp32 8,192 x 4,096: two of 16 bytes 26, one 24)
+  return by_fit<TT, TO, sizeof(TO) == 2>(a.table, a.dim, a.out, a.out_stride, a.dim,
+                                         [&](auto fit) { return lookup<TT, TO, fit()>(a, sms, s); });
 }
 
 int passes_of(int vocab) {
@@ -694,28 +709,47 @@ cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, siz
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab), table, zero_bytes);
 }
 
-template <typename TO, typename TT, bool VEC>
+template <typename TO, typename TT, int FIT>
+cudaError_t join(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, cudaStream_t s) {
+  auto run = [&](auto fit) {
+    constexpr int columns = 32 * Columns<TO, TT, fit()>::W;
+    return launch_pdl(embed_join_kernel<TO, TT, fit()>,
+                      dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, (pl.dim + columns - 1) / columns), dim3(32 * kJoinWarps), 0, s, pl, a);
+  };
+  // More columns a lane where there are more CTAs than run at once (30,000 x 1,000: 51 us instead
+  // of 54), fewer where a long token's CTAs work alone (8,192 x 512: 25 instead of 29)
+  if constexpr (FIT != kNarrow && sizeof(TO) != sizeof(TT)) {
+    const long long ctas = (long long)((pl.chunks + kJoinChunks - 1) / kJoinChunks) * ((pl.dim + 127) / 128);
+    if (ctas > 4LL * sms && rows_fit<TO, TT, kWider>(a.d_out, a.stride, a.d_table, pl.dim, pl.dim))
+      return run(std::integral_constant<int, kWider>{});
+    return run(std::integral_constant<int, kWide>{});
+  }
+  return run(std::integral_constant<int, FIT>{});
+}
+template <typename TO, typename TT, int FIT>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
-  constexpr int W = Columns<TO, TT, VEC>::W;
+  constexpr int W = Columns<TO, TT, FIT>::W;
   const int tiles32 = (pl.dim + 32 * W - 1) / (32 * W), words = (pl.vocab + 31) / 32;
   if (pl.n <= kSmall) {
     ++*launches;
-    return launch_pdl(embed_small_kernel<TO, TT, VEC>, dim3((unsigned)std::min<long long>((long long)words + (long long)pl.n * tiles32, sms * 2)),
+    return launch_pdl(embed_small_kernel<TO, TT, FIT>, dim3((unsigned)std::min<long long>((long long)words + (long long)pl.n * tiles32, sms * 2)),
                       dim3(32 * kSmallWarps), 0, s, pl, a);
   }
   cudaError_t e = sort(pl, a.tokens, a.d_table, a.accumulate ? 0 : sizeof(TT) * (size_t)pl.vocab * pl.dim, sms, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   const int threads = std::min(256, tiles32 * 32), tiles = (tiles32 * 32 + threads - 1) / threads;
-  e = launch_pdl(embed_sum_kernel<TO, TT, VEC>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
+  e = launch_pdl(embed_sum_kernel<TO, TT, FIT>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
   if (e != cudaSuccess) return e;
   *launches += 2;
-  return launch_pdl(embed_join_kernel<TO, TT, VEC>, dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, tiles32), dim3(32 * kJoinWarps), 0, s, pl, a);
+  return join<TO, TT, FIT>(pl, a, sms, s);
 }
 template <typename TO, typename TT>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
-  return rows_fit<TO, TT>(a.d_out, a.stride, a.d_table, pl.dim, pl.dim) ? sums<TO, TT, true>(pl, a, sms, launches, s)
-                                                                        : sums<TO, TT, false>(pl, a, sms, launches, s);
+  // 16 bytes of the table a lane (30,000 x 1,000, fp32 to bf16: 54 us instead of 58; bf16 to fp32
+  // 50,001 x 1,000: 72, with 16 bytes of the rows 77)
+  return by_fit<TO, TT, sizeof(TT) == 2>(a.d_out, a.stride, a.d_table, pl.dim, pl.dim,
+                                         [&](auto fit) { return sums<TO, TT, fit()>(pl, a, sms, launches, s); });
 }
 
 }  // namespace

@@ -257,3 +257,25 @@ def test_runs_over_chunks(table_dtype, out_dtype, D):
         check(backward(d_out, t, V, table_dtype, 0.7), d_out, t, V, 0.7)
         before = torch.randn((V, D), generator=g, device="cuda").to(table_dtype)
         check(backward(d_out, t, V, table_dtype, 0.7, into=before.clone()), d_out, t, V, 0.7, before)
+
+
+@pytest.mark.parametrize("table_dtype,out_dtype", [(F32, BF16), (BF16, F32), (F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("D,pad,offset", [(64, 4, 4), (64, 8, 8), (64, 4, 8), (72, 8, 4), (1032, 12, 4), (60, 4, 4), (64, 2, 4)])
+def test_rows_at_sixteen_bytes(D, pad, offset, table_dtype, out_dtype):
+    """Rows that allow 16 bytes of both types, of the wider one alone, or of neither, by their start, step or length."""
+    df = _df()
+    g = torch.Generator(device="cuda").manual_seed(D + pad)
+    for n in (7, 300):
+        V = 50
+        t = make_tokens(n, V, g, mask=0.3, ignored=0.1)
+        _, d_out = rows_of(n, D, out_dtype, g, pad, offset)
+        d_out.copy_(torch.randn((n, D), generator=g, device="cuda"))
+        check(backward(d_out, t, V, table_dtype, 1.3), d_out, t, V, 1.3)
+        whole = torch.randn(V * D + offset, generator=g, device="cuda").to(table_dtype)
+        table = whole[offset:].view(V, D)
+        store, out = rows_of(n, D, out_dtype, g, pad, offset, fill=555.0)
+        df.dflash_embed_tokens(table, t, out)
+        inside = (t >= 0) & (t < V)
+        want = torch.where(inside[:, None], table[torch.where(inside, t, 0).long()].float(), 0.0).to(out_dtype)
+        assert torch.equal(out, want)
+        assert bool((store[:offset] == 555.0).all()) and bool((store[offset:].view(n, D + pad)[:, D:] == 555.0).all())
