@@ -429,11 +429,10 @@ struct Sum {
   }
 };
 
-template <typename TO, typename TT, int FIT>
+template <typename TT, int W, int S>
 __global__ void __launch_bounds__(32 * kJoinWarps, 4) embed_join_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
   griddep_trigger();
-  constexpr int W = Columns<TO, TT, FIT>::W, S = Columns<TO, TT, FIT>::S;
   __shared__ int s_last[kJoinChunks];              // a chunk's token's last chunk; 0: none begins here and goes on
   __shared__ Sum<W> s_sum[kJoinWarps][32];
   const uint2* order = pl.order;
@@ -709,22 +708,11 @@ cudaError_t sort(const EmbedBwdPlan& pl, const int32_t* tokens, void* table, siz
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel, pl, tokens, passes_of(pl.vocab), table, zero_bytes);
 }
 
-template <typename TO, typename TT, int FIT>
-cudaError_t join(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, cudaStream_t s) {
-  auto run = [&](auto fit) {
-    constexpr int columns = 32 * Columns<TO, TT, fit()>::W;
-    return launch_pdl(embed_join_kernel<TO, TT, fit()>,
-                      dim3((pl.chunks + kJoinChunks - 1) / kJoinChunks, (pl.dim + columns - 1) / columns), dim3(32 * kJoinWarps), 0, s, pl, a);
-  };
-  // More columns a lane where there are more CTAs than run at once (30,000 x 1,000: 51 us instead
-  // of 54), fewer where a long token's CTAs work alone (8,192 x 512: 25 instead of 29)
-  if constexpr (FIT != kNarrow && sizeof(TO) != sizeof(TT)) {
-    const long long ctas = (long long)((pl.chunks + kJoinChunks - 1) / kJoinChunks) * ((pl.dim + 127) / 128);
-    if (ctas > 4LL * sms && rows_fit<TO, TT, kWider>(a.d_out, a.stride, a.d_table, pl.dim, pl.dim))
-      return run(std::integral_constant<int, kWider>{});
-    return run(std::integral_constant<int, kWide>{});
-  }
-  return run(std::integral_constant<int, FIT>{});
+template <typename TT, int W>
+cudaError_t join(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, cudaStream_t s) {
+  const dim3 grid((pl.chunks + kJoinChunks - 1) / kJoinChunks, (pl.dim + 32 * W - 1) / (32 * W));
+  const bool fits = reinterpret_cast<uintptr_t>(a.d_table) % std::min<size_t>(16, W * sizeof(TT)) == 0 && pl.dim % W == 0;
+  return launch_pdl(fits ? embed_join_kernel<TT, W, 1> : embed_join_kernel<TT, W, 32>, grid, dim3(32 * kJoinWarps), 0, s, pl, a);
 }
 template <typename TO, typename TT, int FIT>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
@@ -742,7 +730,10 @@ cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* la
   e = launch_pdl(embed_sum_kernel<TO, TT, FIT>, dim3(pl.chunks, tiles), dim3(threads), 0, s, pl, a);
   if (e != cudaSuccess) return e;
   *launches += 2;
-  return join<TO, TT, FIT>(pl, a, sms, s);
+  // eight columns a lane where there are more CTAs than run at once (30,000 x 1,000: 51 us, with
+  // four 54), four where a long token's CTAs work alone (8,192 x 512: 25 us, with eight 29)
+  const long long ctas = (long long)((pl.chunks + kJoinChunks - 1) / kJoinChunks) * ((pl.dim + 127) / 128);
+  return ctas > 4LL * sms ? join<TT, 8>(pl, a, s) : join<TT, 4>(pl, a, s);
 }
 template <typename TO, typename TT>
 cudaError_t sums(const EmbedBwdPlan& pl, const EmbedBwdArgs& a, int sms, int* launches, cudaStream_t s) {
