@@ -19,7 +19,7 @@
 // along.  Few tokens take one launch.
 //
 // What bounds it: HBM where the table is large (8,192 rows of 4,096 into 151,936 bf16:
-// 224 us, its 1.38 GB at 6.2 TB/s, of which sort and zeroing 185, sums 31, joins 11), the
+// 224 us, its 1.38 GB at 6.2 TB/s, of which sort and zeroing 186, sums 29, joins 13), the
 // sort and the latency of three launches where it is not (5,470 x 183 into 16,467: 23
 // us; 48 x 256, one launch, 5).
 #include <algorithm>
@@ -347,7 +347,7 @@ __device__ __forceinline__ void put_sum(TT* p, int left, const float* sum, float
 // A chunk's sums over blockDim.x * W columns: a CTA reads each row of d_out in its chunk
 // once (50,001 bf16 rows of 1,000 in 35 us, 5.7 TB/s with the rows written).  A token that
 // goes on is not followed into the next chunk: longer chains of loads cost what the joins
-// save (17,152 x 1,001 of 30,000 tokens: 63 us, with it 72).
+// save (30,000 rows of 1,001 into 17,152: 72 us instead of 63).
 template <typename TO, typename TT, int FIT>
 __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBwdArgs a) {
   griddep_wait();
@@ -401,10 +401,11 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedBwdPlan pl, EmbedBw
 // each addition rounds off summed beside them.  A CTA looks at the ends of kJoinChunks
 // chunks, over 32 * W columns.  A token of few chunks is one warp's; those of more are
 // taken by all warps together, a run of chunks each.
-// Latency: order, the search for the token's end, its chunks' sums, the table; 11 us for
-// a token of 7,700 rows, 15 for 1,562 chunks of text.  So CTAs an SM count (the whole gradient of
-// 50,001 x 1,000: three 77.6 us, four 72.5, five 73.7) and warps a CTA, for long
-// tokens (24,026 x 138, nine tenths one token: 35.5 us, with four warps 43).
+// Latency: order, the search for the token's end, its chunks' sums, the table; 13 us for
+// a token of 7,700 rows, 9 for 1,562 chunks of text.  So CTAs an SM count (the whole gradient of
+// 50,001 x 1,000 with four columns a lane: three 77.6 us, four 72.5, five 73.7), and warps a CTA
+// for long tokens (24,026 x 138, nine tenths one token: 36 us, with four warps 43, sixteen 33; but
+// 8,192 x 4,096 225 and, with sixteen, 228).
 constexpr int kJoinWarps = 8, kJoinChunks = 8, kJoinAlone = 12;
 
 template <int W>

@@ -549,7 +549,8 @@ int32_t dflash_linear_cross_entropy(const void* hidden_dev, int32_t dtype, int64
  *                 element written; NULL where the head is frozen.  Not both NULL
  *   workspace     >= dflash_linear_cross_entropy_backward_workspace_bytes(...)
  * The gradients overlap neither each other nor an operand in any other way.
- * Precision: as the forward; G of bf16 tensors is rounded to one bf16 before its
+ * Precision: as the forward; an lse that is off by d (another program's) scales
+ * its row's probabilities by e^-d; G of bf16 tensors is rounded to one bf16 before its
  * products (what that leaves of the target's value is added to d_hidden in
  * fp32), G of fp32 tensors enters with all 24 bits.  Sums are added in a
  * fixed order: the same call gives the same bits on the same device.  rows = 0

@@ -279,3 +279,23 @@ def test_rows_at_sixteen_bytes(D, pad, offset, table_dtype, out_dtype):
         want = torch.where(inside[:, None], table[torch.where(inside, t, 0).long()].float(), 0.0).to(out_dtype)
         assert torch.equal(out, want)
         assert bool((store[:offset] == 555.0).all()) and bool((store[offset:].view(n, D + pad)[:, D:] == 555.0).all())
+
+
+@pytest.mark.parametrize("table_dtype,out_dtype", [(F32, BF16), (BF16, F32), (F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("D,pad", [(1032, 0), (1031, 2), (1028, 4)])
+def test_many_rows(D, pad, table_dtype, out_dtype):
+    """Enough rows for the lookup's accesses in pairs and for the joins of eight columns a lane."""
+    df = _df()
+    n, V = 20011, 500
+    g = torch.Generator(device="cuda").manual_seed(D)
+    t = make_tokens(n, V, g, mask=0.2, ignored=0.05)
+    _, d_out = rows_of(n, D, out_dtype, g, pad)
+    d_out.copy_(torch.randn((n, D), generator=g, device="cuda"))
+    check(backward(d_out, t, V, table_dtype, 0.9), d_out, t, V, 0.9)
+    table = torch.randn((V, D), generator=g, device="cuda").to(table_dtype)
+    store, out = rows_of(n, D, out_dtype, g, pad, fill=555.0)
+    df.dflash_embed_tokens(table, t, out)
+    inside = (t >= 0) & (t < V)
+    want = torch.where(inside[:, None], table[torch.where(inside, t, 0).long()].float(), 0.0).to(out_dtype)
+    assert torch.equal(out, want)
+    assert bool((store.view(n, D + pad)[:, D:] == 555.0).all())
