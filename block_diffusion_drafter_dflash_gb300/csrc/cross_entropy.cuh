@@ -17,7 +17,7 @@ struct CePlan {
   int planes;            // bf16 planes of an operand: 1 (bf16 tensors) or 3 (fp32 tensors)
   int direct;            // gradient: the hidden states' gradient needs no sums in memory
   int ctas, tile, bn;    // CTAs that share a tile, its rows and columns
-  int rows_pad, dim_pad; // multiples of a tile's rows (256 or, for fp32 tensors, 128) and of 64
+  int rows_pad, dim_pad; // multiples of a tile's rows (256 for a pair of CTAs, else 128) and of 64
   int piece;             // vocabulary columns of a piece (a multiple of 256)
   int32_t* status;
   int32_t* kept;         // [2] rows kept; parts of a cut tile (the hidden states' gradient)
@@ -48,7 +48,7 @@ struct CeTensors {
   void* d_weight;
 };
 
-// want_hidden / want_weight: which gradients (neither: the forward)
+// backward: the gradient's; want_hidden: with room for the sums of the hidden states' gradient
 CePlan ce_plan(void* ws, int rows, int dim, int vocab, bool f32, bool backward, bool want_hidden, int sms);
 // Shared-memory opt-in of the kernels (once per device).
 cudaError_t ce_prepare_f32();
